@@ -431,6 +431,149 @@ moe_status moe_cache_get_stats(const moe_expert_cache* cache, moe_cache_stats* s
 /* Slot holding `expert` (host output), or -1 if it is not resident. */
 moe_status moe_cache_slot_of(const moe_expert_cache* cache, int32_t expert, int32_t* slot);
 
+/* MXFP4 and router-balance operators
+ * ----------------------------------
+ * Operators beside the layer, for training and for experts in the OCP
+ * microscaled 4-bit format (page "NVIDIA stellt neues GLM-5.2 NVFP4 Modell
+ * vor" has its 16-element relative, MOE_WFMT_NVFP4).  The conventions above
+ * hold: device pointers, caller-owned buffers, everything enqueued on
+ * `stream`, checks before any HIP call, no floating-point atomics (identical
+ * inputs give bit-identical outputs).  They allocate nothing and, where no
+ * workspace is listed, need none.
+ *
+ * MXFP4 layout of a matrix [rows][cols]: nb = ceil(cols / 32) blocks a row.
+ *   codes  uint8 [rows][16 nb]: byte j of a row holds input 2j in the low
+ *          nibble and input 2j+1 in the high nibble; a nibble is an E2M1 code
+ *          (bit 3 sign; 0, 0.5, 1, 1.5, 2, 3, 4, 6).
+ *   scale  uint8 [rows][nb]: E8M0, value 2^(s - 127); 255 is NaN and makes
+ *          the whole block NaN.
+ * Inputs past cols in a row's last block are held as +0. */
+typedef enum {
+  MOE_DT_F32 = 0,   /* = MOE_OUT_F32 */
+  MOE_DT_BF16 = 1,  /* = MOE_OUT_BF16 */
+  MOE_DT_F16 = 2,
+  MOE_DT_MXFP4 = 3  /* codes and scales, rows packed without gaps */
+} moe_dtype;
+
+/* Rows to MXFP4.  Per block of 32: with e = floor(log2(largest magnitude)),
+ * the scale is 2^clamp(e - 2, -127, 127) (2^-127 for a block of zeros) and
+ * each code the nearest E2M1 value of x / scale, ties to the even code,
+ * magnitudes above 6 to 6.  A block that holds an infinity or a NaN gets scale
+ * 255 and code 0 throughout.
+ *   src    [rows][cols] of dtype MOE_DT_F32, _BF16 or _F16, row stride ld >=
+ *          cols elements, element-aligned, last dimension contiguous
+ *   codes  16-byte aligned; scale any alignment
+ * rows == 0 enqueues nothing; cols >= 1, cols <= 2^24 and rows <= 2^31 - 1
+ * (else MOE_ERR_UNSUPPORTED). */
+moe_status moe_mxfp4_quantize(const void* src, int32_t dtype, int64_t rows, int64_t cols,
+                              int64_t ld, uint8_t* codes, uint8_t* scale, hipStream_t stream);
+
+/* MXFP4 rows to dst [rows][cols] of dtype MOE_DT_F32, _BF16 or _F16 (rounded
+ * to nearest even where the type cannot hold the value), row stride ld.
+ * Exact in F32 and BF16. */
+moe_status moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scale, int64_t rows,
+                                int64_t cols, void* dst, int32_t dtype, int64_t ld,
+                                hipStream_t stream);
+
+/* Geometry of a grouped product.  Limits (else MOE_ERR_INVALID_ARG): rows >=
+ * 0; n, k, n_experts >= 1; k a multiple of 32; the dtypes as each entry point
+ * states.  Kernel limits (else MOE_ERR_UNSUPPORTED): n_experts <= 256, n and k
+ * <= 65536, rows and a_rows <= 16 * MOE_MAX_TOKENS. */
+typedef struct {
+  int32_t rows;       /* R: rows of the output, grouped by expert */
+  int32_t n;          /* output features of each expert's weights [n][k] */
+  int32_t k;          /* input features */
+  int32_t n_experts;  /* E */
+  int32_t a_rows;     /* rows of the input matrix; = rows without a row index */
+  int32_t a_dtype;    /* moe_dtype of the input */
+  int32_t out_dtype;  /* MOE_DT_F32 or MOE_DT_BF16 */
+  int64_t lda;        /* row stride of the input, elements (MOE_DT_MXFP4: k) */
+  int64_t ldo;        /* row stride of the output, elements */
+} moe_matmul_config;
+
+/* Grouped product over MXFP4 weights:
+ *   out[r][j] = sum_i a[idx(r)][i] * W[e(r)][j][i],  j < n,
+ * where row r belongs to the expert e with expert_offsets[e] <= r <
+ * expert_offsets[e + 1] and idx(r) = row_index[r] (r without an index).
+ *   a        MOE_DT_BF16: [a_rows][k], row stride lda >= k, lda a multiple of
+ *            8; MOE_DT_MXFP4: codes [a_rows][k/2] with a_scale [a_rows][k/32].
+ *            16-byte aligned; a_scale is NULL for BF16, 4-byte aligned else
+ *   w_codes  [E][n][k/2], 16-byte aligned; w_scale [E][n][k/32], 4-byte aligned
+ *   expert_offsets  int32 [E+1], ascending, as moe_permute writes them; rows
+ *            from expert_offsets[E] on belong to no expert and are left as they
+ *            are.  NULL iff E == 1: every row belongs to the one expert
+ *   row_index  int32 [R] (moe_permute's sorted_token), or NULL; a row whose
+ *            index lies outside [0, a_rows) reads as zeros
+ *   out      [R][n] of out_dtype, row stride ldo >= n, 16-byte aligned
+ * Products are exact, sums are held in fp32; one rounding at the store.
+ * R == 0 enqueues nothing. */
+moe_status moe_mxfp4_matmul(const moe_matmul_config* cfg, const void* a, const uint8_t* a_scale,
+                            const uint8_t* w_codes, const uint8_t* w_scale,
+                            const int32_t* expert_offsets, const int32_t* row_index, void* out,
+                            hipStream_t stream);
+
+/* Gradient of moe_mxfp4_matmul with respect to its (bfloat16) rows, the 4-bit
+ * weights being constants:
+ *   dx[r][i] = sum_j dy[r][j] * W[e(r)][j][i],  i < k,
+ * one row per output row (the gradient of a gathered row is the sum of its
+ * rows here: moe_combine with weights of 1).
+ *   dy  [R][n] bf16, row stride lda >= n, lda a multiple of 8, 16-byte aligned
+ *   dx  [R][k] of out_dtype, row stride ldo >= k, 16-byte aligned
+ * cfg as for moe_mxfp4_matmul with a_dtype MOE_DT_BF16, a_rows == rows, and n
+ * a multiple of 32 (else MOE_ERR_INVALID_ARG). */
+moe_status moe_mxfp4_matmul_dx(const moe_matmul_config* cfg, const void* dy,
+                               const uint8_t* w_codes, const uint8_t* w_scale,
+                               const int32_t* expert_offsets, void* dx, hipStream_t stream);
+
+/* Balance loss of a router, with its per-expert counts.  For token t with
+ * router logits l_t, the shares are
+ *   p_t = softmax(l_t)              (MOE_SCORE_SOFTMAX)
+ *   p_t = sigmoid(l_t) / sum of it  (MOE_SCORE_SIGMOID)
+ * and with, in sequence s, n_s routed tokens, c_si picks of expert i and C_s =
+ * sum_i c_si picks in all,
+ *   f_si = E c_si / C_s,  P_si = (sum over the routed t of p_ti) / n_s,
+ *   loss = coef / S * sum_s sum_i f_si P_si.
+ * A token is routed if at least one of its picks lies in [0, E); the logits of
+ * the others (padding) are not used, whatever they hold.  Sequences with no
+ * routed token contribute 0.  Counts are constants of the gradient:
+ *   dloss/dl_tj = coef / (S n_s) p_tj (f_sj - sum_i f_si p_ti) * d_tj,
+ *   d_tj = 1 (softmax) or sigmoid(-l_tj); 0 for tokens that are not routed.
+ * Infinite logits act as limits where those exist (an expert at -inf has share
+ * 0 and gradient 0); a routed row with a NaN, with +inf among softmax logits,
+ * or with -inf throughout gives NaN. */
+typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;
+
+typedef struct {
+  int32_t tokens;        /* T */
+  int32_t n_experts;     /* E: 1..256 (larger: MOE_ERR_UNSUPPORTED) */
+  int32_t top_k;         /* k: picks per token, 1..16 (larger: MOE_ERR_UNSUPPORTED) */
+  int32_t n_seq;         /* S: 1..65536 (larger: MOE_ERR_UNSUPPORTED) */
+  int32_t score;         /* moe_score */
+  int32_t logits_dtype;  /* MOE_DT_F32 or MOE_DT_BF16; of logits and dlogits */
+  float coef;            /* finite */
+} moe_balance_config;
+
+/* Bytes of workspace moe_balance_loss needs (host output). */
+moe_status moe_balance_workspace_size(const moe_balance_config* cfg, size_t* bytes);
+
+/*   logits       [T][E] of logits_dtype, contiguous, 16-byte aligned
+ *   topk_ids     int32 [T][k]: moe_route's ids (values outside [0, E): no pick)
+ *   seq_offsets  int32 [S+1], ascending from 0 to T; NULL iff S == 1
+ *   counts       int32 [S][E] out; tokens int32 [S] out: n_s; loss fp32 [1] out
+ * T == 0 writes zeros.  Workspace 256-byte aligned. */
+moe_status moe_balance_loss(const moe_balance_config* cfg, const void* logits,
+                            const int32_t* topk_ids, const int32_t* seq_offsets, int32_t* counts,
+                            int32_t* tokens, float* loss, void* ws, size_t ws_bytes,
+                            hipStream_t stream);
+
+/* dlogits [T][E] of logits_dtype = dloss * the gradient above, from counts and
+ * tokens as moe_balance_loss wrote them; dloss fp32 [1] on the device, or NULL
+ * for 1.  Every row is written. */
+moe_status moe_balance_loss_grad(const moe_balance_config* cfg, const void* logits,
+                                 const int32_t* topk_ids, const int32_t* seq_offsets,
+                                 const int32_t* counts, const int32_t* tokens, const float* dloss,
+                                 void* dlogits, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,4 +11,8 @@ from .binding import (  # noqa: F401
     MOE_FLAG_GRID_WAIT_TIMEOUT, moe_layer_noalloc, MOE_NOALLOC_WS_BYTES,
     MoeCacheStats, moe_cache_create, moe_cache_destroy, moe_layer_cached, moe_cache_prefetch,
     moe_cache_pin, moe_cache_unpin_all, moe_cache_get_stats, moe_cache_slot_of,
+    MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16, MOE_DT_MXFP4, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX,
+    MoeMatmulConfig, MoeBalanceConfig, mxfp4_empty, moe_mxfp4_quantize, moe_mxfp4_dequantize,
+    moe_mxfp4_matmul, moe_mxfp4_matmul_dx, make_balance_config, moe_balance_workspace_size,
+    balance_workspace, moe_balance_loss, moe_balance_loss_grad,
 )

@@ -24,6 +24,8 @@ MOE_WFMT_INT4_ROW_F32, MOE_WFMT_INT8_ROW_F32, MOE_WFMT_INT2_ROW_F32 = 2, 3, 4
 MOE_OUT_F32, MOE_OUT_BF16 = 0, 1
 MOE_OPT_NO_GRID_WAIT, MOE_OPT_GRID_WAIT_NONE, MOE_OPT_INT8_ACTIVATIONS = 1, 2, 4
 MOE_FLAG_GRID_WAIT_TIMEOUT = 1
+MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16, MOE_DT_MXFP4 = 0, 1, 2, 3
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
 MOE_MAX_TOKENS = 262144
 MOE_NOALLOC_WS_BYTES = 32 << 20
 WFMT = {"int4": MOE_WFMT_INT4_G32_F16, "nvfp4": MOE_WFMT_NVFP4, "int4_row": MOE_WFMT_INT4_ROW_F32,
@@ -67,6 +69,19 @@ class MoeCacheStats(ctypes.Structure):
                 ("bytes_loaded", ctypes.c_uint64)]
 
 
+class MoeMatmulConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("n_experts", ctypes.c_int32), ("a_rows", ctypes.c_int32),
+                ("a_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("lda", ctypes.c_int64), ("ldo", ctypes.c_int64)]
+
+
+class MoeBalanceConfig(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("n_experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("n_seq", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("logits_dtype", ctypes.c_int32), ("coef", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -81,6 +96,8 @@ def lib() -> ctypes.CDLL:
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         cfgp = ctypes.POINTER(MoeConfig)
         exp = ctypes.POINTER(MoeQExperts)
+        i64 = ctypes.c_int64
+        mmp, balp = ctypes.POINTER(MoeMatmulConfig), ctypes.POINTER(MoeBalanceConfig)
         sig = {
             "moe_workspace_size": [cfgp, i32, ctypes.POINTER(sz)],
             "moe_route": [cfgp, i32, vp, vp, vp, vp, vp, vp, sz, vp],
@@ -100,6 +117,13 @@ def lib() -> ctypes.CDLL:
             "moe_cache_unpin_all": [vp],
             "moe_cache_get_stats": [vp, ctypes.POINTER(MoeCacheStats)],
             "moe_cache_slot_of": [vp, i32, ctypes.POINTER(i32)],
+            "moe_mxfp4_quantize": [vp, i32, i64, i64, i64, vp, vp, vp],
+            "moe_mxfp4_dequantize": [vp, vp, i64, i64, vp, i32, i64, vp],
+            "moe_mxfp4_matmul": [mmp, vp, vp, vp, vp, vp, vp, vp, vp],
+            "moe_mxfp4_matmul_dx": [mmp, vp, vp, vp, vp, vp, vp],
+            "moe_balance_workspace_size": [balp, ctypes.POINTER(sz)],
+            "moe_balance_loss": [balp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+            "moe_balance_loss_grad": [balp, vp, vp, vp, vp, vp, vp, vp, vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -280,3 +304,167 @@ def moe_cache_slot_of(cache, expert: int) -> int:
     s = ctypes.c_int32(0)
     _check(lib().moe_cache_slot_of(cache, expert, ctypes.byref(s)), "moe_cache_slot_of")
     return s.value
+
+
+# ---- MXFP4 and router-balance operators --------------------------------------
+# Sizes, types and strides come from the tensors; one whose shape, type or
+# layout does not fit the others raises QmoeError (MOE_ERR_INVALID_ARG).
+_DT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
+_SCORE = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}
+
+
+def _require(ok: bool, where: str):
+    if not ok:
+        raise QmoeError(MOE_ERR_INVALID_ARG, where)
+
+
+def _fits(where: str, t: torch.Tensor, dtype, shape):
+    """`t` is a contiguous device tensor of this type and shape."""
+    _require(t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
+             where)
+
+
+def _matrix(where: str, t: torch.Tensor, dtypes):
+    """`t` is a device matrix whose rows are contiguous; returns its row stride."""
+    _require(t.is_cuda and t.dim() == 2 and t.dtype in dtypes, where)
+    rows, cols = t.shape
+    _require(cols <= 1 or t.stride(1) == 1, where)
+    _require(rows <= 1 or t.stride(0) >= cols, where)
+    return t.stride(0) if rows > 1 else max(cols, 1)
+
+
+def mxfp4_empty(rows: int, cols: int, device="cuda"):
+    """Uninitialised MXFP4 storage of a [rows][cols] matrix: (codes, scales)."""
+    nb = (cols + 31) // 32
+    return (torch.empty(rows, 16 * nb, dtype=torch.uint8, device=device),
+            torch.empty(rows, nb, dtype=torch.uint8, device=device))
+
+
+def _mxfp4_rows(where, x, codes, scales):
+    ld = _matrix(where, x, _DT)
+    rows, cols = x.shape
+    nb = (cols + 31) // 32
+    _fits(where, codes, torch.uint8, (rows, 16 * nb))
+    _fits(where, scales, torch.uint8, (rows, nb))
+    return rows, cols, ld
+
+
+def moe_mxfp4_quantize(src, codes, scales, stream=None):
+    """Rows of `src` (fp32, bf16 or fp16) to MXFP4 codes and scales."""
+    rows, cols, ld = _mxfp4_rows("moe_mxfp4_quantize", src, codes, scales)
+    _check(lib().moe_mxfp4_quantize(_p(src), _DT[src.dtype], rows, cols, ld, _p(codes), _p(scales),
+                                    _stream(stream)), "moe_mxfp4_quantize")
+
+
+def moe_mxfp4_dequantize(codes, scales, dst, stream=None):
+    """The values of MXFP4 rows, into `dst` (fp32, bf16 or fp16)."""
+    rows, cols, ld = _mxfp4_rows("moe_mxfp4_dequantize", dst, codes, scales)
+    _check(lib().moe_mxfp4_dequantize(_p(codes), _p(scales), rows, cols, _p(dst), _DT[dst.dtype], ld,
+                                      _stream(stream)), "moe_mxfp4_dequantize")
+
+
+def _grouped_weights(where, w_codes, w_scales, expert_offsets):
+    _require(w_codes.dim() == 3, where)
+    E, N, kb = w_codes.shape
+    _fits(where, w_codes, torch.uint8, (E, N, kb))
+    _fits(where, w_scales, torch.uint8, (E, N, kb // 16))
+    if expert_offsets is not None:
+        _fits(where, expert_offsets, torch.int32, (E + 1,))
+    return E, N, kb * 2
+
+
+def moe_mxfp4_matmul(a, w_codes, w_scales, out, a_scale=None, expert_offsets=None, row_index=None,
+                     stream=None):
+    """out[r] = a[row_index[r]] @ W[expert of r].T over MXFP4 weights [E][n][k/2];
+    `a` is bf16 [rows][k], or MXFP4 codes uint8 [rows][k/2] with `a_scale`."""
+    where = "moe_mxfp4_matmul"
+    E, N, K = _grouped_weights(where, w_codes, w_scales, expert_offsets)
+    ldo = _matrix(where, out, (torch.float32, torch.bfloat16))
+    R = out.shape[0]
+    _require(out.shape[1] == N, where)
+    if a_scale is None:
+        lda = _matrix(where, a, (torch.bfloat16,))
+        _require(a.shape[1] == K, where)
+        dt = MOE_DT_BF16
+    else:
+        _require(a.dim() == 2, where)
+        _fits(where, a, torch.uint8, (a.shape[0], K // 2))
+        _fits(where, a_scale, torch.uint8, (a.shape[0], K // 32))
+        lda, dt = K, MOE_DT_MXFP4
+    if row_index is not None:
+        _fits(where, row_index, torch.int32, (R,))
+    cfg = MoeMatmulConfig(R, N, K, E, a.shape[0], dt, _DT[out.dtype], lda, ldo)
+    _check(lib().moe_mxfp4_matmul(ctypes.byref(cfg), _p(a), _p(a_scale), _p(w_codes), _p(w_scales),
+                                  _p(expert_offsets), _p(row_index), _p(out), _stream(stream)), where)
+
+
+def moe_mxfp4_matmul_dx(dy, w_codes, w_scales, dx, expert_offsets=None, stream=None):
+    """dx[r] = dy[r] @ W[expert of r]: the gradient of moe_mxfp4_matmul's rows."""
+    where = "moe_mxfp4_matmul_dx"
+    E, N, K = _grouped_weights(where, w_codes, w_scales, expert_offsets)
+    lda = _matrix(where, dy, (torch.bfloat16,))
+    ldo = _matrix(where, dx, (torch.float32, torch.bfloat16))
+    R = dx.shape[0]
+    _require(tuple(dy.shape) == (R, N) and dx.shape[1] == K, where)
+    cfg = MoeMatmulConfig(R, N, K, E, R, MOE_DT_BF16, _DT[dx.dtype], lda, ldo)
+    _check(lib().moe_mxfp4_matmul_dx(ctypes.byref(cfg), _p(dy), _p(w_codes), _p(w_scales),
+                                     _p(expert_offsets), _p(dx), _stream(stream)), where)
+
+
+def make_balance_config(tokens: int, n_experts: int, top_k: int = 1, n_seq: int = 1,
+                        score: str = "sigmoid", dtype=torch.float32,
+                        coef: float = 1.0) -> MoeBalanceConfig:
+    return MoeBalanceConfig(tokens, n_experts, top_k, n_seq, _SCORE.get(score, score), _DT[dtype], coef)
+
+
+def moe_balance_workspace_size(cfg: MoeBalanceConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_balance_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_balance_workspace_size")
+    return n.value
+
+
+def balance_workspace(tokens: int, n_experts: int, n_seq: int = 1, device="cuda") -> torch.Tensor:
+    """A torch-allocated workspace for moe_balance_loss of this size."""
+    n = moe_balance_workspace_size(make_balance_config(tokens, n_experts, n_seq=n_seq))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets):
+    _require(logits.dim() == 2 and topk_ids.dim() == 2 and counts.dim() == 2 and score in _SCORE, where)
+    T, E = logits.shape
+    S = counts.shape[0]
+    _require(logits.dtype in (torch.float32, torch.bfloat16), where)
+    _fits(where, logits, logits.dtype, (T, E))
+    _fits(where, topk_ids, torch.int32, (T, topk_ids.shape[1]))
+    _fits(where, counts, torch.int32, (S, E))
+    _fits(where, tokens, torch.int32, (S,))
+    if seq_offsets is not None:
+        _fits(where, seq_offsets, torch.int32, (S + 1,))
+    return make_balance_config(T, E, topk_ids.shape[1], S, score, logits.dtype, coef)
+
+
+def moe_balance_loss(logits, topk_ids, counts, tokens, loss, coef, score="sigmoid", seq_offsets=None,
+                     ws=None, stream=None):
+    """The router's balance loss (loss [1]), its picks per sequence and expert
+    (counts [S][E]) and routed tokens per sequence (tokens [S])."""
+    where = "moe_balance_loss"
+    cfg = _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets)
+    _fits(where, loss, torch.float32, (1,))
+    _check(lib().moe_balance_loss(ctypes.byref(cfg), _p(logits), _p(topk_ids), _p(seq_offsets),
+                                  _p(counts), _p(tokens), _p(loss), _p(ws),
+                                  0 if ws is None else ws.numel(), _stream(stream)), where)
+
+
+def moe_balance_loss_grad(logits, topk_ids, counts, tokens, dlogits, coef, score="sigmoid",
+                          seq_offsets=None, dloss=None, stream=None):
+    """dlogits [T][E]: dloss (1 if None) times the loss's gradient, from the
+    counts and tokens that moe_balance_loss wrote."""
+    where = "moe_balance_loss_grad"
+    cfg = _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets)
+    _fits(where, dlogits, logits.dtype, logits.shape)
+    if dloss is not None:
+        _fits(where, dloss, torch.float32, (1,))
+    _check(lib().moe_balance_loss_grad(ctypes.byref(cfg), _p(logits), _p(topk_ids), _p(seq_offsets),
+                                       _p(counts), _p(tokens), _p(dloss), _p(dlogits),
+                                       _stream(stream)), where)
