@@ -12,6 +12,8 @@
 // byte.  Rows in bf16: the codes become bf16 with their scale (exact: E2M1
 // times a power of two) in four 16x16x32 steps.  Rows in MXFP4: the codes go
 // into one 16x16x128 scaled step as they are.
+#include <algorithm>
+
 #include "operators_internal.h"
 #include "qmoe_device.h"
 
@@ -81,6 +83,19 @@ __device__ __forceinline__ int64_t source_row(const MatmulArgs& g, int r) {
   return t >= 0 && t < g.a_rows ? t : -1;
 }
 
+// Eight codes as bf16 with their block's scale (an fp32 whose exponent it is).
+__device__ __forceinline__ bf16x8 bf16_of(uint32_t w, float s) {
+  union {
+    bf16x2 p[4];
+    bf16x8 v;
+  } A;
+  A.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
+  A.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
+  A.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
+  A.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
+  return A.v;
+}
+
 // One wave: 16 outputs x 16 rows.
 template <bool MX>
 __global__ void __launch_bounds__(256) mx_matmul_kernel(MatmulArgs g, int nt) {
@@ -121,15 +136,7 @@ __global__ void __launch_bounds__(256) mx_matmul_kernel(MatmulArgs g, int nt) {
         uint4 x = make_uint4(0, 0, 0, 0);
         if (arow >= 0 && b < nb)
           x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.a) + arow * g.lda + b * kMxBlock + 8 * i);
-        union {
-          bf16x2 p[4];
-          bf16x8 v;
-        } A;
-        A.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(ww[i], s, 0);
-        A.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(ww[i], s, 1);
-        A.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(ww[i], s, 2);
-        A.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(ww[i], s, 3);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A.v, __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_of(ww[i], s), __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
       }
     }
   }
@@ -161,9 +168,321 @@ __global__ void __launch_bounds__(256) mx_matmul_dx_kernel(MatmulArgs g, int nt)
   store_out(g, u.r0, k + 1, a1);
 }
 
+// ---------------------------------------------------------------------------
+// Large products.  One workgroup of eight waves per CU; a work item is up to
+// 256 rows of one expert times 256 outputs (waves 4 x 2), or up to 128 rows
+// times 512 outputs (8 x 1): either way a wave holds 64 outputs x 128 rows in
+// its accumulators, and a K block costs the CU 64 KB of LDS reads for 2048
+// (bf16) MFMAs.  The weights go from global memory straight into registers
+// (no other wave of the 8 x 1 form needs them), the rows of `a` through LDS by
+// direct loads, two stages deep: block kb + 1 is requested when block kb has
+// landed, a K block's MFMAs (two waves per SIMD) taking longer than the loads.
+// ---------------------------------------------------------------------------
+constexpr int kFatRows = 256, kFatThreads = 512;
+constexpr int kStageBytes = 64 * 1024;
+
+// Work item of workgroup b: workgroups go round-robin over the 8 XCDs, and
+// each XCD's share is a contiguous range, so that the output tiles of one run
+// of rows meet in one L2.
+__device__ __forceinline__ int xcd_item(int b, int total) {
+  const int x = b & 7, q = total >> 3, r = total & 7;
+  return x * q + min(x, r) + (b >> 3);
+}
+
+
+struct FatItem {
+  int e, r0, M, tile;
+  bool wide;   // 4 x 2 waves: 256 outputs; else 8 x 1: 512
+};
+
+// Items in order of expert, rows, output tile; a run of up to 256 rows takes
+// the narrow form if it has at most 128.  All 512 threads call it.
+__device__ __forceinline__ bool find_item(const int32_t* offsets, int E, int R, int ntw, int ntn, FatItem& it) {
+  __shared__ int ws[4], hit[4], tot;
+  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+  int lo = 0, cnt = 0;
+  if (!offsets) {
+    cnt = t == 0 ? R : 0;
+  } else if (t < E) {
+    lo = min(max(offsets[t], 0), R);
+    cnt = min(max(offsets[t + 1], lo), R) - lo;
+  }
+  const int rem = cnt & (kFatRows - 1);
+  const int u = (cnt / kFatRows) * ntw + (rem > kFatRows / 2 ? ntw : rem > 0 ? ntn : 0);
+  int inc = u;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(inc, d, 64);
+    if (lane >= d) inc += v;
+  }
+  if (lane == 63 && wv < 4) ws[wv] = inc;
+  __syncthreads();
+  if (wv < 4)
+    for (int i = 0; i < wv; ++i) inc += ws[i];
+  if (t == 255) tot = inc;
+  __syncthreads();
+  const int total = tot;
+  if ((int)blockIdx.x >= total) return false;
+  const int w = xcd_item(blockIdx.x, total);
+  if (wv < 4 && w >= inc - u && w < inc) {
+    const int k = w - (inc - u), run = min(k / ntw, cnt / kFatRows);
+    const int m = min(kFatRows, cnt - run * kFatRows);
+    hit[0] = t;
+    hit[1] = lo + run * kFatRows;
+    hit[2] = m;
+    hit[3] = k - run * ntw;
+  }
+  __syncthreads();
+  it.e = __builtin_amdgcn_readfirstlane(hit[0]);
+  it.r0 = __builtin_amdgcn_readfirstlane(hit[1]);
+  it.M = __builtin_amdgcn_readfirstlane(hit[2]);
+  it.tile = __builtin_amdgcn_readfirstlane(hit[3]);
+  it.wide = it.M > kFatRows / 2;
+  return true;
+}
+
+constexpr uint32_t kOutside = 0xff000000u;   // offset past every descriptor here, with room for a row's length
+
+// 16 bytes per lane from buffer offset `off` into LDS at dst + 16 lane.
+__device__ __forceinline__ void to_lds16(const rsrc_t& r, uint8_t* dst, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
+}
+
+// Stores four consecutive outputs of one row (col % 4 == 0).
+__device__ __forceinline__ void store4(const MatmulArgs& g, bool vec, int row, int col, const f32x4& v) {
+  const int64_t i = (int64_t)row * g.ldo + col;
+  if (vec && col + 4 <= g.N) {
+    if (g.out_bf16) {
+      typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+      bf16x4 o = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+      *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(g.out) + i) = o;
+    } else {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + i) = v;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (col + j < g.N) store_out(g, row, col + j, v[j]);
+}
+
+// LDS of one stage: rows of 256 bytes (bf16: 128 inputs) or 128 bytes (MXFP4:
+// 256 inputs), 16-byte chunk c of row r at chunk c ^ (r mod 16) of its row, or
+// c ^ (r / 2 mod 8): the 16 rows that one operand read touches then lie on
+// distinct banks.
+template <bool MX>
+struct FatShape {
+  static constexpr int kK = MX ? 256 : 128;             // inputs per K block
+  static constexpr int kRowBytes = MX ? 128 : 256;
+  static constexpr int kChunks = kRowBytes / 16;
+  static constexpr int kWC = MX ? 2 : 1;                // 16-byte weight chunks per lane and row tile
+  static __device__ __forceinline__ int place(int row, int c) {
+    return MX ? c ^ ((row >> 1) & 7) : c ^ (row & 15);
+  }
+};
+
+template <bool MX, int WT, int CT>
+__device__ __forceinline__ void fat_tile(const MatmulArgs& g, const FatItem& it, uint8_t* st0, uint8_t* st1,
+                                         uint32_t* sc0, uint32_t* sc1) {
+  using F = FatShape<MX>;
+  constexpr int WN = 8 / WT, RT = 4, ROWS = 16 * CT * WT;
+  constexpr int SLOTS = ROWS * F::kChunks, NA = (SLOTS + kFatThreads - 1) / kFatThreads;
+  static_assert(ROWS * F::kRowBytes <= kStageBytes, "a stage fits");
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wv % WN, wt = wv / WN;
+  const int n0 = it.tile * (64 * WN) + wn * 64;
+  const int nb = g.K / kMxBlock, nkb = (g.K + F::kK - 1) / F::kK;
+
+  // rows of `a`: this thread's chunk of each load
+  const int64_t ldb = MX ? g.K / 2 : g.lda * 2;
+  const uint8_t* abase = static_cast<const uint8_t*>(g.a) + (g.index ? 0 : (int64_t)it.r0 * ldb);
+  const rsrc_t ar = make_rsrc(abase, kOutside);
+  uint32_t aoff[NA];
+#pragma unroll
+  for (int i = 0; i < NA; ++i) {
+    const int slot = i * kFatThreads + tid, row = slot / F::kChunks;
+    aoff[i] = kOutside;
+    if (row < it.M) {
+      const int64_t src = g.index ? source_row(g, it.r0 + row) : row;
+      if (src >= 0) aoff[i] = (uint32_t)(src * ldb) + 16u * F::place(row, slot % F::kChunks);
+    }
+  }
+  // MXFP4 rows: thread t < 2 ROWS carries four scale bytes of row t / 2
+  const rsrc_t asr = make_rsrc(MX ? g.a_scale + (g.index ? 0 : (int64_t)it.r0 * nb) : nullptr, kOutside);
+  uint32_t asoff = kOutside;
+  if (MX && tid < 2 * ROWS && tid / 2 < it.M) {
+    const int64_t src = g.index ? source_row(g, it.r0 + tid / 2) : tid / 2;
+    if (src >= 0) asoff = (uint32_t)(src * nb) + 4u * (tid & 1);
+  }
+  // weights: rows past N lie past the descriptors
+  const int64_t erow = (int64_t)it.e * g.N;
+  const rsrc_t wr = make_rsrc(g.w_codes + erow * (g.K / 2), (uint32_t)g.N * (uint32_t)(g.K / 2));
+  const rsrc_t sr = make_rsrc(g.w_scale + erow * nb, (uint32_t)g.N * (uint32_t)nb);
+  uint32_t woff[RT], soff[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const uint32_t row = (uint32_t)(n0 + 16 * rt + lr);
+    woff[rt] = row * (uint32_t)(g.K / 2) + 16u * F::kWC * lq;
+    soff[rt] = row * (uint32_t)nb + (uint32_t)(F::kWC * lq);
+  }
+
+  uint32_t wq[2][RT][F::kWC][4], wsc[2][RT], asc = 0;
+  auto issue = [&](auto P, int kb) {
+    constexpr int p = decltype(P)::value;
+    uint8_t* st = p ? st1 : st0;
+    const bool tail = (kb + 1) * F::kK > g.K;
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      if (i * kFatThreads + wv * 64 < SLOTS) {
+        uint32_t off = aoff[i] + (uint32_t)kb * F::kRowBytes;
+        if (tail) {
+          const int slot = i * kFatThreads + tid, c = F::place(slot / F::kChunks, slot % F::kChunks);
+          if (kb * F::kK + c * (F::kK / F::kChunks) >= g.K) off = kOutside;
+        }
+        to_lds16(ar, st + (i * kFatThreads + wv * 64) * 16, off);
+      }
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+      for (int c = 0; c < F::kWC; ++c) bload16(wq[p][rt][c], wr, woff[rt] + (uint32_t)kb * (F::kK / 2) + 16u * c, 0);
+      const uint32_t so = soff[rt] + (uint32_t)kb * (F::kK / 32);
+      if constexpr (MX) {
+        wsc[p][rt] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(sr, so, 0, 0) |
+                     (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(sr, so + 1, 0, 0) << 8;
+      } else {
+        wsc[p][rt] = __builtin_amdgcn_raw_buffer_load_b8(sr, so, 0, 0);
+      }
+    }
+    if constexpr (MX) {
+      asc = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (!tail || kb * 8 + 4 * (tid & 1) + j < nb)
+          asc |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(asr, asoff + (uint32_t)(kb * 8 + j), 0, 0) << (8 * j);
+    }
+    if (tail) {   // blocks past K: the next row's scales, which may be NaN, times zeros
+      const int b = kb * (F::kK / 32) + F::kWC * lq;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        if (b >= nb) wsc[p][rt] = 0;
+        else if (MX && b + 1 >= nb) wsc[p][rt] &= 0xffu;
+      }
+    }
+  };
+
+  f32x4 acc[RT][CT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int c = 0; c < CT; ++c) acc[rt][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](auto P) {
+    constexpr int p = decltype(P)::value;
+    const uint8_t* st = p ? st1 : st0;
+    if constexpr (MX) {
+      uint32_t ts[CT];
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+        ts[c] = reinterpret_cast<const uint16_t*>(p ? sc1 : sc0)[((wt * CT + c) * 16 + lr) * 4 + lq];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        i32x8 B[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          const int row = (wt * CT + c) * 16 + lr;
+          const uint4 v = *reinterpret_cast<const uint4*>(st + row * 128 + 16 * F::place(lr, 2 * lq + s));
+          B[c] = i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const i32x8 A = {(int)wq[p][rt][s][0], (int)wq[p][rt][s][1], (int)wq[p][rt][s][2], (int)wq[p][rt][s][3], 0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+            acc[rt][c] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B[c], acc[rt][c], 4, 4, 0, (int)wsc[p][rt], 0, (int)ts[c])
+                                : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B[c], acc[rt][c], 4, 4, 1, (int)wsc[p][rt], 1, (int)ts[c]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        bf16x8 A[RT], B[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          const int row = (wt * CT + c) * 16 + lr;
+          B[c] = *reinterpret_cast<const bf16x8*>(st + row * 256 + 16 * F::place(lr, 4 * lq + s));
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) A[rt] = bf16_of(wq[p][rt][0][s], __uint_as_float(wsc[p][rt] << 23));
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            acc[rt][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[rt], B[c], acc[rt][c], 0, 0, 0);
+      }
+    }
+  };
+  auto block = [&](auto P, int kb) {
+    constexpr int p = decltype(P)::value;
+    if constexpr (MX) {
+      if (tid < 2 * ROWS) (p ? sc1 : sc0)[tid] = asc;
+    }
+    // block kb has landed, in every wave; nobody reads the other stage any more
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (kb + 1 < nkb) issue(std::integral_constant<int, 1 - p>{}, kb + 1);
+    compute(P);
+  };
+  issue(std::integral_constant<int, 0>{}, 0);
+  for (int kb = 0; kb < nkb; kb += 2) {
+    block(std::integral_constant<int, 0>{}, kb);
+    if (kb + 1 < nkb) block(std::integral_constant<int, 1>{}, kb + 1);
+  }
+
+  const bool vec = g.ldo % 4 == 0;
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    const int row = (wt * CT + c) * 16 + lr;
+    if (row >= it.M) continue;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) store4(g, vec, it.r0 + row, n0 + 16 * rt + 4 * lq, acc[rt][c]);
+  }
+}
+
+template <bool MX>
+__global__ void __launch_bounds__(kFatThreads, 2) mx_matmul_fat_kernel(MatmulArgs g, int ntw, int ntn) {
+  __shared__ __attribute__((aligned(16))) uint8_t st0[kStageBytes / (MX ? 2 : 1)];
+  __shared__ __attribute__((aligned(16))) uint8_t st1[kStageBytes / (MX ? 2 : 1)];
+  __shared__ uint32_t sc0[MX ? 512 : 1], sc1[MX ? 512 : 1];
+  FatItem it;
+  if (!find_item(g.offsets, g.E, g.R, ntw, ntn, it)) return;
+  if (it.wide) {
+    if (it.M > 192) fat_tile<MX, 2, 8>(g, it, st0, st1, sc0, sc1);
+    else fat_tile<MX, 2, 6>(g, it, st0, st1, sc0, sc1);
+  } else {
+    if (it.M > 96) fat_tile<MX, 1, 8>(g, it, st0, st1, sc0, sc1);
+    else if (it.M > 64) fat_tile<MX, 1, 6>(g, it, st0, st1, sc0, sc1);
+    else if (it.M > 32) fat_tile<MX, 1, 4>(g, it, st0, st1, sc0, sc1);
+    else if (it.M > 16) fat_tile<MX, 1, 2>(g, it, st0, st1, sc0, sc1);
+    else fat_tile<MX, 1, 1>(g, it, st0, st1, sc0, sc1);
+  }
+}
+
 }  // namespace
 
 hipError_t launch_mx_matmul(const MatmulArgs& g, bool a_mxfp4, hipStream_t s) {
+  // few rows per expert, or too few outputs to give a quarter of the CUs an
+  // item: the small kernel; sources past 32-bit offsets too
+  const int64_t ldb = a_mxfp4 ? g.K / 2 : g.lda * 2;
+  const int64_t span = (g.index ? (int64_t)g.a_rows : kFatRows) * ldb;
+  if (g.R >= 8 * (int64_t)g.E && (int64_t)g.R * g.N >= 64 * 256 * 256 && span < (int64_t)kOutside) {
+    const int ntw = (g.N + 255) / 256, ntn = (g.N + 511) / 512;
+    const dim3 grid((unsigned)(((long)g.R / kFatRows + std::min(g.E, g.R)) * ntw));
+    if (a_mxfp4) hipLaunchKernelGGL(mx_matmul_fat_kernel<true>, grid, dim3(kFatThreads), 0, s, g, ntw, ntn);
+    else hipLaunchKernelGGL(mx_matmul_fat_kernel<false>, grid, dim3(kFatThreads), 0, s, g, ntw, ntn);
+    return hipGetLastError();
+  }
   const int nt = (g.N + 63) / 64;
   const dim3 grid((unsigned)(max_units(g, 16) * nt));
   if (a_mxfp4) hipLaunchKernelGGL(mx_matmul_kernel<true>, grid, dim3(256), 0, s, g, nt);
