@@ -195,8 +195,9 @@ struct FatItem {
   bool wide;   // 4 x 2 waves: 256 outputs; else 8 x 1: 512
 };
 
-// Items in order of expert, rows, output tile; a run of up to 256 rows takes
-// the narrow form if it has at most 128.  All 512 threads call it.
+// Items in order of expert, output tile, run of up to 256 rows, so that what an
+// XCD works on at a time shares weights as well as rows; a last run of at most
+// 128 rows takes the narrow form, after the others.  All 512 threads call it.
 __device__ __forceinline__ bool find_item(const int32_t* offsets, int E, int R, int ntw, int ntn, FatItem& it) {
   __shared__ int ws[4], hit[4], tot;
   const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
@@ -208,7 +209,8 @@ __device__ __forceinline__ bool find_item(const int32_t* offsets, int E, int R, 
     cnt = min(max(offsets[t + 1], lo), R) - lo;
   }
   const int rem = cnt & (kFatRows - 1);
-  const int u = (cnt / kFatRows) * ntw + (rem > kFatRows / 2 ? ntw : rem > 0 ? ntn : 0);
+  const int wide = cnt / kFatRows + (rem > kFatRows / 2);   // runs of the wide form
+  const int u = wide * ntw + (rem > 0 && rem <= kFatRows / 2 ? ntn : 0);
   int inc = u;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -225,12 +227,12 @@ __device__ __forceinline__ bool find_item(const int32_t* offsets, int E, int R, 
   if ((int)blockIdx.x >= total) return false;
   const int w = xcd_item(blockIdx.x, total);
   if (wv < 4 && w >= inc - u && w < inc) {
-    const int k = w - (inc - u), run = min(k / ntw, cnt / kFatRows);
-    const int m = min(kFatRows, cnt - run * kFatRows);
+    const int k = w - (inc - u);
+    const int run = k < wide * ntw ? k % wide : wide;
     hit[0] = t;
     hit[1] = lo + run * kFatRows;
-    hit[2] = m;
-    hit[3] = k - run * ntw;
+    hit[2] = min(kFatRows, cnt - run * kFatRows);
+    hit[3] = k < wide * ntw ? k / wide : k - wide * ntw;
   }
   __syncthreads();
   it.e = __builtin_amdgcn_readfirstlane(hit[0]);
@@ -281,12 +283,21 @@ struct FatShape {
   }
 };
 
-template <bool MX, int WT, int CT>
-__device__ __forceinline__ void fat_tile(const MatmulArgs& g, const FatItem& it, uint8_t* st0, uint8_t* st1,
-                                         uint32_t* sc0, uint32_t* sc1) {
+struct FatLds {
+  uint8_t *st0, *st1;     // stages of K blocks
+  uint32_t *sc0, *sc1;    // scales of MXFP4 rows, one stage each
+  uint8_t* ws;            // weight scales: two groups of 16 blocks, 16 bytes per output
+};
+
+// SL: the scales of 16 blocks of an output are 16 aligned bytes (K % 128 ==
+// 0), which come into LDS one group ahead: a scale byte per lane costs the
+// address units as much as 16 bytes of codes.  Otherwise lanes load bytes.
+template <bool MX, bool SL, int WT, int CT>
+__device__ __forceinline__ void fat_tile(const MatmulArgs& g, const FatItem& it, const FatLds& lds) {
   using F = FatShape<MX>;
   constexpr int WN = 8 / WT, RT = 4, ROWS = 16 * CT * WT;
   constexpr int SLOTS = ROWS * F::kChunks, NA = (SLOTS + kFatThreads - 1) / kFatThreads;
+  constexpr int GB = 16 / (F::kK / kMxBlock);   // K blocks per group of scales
   static_assert(ROWS * F::kRowBytes <= kStageBytes, "a stage fits");
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -319,55 +330,63 @@ __device__ __forceinline__ void fat_tile(const MatmulArgs& g, const FatItem& it,
   const int64_t erow = (int64_t)it.e * g.N;
   const rsrc_t wr = make_rsrc(g.w_codes + erow * (g.K / 2), (uint32_t)g.N * (uint32_t)(g.K / 2));
   const rsrc_t sr = make_rsrc(g.w_scale + erow * nb, (uint32_t)g.N * (uint32_t)nb);
-  uint32_t woff[RT], soff[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const uint32_t row = (uint32_t)(n0 + 16 * rt + lr);
-    woff[rt] = row * (uint32_t)(g.K / 2) + 16u * F::kWC * lq;
-    soff[rt] = row * (uint32_t)nb + (uint32_t)(F::kWC * lq);
-  }
+  const uint32_t woff = (uint32_t)(n0 + lr) * (uint32_t)(g.K / 2) + 16u * F::kWC * lq;
+  const uint32_t soff = (uint32_t)(n0 + (SL ? lane : lr)) * (uint32_t)nb + (SL ? 0u : (uint32_t)(F::kWC * lq));
 
   uint32_t wq[2][RT][F::kWC][4], wsc[2][RT], asc = 0;
-  auto issue = [&](auto P, int kb) {
+  auto issue_a = [&](auto P, int kb, int i) {
     constexpr int p = decltype(P)::value;
-    uint8_t* st = p ? st1 : st0;
-    const bool tail = (kb + 1) * F::kK > g.K;
-#pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      if (i * kFatThreads + wv * 64 < SLOTS) {
-        uint32_t off = aoff[i] + (uint32_t)kb * F::kRowBytes;
-        if (tail) {
-          const int slot = i * kFatThreads + tid, c = F::place(slot / F::kChunks, slot % F::kChunks);
-          if (kb * F::kK + c * (F::kK / F::kChunks) >= g.K) off = kOutside;
-        }
-        to_lds16(ar, st + (i * kFatThreads + wv * 64) * 16, off);
-      }
+    if (i * kFatThreads + wv * 64 >= SLOTS) return;
+    uint32_t off = aoff[i] + (uint32_t)kb * F::kRowBytes;
+    if constexpr (MX || !SL) {   // chunks past K
+      const int slot = i * kFatThreads + tid, c = F::place(slot / F::kChunks, slot % F::kChunks);
+      off = kb * F::kK + c * (F::kK / F::kChunks) >= g.K ? kOutside : off;
     }
+    to_lds16(ar, (p ? lds.st1 : lds.st0) + (i * kFatThreads + wv * 64) * 16, off);
+  };
+  auto issue_w = [&](auto P, int kb, int rt) {
+    constexpr int p = decltype(P)::value;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-      for (int c = 0; c < F::kWC; ++c) bload16(wq[p][rt][c], wr, woff[rt] + (uint32_t)kb * (F::kK / 2) + 16u * c, 0);
-      const uint32_t so = soff[rt] + (uint32_t)kb * (F::kK / 32);
-      if constexpr (MX) {
-        wsc[p][rt] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(sr, so, 0, 0) |
-                     (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(sr, so + 1, 0, 0) << 8;
-      } else {
-        wsc[p][rt] = __builtin_amdgcn_raw_buffer_load_b8(sr, so, 0, 0);
-      }
-    }
-    if constexpr (MX) {
-      asc = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (!tail || kb * 8 + 4 * (tid & 1) + j < nb)
-          asc |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(asr, asoff + (uint32_t)(kb * 8 + j), 0, 0) << (8 * j);
-    }
-    if (tail) {   // blocks past K: the next row's scales, which may be NaN, times zeros
+    for (int c = 0; c < F::kWC; ++c)
+      bload16(wq[p][rt][c], wr, woff + (uint32_t)rt * 16u * (uint32_t)(g.K / 2) + (uint32_t)kb * (F::kK / 2) + 16u * c, 0);
+    if constexpr (!SL) {
+      // blocks past K: the next row's scales, which may be NaN, times zeros
       const int b = kb * (F::kK / 32) + F::kWC * lq;
+      const uint32_t so = soff + (uint32_t)rt * 16u * (uint32_t)nb + (uint32_t)kb * (F::kK / 32);
+      wsc[p][rt] = __builtin_amdgcn_raw_buffer_load_b8(sr, b < nb ? so : kOutside, 0, 0);
+      if constexpr (MX)
+        wsc[p][rt] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(sr, b + 1 < nb ? so + 1 : kOutside, 0, 0) << 8;
+    }
+  };
+  // K block kb's scales of the rows (MXFP4), and the weight scales of its group if kb starts one
+  auto issue_s = [&](int kb) {
+    if constexpr (MX) {
+      if constexpr (SL) {
+        asc = __builtin_amdgcn_raw_buffer_load_b32(asr, kb * 8 + 4 * (tid & 1) < nb ? asoff + (uint32_t)kb * 8u : kOutside, 0, 0);
+      } else {
+        asc = 0;
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        if (b >= nb) wsc[p][rt] = 0;
-        else if (MX && b + 1 >= nb) wsc[p][rt] &= 0xffu;
+        for (int j = 0; j < 4; ++j)
+          asc |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(asr, kb * 8 + 4 * (tid & 1) + j < nb ? asoff + (uint32_t)(kb * 8 + j) : kOutside, 0, 0) << (8 * j);
+      }
+    }
+    if constexpr (SL) {
+      if (wt == 0 && kb % GB == 0)
+        to_lds16(sr, lds.ws + ((kb / GB) & 1) * (512 * 16) + wn * 1024, soff + (uint32_t)kb * (F::kK / 32));
+    }
+  };
+  // the weight scales of K block kb, from LDS
+  auto read_ws = [&](auto P, int kb) {
+    constexpr int p = decltype(P)::value;
+    if constexpr (SL) {
+      const uint8_t* b = lds.ws + ((kb / GB) & 1) * (512 * 16) + (wn * 64 + lr) * 16 + (kb % GB) * (F::kK / 32) + F::kWC * lq;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        wsc[p][rt] = MX ? *reinterpret_cast<const uint16_t*>(b + rt * 256) : b[rt * 256];
+      // a group that ends past K holds the next row's scales there
+      if ((kb + 1) * F::kK > g.K && kb * (F::kK / 32) + F::kWC * lq >= nb) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) wsc[p][rt] = 0;
       }
     }
   };
@@ -378,63 +397,95 @@ __device__ __forceinline__ void fat_tile(const MatmulArgs& g, const FatItem& it,
 #pragma unroll
     for (int c = 0; c < CT; ++c) acc[rt][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](auto P) {
-    constexpr int p = decltype(P)::value;
-    const uint8_t* st = p ? st1 : st0;
-    if constexpr (MX) {
-      uint32_t ts[CT];
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-        ts[c] = reinterpret_cast<const uint16_t*>(p ? sc1 : sc0)[((wt * CT + c) * 16 + lr) * 4 + lq];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        i32x8 B[CT];
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          const int row = (wt * CT + c) * 16 + lr;
-          const uint4 v = *reinterpret_cast<const uint4*>(st + row * 128 + 16 * F::place(lr, 2 * lq + s));
-          B[c] = i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const i32x8 A = {(int)wq[p][rt][s][0], (int)wq[p][rt][s][1], (int)wq[p][rt][s][2], (int)wq[p][rt][s][3], 0, 0, 0, 0};
-#pragma unroll
-          for (int c = 0; c < CT; ++c)
-            acc[rt][c] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B[c], acc[rt][c], 4, 4, 0, (int)wsc[p][rt], 0, (int)ts[c])
-                                : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B[c], acc[rt][c], 4, 4, 1, (int)wsc[p][rt], 1, (int)ts[c]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        bf16x8 A[RT], B[CT];
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          const int row = (wt * CT + c) * 16 + lr;
-          B[c] = *reinterpret_cast<const bf16x8*>(st + row * 256 + 16 * F::place(lr, 4 * lq + s));
-        }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) A[rt] = bf16_of(wq[p][rt][0][s], __uint_as_float(wsc[p][rt] << 23));
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-            acc[rt][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[rt], B[c], acc[rt][c], 0, 0, 0);
-      }
-    }
-  };
+  // Multiplies K block kb in sub-steps of HB column tiles, the operands of the
+  // next one read from LDS while this one's MFMAs run.  The requests for block
+  // kb + 1 are spread over the first half of the sub-steps: issued at once they
+  // would stall every wave until the address units have taken them all.
+  constexpr int HB = CT < 2 ? 1 : 2, SUB = CT / HB;
+  constexpr int STEPS = MX ? 2 : 4, NSUB = STEPS * SUB, IS = NSUB > 1 ? NSUB / 2 : 1;
   auto block = [&](auto P, int kb) {
     constexpr int p = decltype(P)::value;
+    using Q = std::integral_constant<int, 1 - p>;
+    const uint8_t* st = p ? lds.st1 : lds.st0;
     if constexpr (MX) {
-      if (tid < 2 * ROWS) (p ? sc1 : sc0)[tid] = asc;
+      if (tid < 2 * ROWS) (p ? lds.sc1 : lds.sc0)[tid] = asc;
     }
     // block kb has landed, in every wave; nobody reads the other stage any more
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    if (kb + 1 < nkb) issue(std::integral_constant<int, 1 - p>{}, kb + 1);
-    compute(P);
+    read_ws(P, kb);
+    uint32_t ts[CT];
+    if constexpr (MX) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+        ts[c] = reinterpret_cast<const uint16_t*>(p ? lds.sc1 : lds.sc0)[((wt * CT + c) * 16 + lr) * 4 + lq];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const int kn = min(kb + 1, nkb - 1);   // the last block is requested twice: no branch
+    bf16x8 A[RT];
+    uint4 B[2][HB];
+    auto read_b = [&](int j) {   // column tiles HB (j % SUB) .. of step j / SUB
+      const int s = j / SUB;
+#pragma unroll
+      for (int c = 0; c < HB; ++c) {
+        const int row = (wt * CT + HB * (j % SUB) + c) * 16 + lr;
+        B[j & 1][c] = *reinterpret_cast<const uint4*>(st + row * F::kRowBytes + 16 * F::place(lr, (MX ? 2 : 4) * lq + s));
+      }
+    };
+    read_b(0);
+    if constexpr (!MX) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) A[rt] = bf16_of(wq[p][rt][0][0], __uint_as_float(wsc[p][rt] << 23));
+    }
+#pragma unroll
+    for (int j = 0; j < NSUB; ++j) {
+      const int s = j / SUB;
+      if (j + 1 < NSUB) read_b(j + 1);
+      if (j < IS) {
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+          if (i % IS == j) issue_a(Q{}, kn, i);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          if (rt % IS == j) issue_w(Q{}, kn, rt);
+        if (j == 0) issue_s(kn);
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+        for (int c = 0; c < HB; ++c) {
+          const int ct = HB * (j % SUB) + c;
+          if constexpr (MX) {
+            const uint32_t* w = wq[p][rt][s % F::kWC];
+            const i32x8 Av = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+            const uint4 v = B[j & 1][c];
+            const i32x8 Bv = {(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+            acc[rt][ct] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(Av, Bv, acc[rt][ct], 4, 4, 0, (int)wsc[p][rt], 0, (int)ts[ct])
+                                 : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(Av, Bv, acc[rt][ct], 4, 4, 1, (int)wsc[p][rt], 1, (int)ts[ct]);
+          } else {
+            acc[rt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[rt], __builtin_bit_cast(bf16x8, B[j & 1][c]), acc[rt][ct], 0, 0, 0);
+          }
+        }
+        // the next step's operand, in the registers that these MFMAs are done with
+        if constexpr (!MX)
+          if (j % SUB == SUB - 1 && s + 1 < STEPS)
+            A[rt] = bf16_of(wq[p][rt][0][s + 1], __uint_as_float(wsc[p][rt] << 23));
+      }
+      // the next reads first, then the next codes' conversion between the MFMAs
+      __builtin_amdgcn_sched_group_barrier(0x100, HB, 0);
+#pragma unroll
+      for (int i = 0; i < HB * RT; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
-  issue(std::integral_constant<int, 0>{}, 0);
+  issue_s(0);
+#pragma unroll
+  for (int i = 0; i < NA; ++i) issue_a(std::integral_constant<int, 0>{}, 0, i);
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) issue_w(std::integral_constant<int, 0>{}, 0, rt);
   for (int kb = 0; kb < nkb; kb += 2) {
     block(std::integral_constant<int, 0>{}, kb);
     if (kb + 1 < nkb) block(std::integral_constant<int, 1>{}, kb + 1);
@@ -450,22 +501,24 @@ __device__ __forceinline__ void fat_tile(const MatmulArgs& g, const FatItem& it,
   }
 }
 
-template <bool MX>
+template <bool MX, bool SL>
 __global__ void __launch_bounds__(kFatThreads, 2) mx_matmul_fat_kernel(MatmulArgs g, int ntw, int ntn) {
   __shared__ __attribute__((aligned(16))) uint8_t st0[kStageBytes / (MX ? 2 : 1)];
   __shared__ __attribute__((aligned(16))) uint8_t st1[kStageBytes / (MX ? 2 : 1)];
+  __shared__ __attribute__((aligned(16))) uint8_t wsl[SL ? 2 * 512 * 16 : 16];
   __shared__ uint32_t sc0[MX ? 512 : 1], sc1[MX ? 512 : 1];
   FatItem it;
   if (!find_item(g.offsets, g.E, g.R, ntw, ntn, it)) return;
+  const FatLds lds{st0, st1, sc0, sc1, wsl};
   if (it.wide) {
-    if (it.M > 192) fat_tile<MX, 2, 8>(g, it, st0, st1, sc0, sc1);
-    else fat_tile<MX, 2, 6>(g, it, st0, st1, sc0, sc1);
+    if (it.M > 192) fat_tile<MX, SL, 2, 8>(g, it, lds);
+    else fat_tile<MX, SL, 2, 6>(g, it, lds);
   } else {
-    if (it.M > 96) fat_tile<MX, 1, 8>(g, it, st0, st1, sc0, sc1);
-    else if (it.M > 64) fat_tile<MX, 1, 6>(g, it, st0, st1, sc0, sc1);
-    else if (it.M > 32) fat_tile<MX, 1, 4>(g, it, st0, st1, sc0, sc1);
-    else if (it.M > 16) fat_tile<MX, 1, 2>(g, it, st0, st1, sc0, sc1);
-    else fat_tile<MX, 1, 1>(g, it, st0, st1, sc0, sc1);
+    if (it.M > 96) fat_tile<MX, SL, 1, 8>(g, it, lds);
+    else if (it.M > 64) fat_tile<MX, SL, 1, 6>(g, it, lds);
+    else if (it.M > 32) fat_tile<MX, SL, 1, 4>(g, it, lds);
+    else if (it.M > 16) fat_tile<MX, SL, 1, 2>(g, it, lds);
+    else fat_tile<MX, SL, 1, 1>(g, it, lds);
   }
 }
 
@@ -479,8 +532,10 @@ hipError_t launch_mx_matmul(const MatmulArgs& g, bool a_mxfp4, hipStream_t s) {
   if (g.R >= 8 * (int64_t)g.E && (int64_t)g.R * g.N >= 64 * 256 * 256 && span < (int64_t)kOutside) {
     const int ntw = (g.N + 255) / 256, ntn = (g.N + 511) / 512;
     const dim3 grid((unsigned)(((long)g.R / kFatRows + std::min(g.E, g.R)) * ntw));
-    if (a_mxfp4) hipLaunchKernelGGL(mx_matmul_fat_kernel<true>, grid, dim3(kFatThreads), 0, s, g, ntw, ntn);
-    else hipLaunchKernelGGL(mx_matmul_fat_kernel<false>, grid, dim3(kFatThreads), 0, s, g, ntw, ntn);
+    const bool sl = g.K % 128 == 0;
+    auto* k = a_mxfp4 ? (sl ? mx_matmul_fat_kernel<true, true> : mx_matmul_fat_kernel<true, false>)
+                      : (sl ? mx_matmul_fat_kernel<false, true> : mx_matmul_fat_kernel<false, false>);
+    hipLaunchKernelGGL(k, grid, dim3(kFatThreads), 0, s, g, ntw, ntn);
     return hipGetLastError();
   }
   const int nt = (g.N + 63) / 64;

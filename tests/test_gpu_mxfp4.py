@@ -204,6 +204,43 @@ def test_matmul(counts, n, k, extra, gather, act, out):
     _run(Problem(counts, n, k, seed=n + k, extra=extra, gather=gather), act, out)
 
 
+LARGE = [  # large enough for the tiles of 256 and 512 outputs; every count of column tiles
+    ([1100], 4097, 128, 0, 0), ([300, 0, 129, 17, 33, 65, 97, 1, 257, 150], 4100, 160, 3, 77), ([513, 512], 4608, 672, 0, 0),
+    ([190, 70, 200, 256, 90, 40, 10, 20], 5000, 1152, 0, 500), ([200, 5, 120, 255, 30], 6300, 2112, 2, 33)]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("counts,n,k,extra,gather", LARGE)
+def test_large_matmul(counts, n, k, extra, gather, act, out):
+    _run(Problem(counts, n, k, seed=n + k, extra=extra, gather=gather), act, out, ldo=n + 3 if k == 672 else None)
+
+
+@pytest.mark.parametrize("k", [128, 352])
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+def test_large_matmul_keeps_nan_in_place(act, k):
+    """As below for the large tiles: NaN scales in the row after a tile's last
+    block and in the last block itself, a NaN input, an index outside."""
+    P = Problem([700, 400], 4100, k, seed=k, gather=300)
+    P.index[3], P.index[900] = -1, 300
+    P.a[7, k - 1] = float("nan")
+    P.ws[1, 4099, 0] = 255
+    P.ws[0, 77, k // 32 - 1] = 255
+    o = torch.empty(1100, 4100, device="cuda")
+    idx = P.index.cuda()
+    if act == "bf16":
+        q.moe_mxfp4_matmul(P.a.cuda(), P.wq.cuda(), P.ws.cuda(), o, expert_offsets=P.offsets(), row_index=idx)
+    else:
+        codes, scales = _quantize(P.a.cuda())
+        q.moe_mxfp4_matmul(codes, P.wq.cuda(), P.ws.cuda(), o, a_scale=scales, expert_offsets=P.offsets(),
+                           row_index=idx)
+    nan = torch.isnan(o).cpu()
+    want = (P.index == 7)[:, None].expand(1100, 4100).clone()
+    want[:700, 77] = True
+    want[700:, 4099] = True
+    assert torch.equal(nan, want)
+
+
 @pytest.mark.parametrize("act", ["bf16", "mxfp4"])
 @pytest.mark.parametrize("R", [1, 5, 40, 300])
 def test_matmul_of_one_expert_without_offsets(R, act):
