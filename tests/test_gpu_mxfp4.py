@@ -318,7 +318,10 @@ def test_extreme_weight_scales(act):
 
 DX = [([1], 32, 32, 0), ([1], 256, 256, 0), ([2, 0, 3], 96, 160, 1), ([1] * 8, 512, 544, 0), ([16, 17, 1], 128, 512, 0),
       ([33, 31, 0, 64], 160, 1056, 2), ([127, 129], 256, 96, 0), ([300, 5], 2080, 288, 0), ([0, 0], 64, 64, 3),
-      ([520], 64, 1536, 0), ([1] * 200, 32, 64, 0), ([2, 1, 1, 4], 4096, 128, 0)]
+      ([520], 64, 1536, 0), ([1] * 200, 32, 64, 0), ([2, 1, 1, 4], 4096, 128, 0),
+      # large tiles
+      ([300, 0, 129, 17, 33, 65, 97, 1, 257, 150], 160, 4128, 3), ([700], 96, 6112, 0), ([512, 513], 32, 4352, 0),
+      ([200, 190, 70, 90, 40, 10], 1056, 7200, 0), ([1100], 224, 4096, 1)]
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
@@ -346,6 +349,25 @@ def test_dx_nan_and_strides(R):
     assert np.isnan(o[1]).all() and np.isnan(o[:R, 320:]).all()
     o[1] = 0
     assert np.isfinite(o[:, :320]).all() and np.isfinite(o[R:]).all()
+
+
+def test_large_dx_keeps_nan_in_place():
+    """NaN scales in the row after the last term of an expert's sums and in one
+    column block, a NaN in dy, dy rows inside a matrix of NaN."""
+    n, k = 160, 4128
+    P = Problem([700, 400], n, k, seed=1)
+    wide = torch.full((1100, n + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, :n] = P.dy.cuda()
+    wide[9, n - 1] = float("nan")
+    P.ws[1, 0] = 255
+    P.ws[0, 33, 128] = 255
+    o = torch.empty(1100, k, device="cuda")
+    q.moe_mxfp4_matmul_dx(wide[:, :n], P.wq.cuda(), P.ws.cuda(), o, expert_offsets=P.offsets())
+    want = torch.zeros(1100, k, dtype=torch.bool)
+    want[9] = True
+    want[:700, 4096:4128] = True
+    want[700:] = True
+    assert torch.equal(torch.isnan(o).cpu(), want)
 
 
 @pytest.mark.parametrize("R", [4, 70])
