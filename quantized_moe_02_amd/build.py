@@ -21,7 +21,8 @@ BUILD = os.path.join(ROOT, "_build")
 
 SOURCES = ["qmoe_api.cpp", "route.hip", "permute.hip", "gemv.hip", "decode.hip", "gemm.hip",
            "gemm_i8.hip", "noalloc.hip", "expert_cache.cpp", "operators_api.cpp", "mxfp4.hip",
-           "mxfp4_matmul.hip", "mxfp4_large.hip", "mxfp4_dx.hip", "balance.hip"]
+           "mxfp4_matmul.hip", "mxfp4_large.hip", "mxfp4_large4.hip",
+           "mxfp4_dx.hip", "balance.hip"]
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",
