@@ -318,19 +318,35 @@ def _require(ok: bool, where: str):
         raise QmoeError(MOE_ERR_INVALID_ARG, where)
 
 
-def _fits(where: str, t: torch.Tensor, dtype, shape):
+def _fits(where: str, t: torch.Tensor, dtype, shape: tuple):
     """`t` is a contiguous device tensor of this type and shape."""
-    _require(t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-             where)
+    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+        raise QmoeError(MOE_ERR_INVALID_ARG, where)
 
 
 def _matrix(where: str, t: torch.Tensor, dtypes):
-    """`t` is a device matrix whose rows are contiguous; returns its row stride."""
-    _require(t.is_cuda and t.dim() == 2 and t.dtype in dtypes, where)
-    rows, cols = t.shape
-    _require(cols <= 1 or t.stride(1) == 1, where)
-    _require(rows <= 1 or t.stride(0) >= cols, where)
-    return t.stride(0) if rows > 1 else max(cols, 1)
+    """`t` is a device matrix whose rows are contiguous; returns its rows,
+    columns and row stride."""
+    shape = t.shape
+    if not (t.is_cuda and len(shape) == 2 and t.dtype in dtypes):
+        raise QmoeError(MOE_ERR_INVALID_ARG, where)
+    rows, cols = shape
+    if t.is_contiguous():
+        return rows, cols, max(cols, 1)
+    ld, step = t.stride()
+    _require((cols <= 1 or step == 1) and (rows <= 1 or ld >= cols), where)
+    return rows, cols, ld if rows > 1 else max(cols, 1)
+
+
+def _queue(stream, t: torch.Tensor):
+    """The stream's handle; by default the current stream of `t`'s device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def mxfp4_empty(rows: int, cols: int, device="cuda"):
@@ -341,8 +357,7 @@ def mxfp4_empty(rows: int, cols: int, device="cuda"):
 
 
 def _mxfp4_rows(where, x, codes, scales):
-    ld = _matrix(where, x, _DT)
-    rows, cols = x.shape
+    rows, cols, ld = _matrix(where, x, _DT)
     nb = (cols + 31) // 32
     _fits(where, codes, torch.uint8, (rows, 16 * nb))
     _fits(where, scales, torch.uint8, (rows, nb))
@@ -352,25 +367,30 @@ def _mxfp4_rows(where, x, codes, scales):
 def moe_mxfp4_quantize(src, codes, scales, stream=None):
     """Rows of `src` (fp32, bf16 or fp16) to MXFP4 codes and scales."""
     rows, cols, ld = _mxfp4_rows("moe_mxfp4_quantize", src, codes, scales)
-    _check(lib().moe_mxfp4_quantize(_p(src), _DT[src.dtype], rows, cols, ld, _p(codes), _p(scales),
-                                    _stream(stream)), "moe_mxfp4_quantize")
+    _check(lib().moe_mxfp4_quantize(src.data_ptr(), _DT[src.dtype], rows, cols, ld, codes.data_ptr(),
+                                    scales.data_ptr(), _queue(stream, src)), "moe_mxfp4_quantize")
 
 
 def moe_mxfp4_dequantize(codes, scales, dst, stream=None):
     """The values of MXFP4 rows, into `dst` (fp32, bf16 or fp16)."""
     rows, cols, ld = _mxfp4_rows("moe_mxfp4_dequantize", dst, codes, scales)
-    _check(lib().moe_mxfp4_dequantize(_p(codes), _p(scales), rows, cols, _p(dst), _DT[dst.dtype], ld,
-                                      _stream(stream)), "moe_mxfp4_dequantize")
+    _check(lib().moe_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, dst.data_ptr(),
+                                      _DT[dst.dtype], ld, _queue(stream, dst)), "moe_mxfp4_dequantize")
 
 
 def _grouped_weights(where, w_codes, w_scales, expert_offsets):
-    _require(w_codes.dim() == 3, where)
-    E, N, kb = w_codes.shape
-    _fits(where, w_codes, torch.uint8, (E, N, kb))
+    shape = w_codes.shape
+    _require(len(shape) == 3, where)
+    E, N, kb = shape
+    _fits(where, w_codes, torch.uint8, shape)
     _fits(where, w_scales, torch.uint8, (E, N, kb // 16))
     if expert_offsets is not None:
         _fits(where, expert_offsets, torch.int32, (E + 1,))
     return E, N, kb * 2
+
+
+_OUT_DT = (torch.float32, torch.bfloat16)
+_BF16 = (torch.bfloat16,)
 
 
 def moe_mxfp4_matmul(a, w_codes, w_scales, out, a_scale=None, expert_offsets=None, row_index=None,
@@ -379,36 +399,36 @@ def moe_mxfp4_matmul(a, w_codes, w_scales, out, a_scale=None, expert_offsets=Non
     `a` is bf16 [rows][k], or MXFP4 codes uint8 [rows][k/2] with `a_scale`."""
     where = "moe_mxfp4_matmul"
     E, N, K = _grouped_weights(where, w_codes, w_scales, expert_offsets)
-    ldo = _matrix(where, out, (torch.float32, torch.bfloat16))
-    R = out.shape[0]
-    _require(out.shape[1] == N, where)
+    R, cols, ldo = _matrix(where, out, _OUT_DT)
+    _require(cols == N, where)
     if a_scale is None:
-        lda = _matrix(where, a, (torch.bfloat16,))
-        _require(a.shape[1] == K, where)
+        a_rows, cols, lda = _matrix(where, a, _BF16)
+        _require(cols == K, where)
         dt = MOE_DT_BF16
     else:
-        _require(a.dim() == 2, where)
-        _fits(where, a, torch.uint8, (a.shape[0], K // 2))
-        _fits(where, a_scale, torch.uint8, (a.shape[0], K // 32))
+        a_rows = a.shape[0]
+        _fits(where, a, torch.uint8, (a_rows, K // 2))
+        _fits(where, a_scale, torch.uint8, (a_rows, K // 32))
         lda, dt = K, MOE_DT_MXFP4
     if row_index is not None:
         _fits(where, row_index, torch.int32, (R,))
-    cfg = MoeMatmulConfig(R, N, K, E, a.shape[0], dt, _DT[out.dtype], lda, ldo)
-    _check(lib().moe_mxfp4_matmul(ctypes.byref(cfg), _p(a), _p(a_scale), _p(w_codes), _p(w_scales),
-                                  _p(expert_offsets), _p(row_index), _p(out), _stream(stream)), where)
+    cfg = MoeMatmulConfig(R, N, K, E, a_rows, dt, _DT[out.dtype], lda, ldo)
+    _check(lib().moe_mxfp4_matmul(ctypes.byref(cfg), a.data_ptr(), _at(a_scale), w_codes.data_ptr(),
+                                  w_scales.data_ptr(), _at(expert_offsets), _at(row_index),
+                                  out.data_ptr(), _queue(stream, out)), where)
 
 
 def moe_mxfp4_matmul_dx(dy, w_codes, w_scales, dx, expert_offsets=None, stream=None):
     """dx[r] = dy[r] @ W[expert of r]: the gradient of moe_mxfp4_matmul's rows."""
     where = "moe_mxfp4_matmul_dx"
     E, N, K = _grouped_weights(where, w_codes, w_scales, expert_offsets)
-    lda = _matrix(where, dy, (torch.bfloat16,))
-    ldo = _matrix(where, dx, (torch.float32, torch.bfloat16))
-    R = dx.shape[0]
-    _require(tuple(dy.shape) == (R, N) and dx.shape[1] == K, where)
+    rows, cols, lda = _matrix(where, dy, _BF16)
+    R, dx_cols, ldo = _matrix(where, dx, _OUT_DT)
+    _require(rows == R and cols == N and dx_cols == K, where)
     cfg = MoeMatmulConfig(R, N, K, E, R, MOE_DT_BF16, _DT[dx.dtype], lda, ldo)
-    _check(lib().moe_mxfp4_matmul_dx(ctypes.byref(cfg), _p(dy), _p(w_codes), _p(w_scales),
-                                     _p(expert_offsets), _p(dx), _stream(stream)), where)
+    _check(lib().moe_mxfp4_matmul_dx(ctypes.byref(cfg), dy.data_ptr(), w_codes.data_ptr(),
+                                     w_scales.data_ptr(), _at(expert_offsets), dx.data_ptr(),
+                                     _queue(stream, dx)), where)
 
 
 def make_balance_config(tokens: int, n_experts: int, top_k: int = 1, n_seq: int = 1,
@@ -432,16 +452,16 @@ def balance_workspace(tokens: int, n_experts: int, n_seq: int = 1, device="cuda"
 
 def _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets):
     _require(logits.dim() == 2 and topk_ids.dim() == 2 and counts.dim() == 2 and score in _SCORE, where)
-    T, E = logits.shape
-    S = counts.shape[0]
-    _require(logits.dtype in (torch.float32, torch.bfloat16), where)
-    _fits(where, logits, logits.dtype, (T, E))
-    _fits(where, topk_ids, torch.int32, (T, topk_ids.shape[1]))
+    T, E = shape = logits.shape
+    S, K = counts.shape[0], topk_ids.shape[1]
+    _require(logits.dtype in _OUT_DT, where)
+    _fits(where, logits, logits.dtype, shape)
+    _fits(where, topk_ids, torch.int32, (T, K))
     _fits(where, counts, torch.int32, (S, E))
     _fits(where, tokens, torch.int32, (S,))
     if seq_offsets is not None:
         _fits(where, seq_offsets, torch.int32, (S + 1,))
-    return make_balance_config(T, E, topk_ids.shape[1], S, score, logits.dtype, coef)
+    return MoeBalanceConfig(T, E, K, S, _SCORE[score], _DT[logits.dtype], coef)
 
 
 def moe_balance_loss(logits, topk_ids, counts, tokens, loss, coef, score="sigmoid", seq_offsets=None,
@@ -451,9 +471,11 @@ def moe_balance_loss(logits, topk_ids, counts, tokens, loss, coef, score="sigmoi
     where = "moe_balance_loss"
     cfg = _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets)
     _fits(where, loss, torch.float32, (1,))
-    _check(lib().moe_balance_loss(ctypes.byref(cfg), _p(logits), _p(topk_ids), _p(seq_offsets),
-                                  _p(counts), _p(tokens), _p(loss), _p(ws),
-                                  0 if ws is None else ws.numel(), _stream(stream)), where)
+    _require(ws is None or (ws.is_cuda and ws.dtype is torch.uint8 and ws.is_contiguous()), where)
+    _check(lib().moe_balance_loss(ctypes.byref(cfg), logits.data_ptr(), topk_ids.data_ptr(),
+                                  _at(seq_offsets), counts.data_ptr(), tokens.data_ptr(),
+                                  loss.data_ptr(), _at(ws), 0 if ws is None else ws.numel(),
+                                  _queue(stream, counts)), where)
 
 
 def moe_balance_loss_grad(logits, topk_ids, counts, tokens, dlogits, coef, score="sigmoid",
@@ -465,6 +487,6 @@ def moe_balance_loss_grad(logits, topk_ids, counts, tokens, dlogits, coef, score
     _fits(where, dlogits, logits.dtype, logits.shape)
     if dloss is not None:
         _fits(where, dloss, torch.float32, (1,))
-    _check(lib().moe_balance_loss_grad(ctypes.byref(cfg), _p(logits), _p(topk_ids), _p(seq_offsets),
-                                       _p(counts), _p(tokens), _p(dloss), _p(dlogits),
-                                       _stream(stream)), where)
+    _check(lib().moe_balance_loss_grad(ctypes.byref(cfg), logits.data_ptr(), topk_ids.data_ptr(),
+                                       _at(seq_offsets), counts.data_ptr(), tokens.data_ptr(),
+                                       _at(dloss), dlogits.data_ptr(), _queue(stream, counts)), where)

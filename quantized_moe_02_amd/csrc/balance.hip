@@ -1,17 +1,25 @@
 // Balance loss of the router, its per-expert counts and its gradient.
 //
-// With a = l (softmax) or log sigmoid(l) (sigmoid), a token's shares are
-// p = softmax(a) either way: sigmoid(l) / sum sigmoid(l) = exp(a) / sum
-// exp(a), so subtracting the row's largest a keeps both from overflowing and
-// from 0 / 0 where every sigmoid underflows.  da/dl = 1 or sigmoid(-l).
+// A token's shares are p = y / sum y with y = exp(l) (softmax) or y =
+// sigmoid(l).  Both only depend on l up to a factor of y: the softmax takes
+// the row's largest logit out, and so does the sigmoid where every logit is
+// below -64, where sigmoid(l) = exp(l) to the last bit and could underflow
+// throughout.  Its slope d log y / dl is 1 or sigmoid(-l).
 //
-// Forward: the tokens are cut into chunks; a workgroup sums the shares and
-// counts the picks of each sequence that its chunk touches and writes the
-// partial sums to slot chunk + sequence (both ascend along the tokens, so the
-// slots of different pairs differ).  A second launch, one workgroup per
-// sequence, adds a sequence's partials in order; the last workgroup to finish
-// adds the sequences' losses.  No atomics on floats: the same bits every time.
-// Sums within a chunk are fp32, across chunks and for the loss float64.
+// A lane holds four experts of a token, so a token takes the 4 to 64 lanes that
+// its experts fill (LPT) and a wave several small tokens; sums and maxima over
+// a token cross lanes within them.  Everything is one pass over the logits,
+// bound by HBM: four rows per lane are requested at a time.
+//
+// Forward: the tokens are cut into chunks, one workgroup each; it counts the
+// picks and sums the shares of each sequence that its chunk touches and writes
+// them to slot chunk + sequence (both ascend along the tokens, so the slots of
+// different pairs differ).  A second launch adds a sequence's partials in
+// order, 32 experts per workgroup; the last workgroup to finish adds up the
+// loss.  No atomics on floats: the same bits every time.  Sums within a chunk
+// are fp32, across chunks and for the loss float64.
+#include <algorithm>
+
 #include "operators_internal.h"
 #include "qmoe_device.h"
 
@@ -19,22 +27,36 @@ namespace qmoe {
 namespace {
 
 constexpr int kMaxE = 256;
-constexpr int kPer = kMaxE / kWave;   // experts per lane: lane + 64 j
+constexpr int kMaxChunk = 256;   // MOE_MAX_TOKENS / 1024
+constexpr int kRows = 4;         // rows in flight per lane
+constexpr int kSliceE = 32;      // experts per workgroup of the second launch
+constexpr int kSlices = 8;       // shares of a sequence's chunks in it
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+template <int LPT>
+__device__ __forceinline__ float group_sum(float v) {
+  v += dppf<kDppXor1>(v);
+  v += dppf<kDppXor2>(v);
+  if constexpr (LPT >= 8) v += dppf<kDppHalfMirror>(v);
+  if constexpr (LPT >= 16) v += dppf<kDppMirror>(v);
+  if constexpr (LPT >= 32) v = swap16_sum(v);
+  if constexpr (LPT >= 64) v = swap32_sum(v);
   return v;
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+template <int LPT>
+__device__ __forceinline__ float group_max(float v) {
+  v = fmaxf(v, dppf<kDppXor1>(v));
+  v = fmaxf(v, dppf<kDppXor2>(v));
+  if constexpr (LPT >= 8) v = fmaxf(v, dppf<kDppHalfMirror>(v));
+  if constexpr (LPT >= 16) v = fmaxf(v, dppf<kDppMirror>(v));
+  if constexpr (LPT >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  if constexpr (LPT >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
   return v;
-}
-
-__device__ __forceinline__ float load_logit(const BalanceArgs& a, int64_t i) {
-  return a.bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.logits)[i] << 16)
-                : static_cast<const float*>(a.logits)[i];
 }
 
 // Offset of sequence s, clamped to the tokens.
@@ -53,192 +75,332 @@ __device__ __forceinline__ int seq_of(const BalanceArgs& a, int t) {
   return lo;
 }
 
-// Lane i < K: pick i of token t (-1 beyond); the token is routed if any lane has one.
-__device__ __forceinline__ int load_pick(const BalanceArgs& a, int t, int lane) {
-  const int id = lane < a.K ? a.ids[(int64_t)t * a.K + lane] : -1;
-  return id >= 0 && id < a.E ? id : -1;
-}
-
-// The token's shares at experts lane + 64 j (0 past E), and d of its logits.
-__device__ __forceinline__ void shares(const BalanceArgs& a, int t, int lane, float (&p)[kPer], float (&d)[kPer]) {
-  float m = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = lane + 64 * j;
-    p[j] = -INFINITY;
-    d[j] = 1.0f;
+// Logits of token t at experts e .. e + 3, -inf past E.  VEC: E % 4 == 0.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ float4 load_row(const BalanceArgs& a, int t, int e) {
+  const float none = -INFINITY;
+  const int64_t i = (int64_t)t * a.E + e;
+  float4 v = make_float4(none, none, none, none);
+  if constexpr (VEC) {
     if (e < a.E) {
-      const float l = load_logit(a, (int64_t)t * a.E + e);
-      p[j] = l;
-      if (a.sigmoid) {
-        const float x = expf(-fabsf(l));
-        p[j] = fminf(l, 0.0f) - log1pf(x);
-        d[j] = (l > 0.0f ? x : 1.0f) / (1.0f + x);
-        if (l != l) p[j] = l;   // fminf drops the NaN
+      if constexpr (BF16) {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + i);
+        v = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+      } else {
+        v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + i);
       }
     }
-    m = fmaxf(m, p[j]);
+  } else {
+    auto at = [&](int j) {
+      if (e + j >= a.E) return none;
+      if constexpr (BF16) return bf16_lo(static_cast<const uint16_t*>(a.logits)[i + j]);
+      return static_cast<const float*>(a.logits)[i + j];
+    };
+    v = make_float4(at(0), at(1), at(2), at(3));
   }
-  m = wave_max(m);
-  float z = 0.0f;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    p[j] = lane + 64 * j < a.E ? expf(p[j] - m) : 0.0f;
-    z += p[j];
-  }
-  z = wave_sum(z);
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) p[j] /= z;
+  return v;
 }
 
+// Shares of the token whose logits the LPT lanes of a group hold; with SLOPE
+// also d log y / dl.
+template <int LPT, bool SIGMOID, bool SLOPE>
+__device__ __forceinline__ void shares(const float4& l4, float (&p)[4], float (&d)[4]) {
+  const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+  const float top = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
+  if constexpr (SIGMOID) {
+    // lanes of groups with a logit above -64
+    uint64_t high = __ballot(top > -64.0f);
+    if constexpr (LPT < 64) {
+      const int g0 = (int)(threadIdx.x & 63) & ~(LPT - 1);
+      high = (high >> g0) & ((1ull << LPT) - 1);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x = __expf(-fabsf(l[j]));
+      const float r = __builtin_amdgcn_rcpf(1.0f + x);
+      p[j] = l[j] >= 0.0f ? r : x * r;
+      if constexpr (SLOPE) d[j] = l[j] >= 0.0f ? x * r : r;
+    }
+    if (__any(high == 0)) {
+      const float m = group_max<LPT>(top);
+      if (high == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j] = __expf(l[j] - m);
+      }
+    }
+  } else {
+    const float m = group_max<LPT>(top);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      p[j] = __expf(l[j] - m);
+      if constexpr (SLOPE) d[j] = 1.0f;
+    }
+  }
+  const float z = 1.0f / group_sum<LPT>((p[0] + p[1]) + (p[2] + p[3]));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p[j] *= z;
+}
+
+template <int LPT, bool SIGMOID, bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) balance_partial_kernel(BalanceArgs a, int chunk) {
-  __shared__ float sp[4][kMaxE];
+  constexpr int TPW = 64 / LPT;   // tokens per wave
+  __shared__ __attribute__((aligned(16))) float sp[4 * TPW][LPT * 4];
   __shared__ int sc[kMaxE], sn;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+  __shared__ uint8_t routed[kMaxChunk];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int group = wv * TPW + lane / LPT, e0 = (lane % LPT) * 4;
+  if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;
   const int t0 = blockIdx.x * chunk, t1 = min(a.T, t0 + chunk);
   if (t0 >= t1) return;
   for (int s = seq_of(a, t0); s < a.S; ++s) {
     const int lo = max(t0, seq_at(a, s)), hi = min(t1, seq_at(a, s + 1));
     if (lo >= t1) break;
     if (lo >= hi) continue;
+    sc[tid] = 0;
+    routed[tid] = 0;
+    if (tid == 0) sn = 0;
     __syncthreads();
-    sc[threadIdx.x] = 0;
-    if (threadIdx.x == 0) sn = 0;
-    __syncthreads();
-    float acc[kPer] = {};
-    int n = 0;
-    for (int t = lo + wv; t < hi; t += 4) {
-      const int id = load_pick(a, t, lane);
-      if (!__any(id >= 0)) continue;
-      ++n;
-      if (id >= 0) atomicAdd(&sc[id], 1);
-      float p[kPer], d[kPer];
-      shares(a, t, lane, p, d);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) acc[j] += p[j];
+    const int picks = (hi - lo) * a.K;
+    for (int i = tid; i < picks; i += 256) {
+      const int id = a.ids[(int64_t)lo * a.K + i];
+      if (id >= 0 && id < a.E) {
+        atomicAdd(&sc[id], 1);
+        routed[i / a.K] = 1;
+      }
     }
+    __syncthreads();
+    if (tid < hi - lo && routed[tid]) atomicAdd(&sn, 1);
+    float acc[4] = {};
+    for (int b = lo; b < hi; b += 4 * TPW * kRows) {
+      float4 l[kRows];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) sp[wv][lane + 64 * j] = acc[j];
-    if (lane == 0) atomicAdd(&sn, n);
+      for (int u = 0; u < kRows; ++u) l[u] = load_row<BF16, VEC>(a, min(b + u * 4 * TPW + group, hi - 1), e0);
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int t = b + u * 4 * TPW + group;
+        float p[4], d[4];
+        shares<LPT, SIGMOID, false>(l[u], p, d);
+        const bool on = t < hi && routed[min(t, hi - 1) - lo];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] += on ? p[j] : 0.0f;
+      }
+    }
+    *reinterpret_cast<float4*>(&sp[group][e0]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
     __syncthreads();
     const int64_t slot = (int64_t)blockIdx.x + s;
-    const int e = threadIdx.x;
-    if (e < a.E) {
-      a.part_p[slot * a.E + e] = (sp[0][e] + sp[1][e]) + (sp[2][e] + sp[3][e]);
-      a.part_c[slot * a.E + e] = sc[e];
+    if (tid < a.E) {
+      float t = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4 * TPW; ++i) t += sp[i][tid];
+      a.part_p[slot * a.E + tid] = t;
+      a.part_c[slot * a.E + tid] = sc[tid];
     }
-    if (e == 0) a.part_n[slot] = sn;
+    if (tid == 0) a.part_n[slot] = sn;
+    __syncthreads();
   }
 }
 
-__global__ void __launch_bounds__(256) balance_reduce_kernel(BalanceArgs a, int chunk) {
-  __shared__ double red[256];
-  __shared__ int redi[256];
+// One workgroup: 32 experts of one sequence, eight threads per expert, each a
+// range of the chunks.
+__global__ void __launch_bounds__(256) balance_reduce_kernel(BalanceArgs a, int chunk, int slices) {
+  __shared__ double rp[kSlices][kSliceE], rs[256];
+  __shared__ int rc[kSlices][kSliceE], rn[256];
   __shared__ bool last;
-  const int s = blockIdx.x, e = threadIdx.x;
+  const int s = blockIdx.x / slices, part = blockIdx.x - s * slices;
+  const int tid = threadIdx.x, x = tid % kSliceE, y = tid / kSliceE;
+  const int e = part * kSliceE + x;
   const int lo = seq_at(a, s), hi = seq_at(a, s + 1);
+  const int c0 = lo / chunk, nc = hi > lo ? (hi - 1) / chunk - c0 + 1 : 0;
   double p = 0.0;
   int c = 0, n = 0;
-  if (hi > lo) {
-    const int c0 = lo / chunk, c1 = (hi - 1) / chunk;
-    for (int k = c0; k <= c1; ++k) {
-      const int64_t slot = (int64_t)k + s;
-      if (e < a.E) {
-        p += (double)a.part_p[slot * a.E + e];
-        c += a.part_c[slot * a.E + e];
-      }
-      n += a.part_n[slot];
+  if (e < a.E) {
+    const int per = (nc + kSlices - 1) / kSlices;
+    const int64_t first = (int64_t)c0 + s;
+    const int k1 = min(nc, (y + 1) * per);
+#pragma unroll 8
+    for (int k = y * per; k < k1; ++k) {
+      p += (double)a.part_p[(first + k) * a.E + e];
+      c += a.part_c[(first + k) * a.E + e];
     }
   }
-  if (e < a.E) a.counts[(int64_t)s * a.E + e] = c;
-  if (e == 0) a.tokens[s] = n;
-  red[e] = p * c;
-  redi[e] = c;
+  for (int k = tid; k < nc; k += 256) n += a.part_n[(int64_t)c0 + s + k];
+  rp[y][x] = p;
+  rc[y][x] = c;
+  rn[tid] = n;
   __syncthreads();
   for (int o = 128; o > 0; o >>= 1) {
-    if (e < o) {
-      red[e] += red[e + o];
-      redi[e] += redi[e + o];
-    }
+    if (tid < o) rn[tid] += rn[tid + o];
     __syncthreads();
   }
-  if (e == 0) {
-    const double l = n > 0 ? red[0] * a.E / ((double)redi[0] * n) : 0.0;
-    __hip_atomic_store(&a.seq_loss[s], l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)a.S - 1;
+  if (y == 0) {
+#pragma unroll
+    for (int i = 1; i < kSlices; ++i) {
+      p += rp[i][x];
+      c += rc[i][x];
+    }
+    if (e < a.E) a.counts[(int64_t)s * a.E + e] = c;
+    rp[0][x] = p * c;
+    rc[0][x] = c;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    double t = 0.0;
+    int picks = 0;
+    for (int i = 0; i < kSliceE; ++i) {
+      t += rp[0][i];
+      picks += rc[0][i];
+    }
+    if (part == 0) a.tokens[s] = rn[0];
+    // sum of c p over these experts, scaled by 1 / n; the picks join in the last workgroup
+    __hip_atomic_store(&a.seq_loss[blockIdx.x], rn[0] > 0 ? t / rn[0] : 0.0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(&a.seq_picks[blockIdx.x], picks, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
   double t = 0.0;
-  for (int i = e; i < a.S; i += 256) t += __hip_atomic_load(&a.seq_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  red[e] = t;
+  for (int i = tid; i < a.S; i += 256) {
+    double v = 0.0;
+    int picks = 0;
+    for (int j = 0; j < slices; ++j) {
+      v += __hip_atomic_load(&a.seq_loss[i * slices + j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      picks += __hip_atomic_load(&a.seq_picks[i * slices + j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (picks > 0) t += v * a.E / picks;
+  }
+  rs[tid] = t;
   __syncthreads();
   for (int o = 128; o > 0; o >>= 1) {
-    if (e < o) red[e] += red[e + o];
+    if (tid < o) rs[tid] += rs[tid + o];
     __syncthreads();
   }
-  if (e == 0) *a.loss = (float)(red[0] * a.coef / a.S);
+  if (tid == 0) *a.loss = (float)(rs[0] * a.coef / a.S);
 }
 
-// One wave per token.
-__global__ void __launch_bounds__(256) balance_grad_kernel(BalanceArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= a.T) return;
-  const int s = seq_of(a, t);
-  float g[kPer] = {};
-  if (__any(load_pick(a, t, lane) >= 0) && s < a.S) {
-    float p[kPer], d[kPer], f[kPer];
-    shares(a, t, lane, p, d);
-    int c[kPer], tot = 0;
+// A wave takes `per` consecutive tokens (a multiple of TPW * kRows).
+template <int LPT, bool SIGMOID, bool BF16, bool VEC>
+__global__ void __launch_bounds__(256) balance_grad_kernel(BalanceArgs a, int per) {
+  constexpr int TPW = 64 / LPT;
+  const int lane = threadIdx.x & 63, group = lane / LPT, e0 = (lane % LPT) * 4;
+  const int wave = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t w0 = (int64_t)wave * per;
+  if (w0 >= a.T) return;
+  const int t0 = (int)w0, t1 = min(a.T, t0 + per);
+  const double up = a.dloss ? (double)*a.dloss : 1.0;
+  float f[4] = {}, scale = 0.0f;
+  int s = -1, s_end = -1;   // the sequence that f and scale belong to
+  for (int b = t0; b < t1; b += TPW * kRows) {
+    float4 l[kRows];
+    bool on[kRows];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int e = lane + 64 * j;
-      c[j] = e < a.E ? a.counts[(int64_t)s * a.E + e] : 0;
-      tot += c[j];
+    for (int u = 0; u < kRows; ++u) {
+      const int t = min(b + u * TPW + group, t1 - 1);
+      l[u] = load_row<BF16, VEC>(a, t, e0);
+      bool any = false;
+      for (int i = lane % LPT; i < a.K; i += LPT) {
+        const int id = a.ids[(int64_t)t * a.K + i];
+        any |= id >= 0 && id < a.E;
+      }
+      on[u] = any;
     }
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) tot += __shfl_xor(tot, o, 64);
-    const float scale = (float)((double)a.coef * (a.dloss ? (double)*a.dloss : 1.0) / ((double)a.S * a.tokens[s]));
-    float dot = 0.0f;
+    for (int u = 0; u < kRows; ++u) {
+      const int t = min(b + u * TPW + group, t1 - 1);
+      uint64_t hit = __ballot(on[u]);
+      if constexpr (LPT < 64) hit = (hit >> (lane & ~(LPT - 1))) & ((1ull << LPT) - 1);
+      if (__any(t >= s_end)) {
+        if (t >= s_end) {
+          s = seq_of(a, t);
+          s_end = s < a.S ? seq_at(a, s + 1) : a.T;
+        }
+        float c[4];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      f[j] = (float)a.E * (float)c[j] / (float)tot;
-      dot += f[j] * p[j];
+        for (int j = 0; j < 4; ++j) c[j] = e0 + j < a.E && s < a.S ? (float)a.counts[(int64_t)s * a.E + e0 + j] : 0.0f;
+        // a sequence holds at most 2^22 picks: the sum is exact in fp32
+        const float picks = group_sum<LPT>((c[0] + c[1]) + (c[2] + c[3]));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = (float)a.E * c[j] / picks;
+        scale = s < a.S ? (float)((double)a.coef * up / ((double)a.S * a.tokens[s])) : 0.0f;
+      }
+      float p[4], d[4], g[4];
+      shares<LPT, SIGMOID, true>(l[u], p, d);
+      const float dot = group_sum<LPT>((f[0] * p[0] + f[1] * p[1]) + (f[2] * p[2] + f[3] * p[3]));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] = hit != 0 && s < a.S ? scale * p[j] * (f[j] - dot) * d[j] : 0.0f;
+      if (b + u * TPW + group < t1) {
+        const int64_t i = (int64_t)t * a.E + e0;
+        if constexpr (VEC) {
+          if (e0 < a.E) {
+            if constexpr (BF16) {
+              typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+              *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.dlogits) + i) = bf16x4{(__bf16)g[0], (__bf16)g[1], (__bf16)g[2], (__bf16)g[3]};
+            } else {
+              *reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + i) = make_float4(g[0], g[1], g[2], g[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (e0 + j < a.E) {
+              if constexpr (BF16) static_cast<__bf16*>(a.dlogits)[i + j] = (__bf16)g[j];
+              else static_cast<float*>(a.dlogits)[i + j] = g[j];
+            }
+          }
+        }
+      }
     }
-    dot = wave_sum(dot);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) g[j] = scale * p[j] * (f[j] - dot) * d[j];
   }
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = lane + 64 * j;
-    if (e < a.E) {
-      if (a.bf16) static_cast<__bf16*>(a.dlogits)[(int64_t)t * a.E + e] = (__bf16)g[j];
-      else static_cast<float*>(a.dlogits)[(int64_t)t * a.E + e] = g[j];
-    }
-  }
+}
+
+// Calls f(LPT, SIGMOID, BF16, VEC) as integral constants.
+template <class F>
+void dispatch(const BalanceArgs& a, F&& f) {
+  auto with = [&](auto L) {
+    auto types = [&](auto S) {
+      const bool vec = a.E % 4 == 0;
+      if (a.bf16 && vec) f(L, S, std::true_type{}, std::true_type{});
+      else if (a.bf16) f(L, S, std::true_type{}, std::false_type{});
+      else if (vec) f(L, S, std::false_type{}, std::true_type{});
+      else f(L, S, std::false_type{}, std::false_type{});
+    };
+    if (a.sigmoid) types(std::true_type{});
+    else types(std::false_type{});
+  };
+  if (a.E <= 16) with(std::integral_constant<int, 4>{});
+  else if (a.E <= 32) with(std::integral_constant<int, 8>{});
+  else if (a.E <= 64) with(std::integral_constant<int, 16>{});
+  else if (a.E <= 128) with(std::integral_constant<int, 32>{});
+  else with(std::integral_constant<int, 64>{});
 }
 
 }  // namespace
 
-// At least 64 tokens a chunk, and at most 1024 chunks.
-int balance_chunk(int T) { return T <= 65536 ? 64 : (T + 1023) / 1024; }
+// 32 to 256 tokens a chunk, at most 1024 chunks where more than 32 are needed.
+int balance_chunk(int T) { return std::min(kMaxChunk, std::max(32, (T + 1023) / 1024)); }
+int balance_slices(int E) { return (E + kSliceE - 1) / kSliceE; }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
-  const int chunk = balance_chunk(a.T);
-  const int nc = (a.T + chunk - 1) / chunk;
-  // at least one workgroup: it clears the ticket
-  hipLaunchKernelGGL(balance_partial_kernel, dim3(nc > 0 ? nc : 1), dim3(256), 0, s, a, chunk);
+  const int chunk = balance_chunk(a.T), slices = balance_slices(a.E);
+  const int nc = std::max(1, (a.T + chunk - 1) / chunk);   // at least one workgroup: it clears the ticket
+  dispatch(a, [&](auto L, auto S, auto B, auto V) {
+    hipLaunchKernelGGL((balance_partial_kernel<decltype(L)::value, decltype(S)::value, decltype(B)::value, decltype(V)::value>),
+                       dim3(nc), dim3(256), 0, s, a, chunk);
+  });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(balance_reduce_kernel, dim3(a.S), dim3(256), 0, s, a, chunk);
+  hipLaunchKernelGGL(balance_reduce_kernel, dim3((unsigned)a.S * slices), dim3(256), 0, s, a, chunk, slices);
   return hipGetLastError();
 }
 
 hipError_t launch_balance_grad(const BalanceArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(balance_grad_kernel, dim3((a.T + 3) / 4), dim3(256), 0, s, a);
+  dispatch(a, [&](auto L, auto S, auto B, auto V) {
+    constexpr int step = 64 / decltype(L)::value * kRows;
+    // eight waves per SIMD where there are tokens for them
+    const int per = std::max(1, (a.T + 8191) / 8192 + step - 1) / step * step;
+    const int waves = (a.T + per - 1) / per;
+    hipLaunchKernelGGL((balance_grad_kernel<decltype(L)::value, decltype(S)::value, decltype(B)::value, decltype(V)::value>),
+                       dim3((waves + 3) / 4), dim3(256), 0, s, a, per);
+  });
   return hipGetLastError();
 }
 

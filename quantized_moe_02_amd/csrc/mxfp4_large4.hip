@@ -2,18 +2,22 @@
 //
 // A work item is up to 256 rows times 256 outputs on one workgroup of four
 // waves, one per SIMD with all 512 registers: 128 x 128 each (runs of up to 128
-// rows: 64 outputs x 128 rows each).  A scaled MFMA takes 16 cycles for 2 KB of
+// rows: 64 outputs x 128 rows each).  A scaled MFMA takes 32 cycles for 4 KB of
 // operands, so both sides come through LDS, where a wave tile of 128 x 128
 // costs the CU 64 KB of reads per 1024 cycles of MFMAs, half of what LDS
-// delivers; taken from global memory into registers, as the bf16 product takes
-// its weights, the operands would need more requests than the address units
-// answer.  128 inputs per stage, four stages by direct loads: block kb + 4 is
-// requested when every wave has block kb in registers; the operands of block
-// kb + 1 are read from LDS while block kb is multiplied.
+// delivers.
 //
-// Scales: 16 blocks of a row at a time.  A row's bytes may start anywhere, so
-// a thread loads the five aligned words around them, shifts them into place,
-// clears what lies past K and writes 16 bytes to LDS.
+// What bounds it is the vector cache, which keeps about 80 requests to L2 in
+// flight per CU, whatever their size: with 128 inputs (64 bytes) of a row per
+// stage, half a line per request, it delivered 17 bytes a cycle where the
+// MFMAs ask for 32.  So a stage holds 256 inputs, a whole line per row, and
+// LDS two stages.  Block kb + 1's operands for the first step are read, and
+// block kb + 2 is requested, once every wave has block kb's last step in
+// registers; the requests are spread over the following steps.
+//
+// Scales: 16 blocks of a row at a time.  Where a row's bytes may start
+// anywhere, a thread loads the five aligned words around them, shifts them into
+// place, clears what lies past K and writes 16 bytes to LDS.
 #include <algorithm>
 
 #include "mxfp4_tile.h"
@@ -22,61 +26,19 @@ namespace qmoe {
 namespace {
 
 constexpr int kThreads4 = 256;
-constexpr int kBlk4 = 128;    // inputs per stage
+constexpr int kBlk4 = 256;    // inputs per stage
 
-struct Lds4 {
-  uint8_t *a[4], *w[4];   // rows of 64 bytes, 16-byte chunk c of row r at c ^ (r / 4 mod 4)
-  uint8_t *as, *ws;       // scales: two groups of 16 bytes per row
-};
+// LDS: two stages of each side, rows of 128 bytes, 16-byte chunk c of row r at
+// c ^ (r / 2 mod 8); then two groups of scales of each side, 16 bytes per row.
+constexpr int kLdsA = 0, kLdsW = 65536, kLdsAs = 131072, kLdsWs = kLdsAs + 8192, kLds4 = kLdsWs + 8192;
+static_assert(4 * 128 * (256 + 16) <= kLds4, "the results fit");
 
-// A buffer descriptor as four words, for inline assembly.
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ i32x4 raw_rsrc(const void* base, uint32_t bytes) {
-  const uint64_t b = reinterpret_cast<uint64_t>(base);
-  return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
-               __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)),
-               __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
-}
-// 16 bytes per lane from buffer offset `off` into LDS at dst + 16 lane, past
-// the compiler's bookkeeping: it tells only a few such loads apart and waits
-// for all of them before LDS reads that it cannot prove apart, where this
-// pipeline counts its loads itself.  The load has no register result.
-__device__ __forceinline__ void to_lds16_raw(const i32x4& r, uint8_t* dst, uint32_t off) {
-  const uint32_t d = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)dst;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(__builtin_amdgcn_readfirstlane(d)), "v"(off), "s"(r) : "m0");
-}
-
-// 16 scale bytes of a row starting at byte `off` of a descriptor whose base is
-// 4-byte aligned.
-struct ScaleWords {
-  uint32_t w[5];
-  __device__ __forceinline__ void load(const rsrc_t& r, uint32_t off) {
-    uint32_t v[4];
-    bload16(v, r, off & ~3u, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = v[i];
-    w[4] = __builtin_amdgcn_raw_buffer_load_b32(r, (off & ~3u) + 16u, 0, 0);
-  }
-  // keeps the first `valid` bytes, the others 0
-  __device__ __forceinline__ uint4 bytes(uint32_t off, int valid) const {
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t x = __builtin_amdgcn_alignbyte(w[i + 1], w[i], off & 3u);
-      const int left = valid - 4 * i;
-      o[i] = left >= 4 ? x : left > 0 ? x & (0xffffffffu >> (32 - 8 * left)) : 0u;
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-  }
-};
-
-// SL: K % 128 == 0.  Every stage is full, and 16 scales of a row are aligned
+// SL: K % 256 == 0.  Every stage is full, and 16 scales of a row are aligned
 // words, which come by direct loads too.
 template <bool SL, int RT, int WT, int CT>
-__device__ __forceinline__ void tile4(const MatmulArgs& g, const FatItem& it, const Lds4& lds) {
-  constexpr int NA = 4, NV = 8;   // direct loads per thread and stage: rows, both
-  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
+__device__ __forceinline__ void tile4(const MatmulArgs& g, const FatItem& it, lds8_t* lds) {
+  constexpr int NA = 8, NV = 16;   // direct loads per thread and stage: rows, both
+  const int tid = threadIdx.x, lane = tid & 63, ln = lane & 31, lh = lane >> 5;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wv / WT, wt = wv % WT;
   const int nb = g.K / kMxBlock, nkb = (g.K + kBlk4 - 1) / kBlk4;
@@ -90,14 +52,14 @@ __device__ __forceinline__ void tile4(const MatmulArgs& g, const FatItem& it, co
   auto row_of = [&](int i) {   // row of `a` behind row i of the run, relative to the descriptor; -1: none
     return i < it.M ? (g.index ? source_row(g, it.r0 + i) : (int64_t)i) : (int64_t)-1;
   };
-  const int chunk = (tid & 3) ^ ((tid >> 4) & 3);   // this thread's chunk of a row, the same in each load
+  const int chunk = (tid & 7) ^ ((tid >> 4) & 7);   // this thread's chunk of a row, the same in each load
   uint32_t aoff[NA];
 #pragma unroll
   for (int i = 0; i < NA; ++i) {
-    const int64_t src = row_of(i * 64 + (tid >> 2));
+    const int64_t src = row_of(i * 32 + (tid >> 3));
     aoff[i] = src >= 0 ? (uint32_t)(src * ldb) + 16u * chunk : kOutside;
   }
-  const uint32_t woff = (uint32_t)(n0 + (tid >> 2)) * (uint32_t)ldb + 16u * chunk;
+  const uint32_t woff = (uint32_t)(n0 + (tid >> 3)) * (uint32_t)ldb + 16u * chunk;
 
   // scales: thread t carries row t of the weights' tile and row t of the run.
   // The descriptors start at the aligned word before the first byte and end
@@ -119,8 +81,8 @@ __device__ __forceinline__ void tile4(const MatmulArgs& g, const FatItem& it, co
   ScaleWords sw[2];
   auto issue_s = [&](int grp) {
     if constexpr (SL) {
-      to_lds16_raw(sr_raw[0], lds.ws + (grp & 1) * 4096 + wv * 1024, soff[0] + 16u * (uint32_t)grp);
-      to_lds16_raw(sr_raw[1], lds.as + (grp & 1) * 4096 + wv * 1024, soff[1] + 16u * (uint32_t)grp);
+      to_lds16_raw(sr_raw[0], lds_addr(lds) + kLdsWs + (grp & 1) * 4096 + wv * 1024, soff[0] + 16u * (uint32_t)grp);
+      to_lds16_raw(sr_raw[1], lds_addr(lds) + kLdsAs + (grp & 1) * 4096 + wv * 1024, soff[1] + 16u * (uint32_t)grp);
     } else {
 #pragma unroll
       for (int j = 0; j < 2; ++j) sw[j].load(sr[j], soff[j] + 16u * (uint32_t)grp);
@@ -129,118 +91,160 @@ __device__ __forceinline__ void tile4(const MatmulArgs& g, const FatItem& it, co
   auto write_s = [&](int grp) {
     if constexpr (SL) return;
     const int valid = nb - 16 * grp;
-    *reinterpret_cast<uint4*>(lds.ws + (grp & 1) * 4096 + tid * 16) = sw[0].bytes(soff[0], soff[0] < kOutside ? valid : 0);
-    *reinterpret_cast<uint4*>(lds.as + (grp & 1) * 4096 + tid * 16) = sw[1].bytes(soff[1], soff[1] < kOutside ? valid : 0);
+    *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(lds + kLdsWs + (grp & 1) * 4096 + tid * 16) = sw[0].bytes(soff[0], soff[0] < kOutside ? valid : 0);
+    *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(lds + kLdsAs + (grp & 1) * 4096 + tid * 16) = sw[1].bytes(soff[1], soff[1] < kOutside ? valid : 0);
   };
-  auto issue = [&](auto P, int kb, int i) {   // load i < NV of block kb
-    constexpr int p = decltype(P)::value;
-    const bool past = !SL && kb * 4 + chunk >= nb;
+  // load i < NV of block kb into the stage at byte p (0 or 32768) of each side
+  auto issue = [&](uint32_t p, int kb, int i) {
+    const bool past = !SL && kb * 8 + chunk >= nb;
     if (i < NA)
-      to_lds16_raw(ar, lds.a[p] + (i * 4 + wv) * 1024, past ? kOutside : aoff[i % NA] + (uint32_t)kb * 64u);
+      to_lds16_raw(ar, lds_addr(lds) + kLdsA + p + (i * 4 + wv) * 1024, past ? kOutside : aoff[i % NA] + (uint32_t)kb * 128u);
     else
-      to_lds16_raw(wr, lds.w[p] + ((i - NA) * 4 + wv) * 1024,
-                   past ? kOutside : woff + (uint32_t)(i - NA) * 64u * (uint32_t)ldb + (uint32_t)kb * 64u);
+      to_lds16_raw(wr, lds_addr(lds) + kLdsW + p + ((i - NA) * 4 + wv) * 1024,
+                   past ? kOutside : woff + (uint32_t)(i - NA) * 32u * (uint32_t)ldb + (uint32_t)kb * 128u);
   };
 
-  f32x4 acc[RT][CT];
+  f32x16 acc[RT][CT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-    for (int c = 0; c < CT; ++c) acc[rt][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[rt][c][i] = 0.0f;
 
-  uint4 W[2][RT], A[2][CT];
+  // operands of step t < 4 of a block, 64 inputs: chunk 2 t + lh of each row
+  u32x4 W[2][RT], A[2][CT];
   uint32_t ws[2][RT], as[2][CT];
-  const int at = lr * 64 + 16 * (lq ^ ((lr >> 2) & 3));
-  // part i < 8 of block kb's operands, from stage P into operand set P mod 2
-  auto read = [&](auto P, int kb, int i) {
-    constexpr int p = decltype(P)::value, s = p & 1;
-    const int grp = ((kb >> 2) & 1) * 4096 + (kb & 3) * 4 + lq + lr * 16;
+  // part i < 4 of the operands of step t of block kb, from the stage at p
+  auto read = [&](uint32_t p, auto T, int kb, int i) {
+    constexpr int t = decltype(T)::value, s = t & 1;
+    const int at = ln * 128 + 16 * ((2 * t + lh) ^ ((ln >> 1) & 7));
+    const int grp = ((kb >> 1) & 1) * 4096 + (kb & 1) * 8 + 2 * t + lh + ln * 16;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
-      if (rt % 8 == i) {
-        W[s][rt] = *reinterpret_cast<const uint4*>(lds.w[p] + (wn * RT + rt) * 1024 + at);
-        ws[s][rt] = lds.ws[grp + (wn * RT + rt) * 256];
+      if (rt == i) {
+        W[s][rt] = lds_read16(lds + kLdsW + p + (wn * RT + rt) * 4096 + at);
+        ws[s][rt] = lds[kLdsWs + grp + (wn * RT + rt) * 512];
       }
 #pragma unroll
     for (int c = 0; c < CT; ++c)
-      if (c % 8 == i) {
-        A[s][c] = *reinterpret_cast<const uint4*>(lds.a[p] + (wt * CT + c) * 1024 + at);
-        as[s][c] = lds.as[grp + (wt * CT + c) * 256];
+      if (c == i) {
+        A[s][c] = lds_read16(lds + kLdsA + p + (wt * CT + c) * 4096 + at);
+        as[s][c] = lds[kLdsAs + grp + (wt * CT + c) * 512];
       }
   };
-  auto block = [&](auto P, int kb) {
-    constexpr int p = decltype(P)::value, s = p & 1;
-    using N1 = std::integral_constant<int, (p + 1) % 4>;
-    // block kb is in this wave's registers and its loads of block kb + 1 are in
-    // LDS; past the barrier that holds for every wave
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(2 * NV));
+  auto handover = [&]() {
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(0));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    const int grp = (kb >> 2) + 1;
-    if (p == 0) issue_s(grp);
-    if (p == 2) write_s(grp);
-    // in eight parts: one request, an eighth of the reads, an eighth of the MFMAs
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      issue(P, min(kb + 4, nkb - 1), i);   // past the end: never read
-      read(N1{}, kb + 1, i);
-#pragma unroll
-      for (int j = 0; j < RT * CT; ++j)
-        if (j * 8 / (RT * CT) == i) {
-          const int c = j / RT, rt = j % RT;
-          const i32x8 wv8 = {(int)W[s][rt].x, (int)W[s][rt].y, (int)W[s][rt].z, (int)W[s][rt].w, 0, 0, 0, 0};
-          const i32x8 av8 = {(int)A[s][c].x, (int)A[s][c].y, (int)A[s][c].z, (int)A[s][c].w, 0, 0, 0, 0};
-          acc[rt][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv8, av8, acc[rt][c], 4, 4, 0, (int)ws[s][rt], 0, (int)as[s][c]);
+  };
+  // Step t of block kb: in four parts, requests, the next step's reads (first)
+  // and MFMAs.  Requests: half of block kb + 2 in step 3, into the stage that
+  // its barrier freed, the other half of block kb + 1 in step 0, which leaves
+  // two steps for the last of them to land.
+  using I0 = std::integral_constant<int, 0>;
+  auto block = [&](int kb) {
+    const uint32_t p = (uint32_t)(kb & 1) * 32768u, q = p ^ 32768u;
+    const int k1 = min(kb + 1, nkb - 1), k2 = min(kb + 2, nkb - 1);   // past the end: never read
+    const int grp = (kb >> 1) + 1;
+    static_for<4>([&](auto T) {
+      constexpr int t = decltype(T)::value, s = t & 1;
+      if constexpr (t == 3) handover();   // block kb is read, block kb + 1 has landed, in every wave
+      if (t == 0 && (kb & 1) == 0) issue_s(grp);
+      if (t == 2 && (kb & 1) == 0) write_s(grp);
+      static_for<4>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        if constexpr (t == 3) {
+          issue(p, k2, 2 * i);
+          issue(p, k2, 2 * i + 1);
+        } else if constexpr (t == 0) {
+          issue(q, k1, 8 + 2 * i);
+          issue(q, k1, 9 + 2 * i);
         }
-      __builtin_amdgcn_sched_barrier(0);
-    }
+        if constexpr (i < 2) {
+#pragma unroll
+          for (int j = 2 * i; j < 2 * i + 2; ++j) {
+            if constexpr (t == 3) read(q, I0{}, kb + 1, j);
+            else read(p, std::integral_constant<int, t + 1>{}, kb, j);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < RT * CT; ++j)
+          if (j * 4 / (RT * CT) == i) {
+            const int c = j / RT, rt = j % RT;
+            const u32x4 w = W[s][rt], x = A[s][c];
+            const i32x8 wv8 = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+            const i32x8 xv8 = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
+            acc[rt][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv8, xv8, acc[rt][c], 4, 4, 0, (int)ws[s][rt], 0, (int)as[s][c]);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
   };
   issue_s(0);
-  static_for<4>([&](auto J) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) issue(J, min(decltype(J)::value, nkb - 1), i);
-  });
+  for (int i = 0; i < NV; ++i) issue(0u, 0, i);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) issue(32768u, min(1, nkb - 1), i);
   write_s(0);
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(3 * NV));
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(8));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) read(std::integral_constant<int, 0>{}, 0, i);
-  for (int kb = 0; kb < nkb; kb += 4)
-    static_for<4>([&](auto J) {
-      if (kb + decltype(J)::value < nkb) block(J, kb + decltype(J)::value);
-    });
-  __builtin_amdgcn_s_waitcnt(0);   // the loads past the end
-
-  const bool vec = g.ldo % 4 == 0;
+  for (int i = 0; i < 4; ++i) read(0u, I0{}, 0, i);
+  for (int kb = 0; kb < nkb; ++kb) block(kb);
+  // every wave's reads and loads are done: LDS takes the results
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  lds8_t* t = lds + wv * (CT * 32 * (RT * 64 + 16));
+  const int row0 = it.r0 + wt * CT * 32, rows = min(it.M - wt * CT * 32, CT * 32);
+  if (g.out_bf16) {
+    constexpr int RB = RT * 64;
 #pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    const int row = (wt * CT + c) * 16 + lr;
-    if (row >= it.M) continue;
+    for (int c = 0; c < CT; ++c)
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) store4(g, vec, it.r0 + row, n0 + (wn * RT + rt) * 16 + 4 * lq, acc[rt][c]);
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<__attribute__((address_space(3))) u32x2*>(t + (c * 32 + ln) * (RB + 16) + rt * 64 + 16 * q + 8 * lh) =
+              u32x2{pack_bf16(acc[rt][c][4 * q], acc[rt][c][4 * q + 1]), pack_bf16(acc[rt][c][4 * q + 2], acc[rt][c][4 * q + 3])};
+    store_rows<RB>(g, t, rows, row0, n0 + wn * RT * 32, g.N);
+  } else {
+    // half of the outputs at a time
+    constexpr int RB = RT * 64;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int rt = 0; rt < RT / 2; ++rt)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16& v = acc[h * (RT / 2) + rt][c];
+            *reinterpret_cast<__attribute__((address_space(3))) f32x4*>(t + (c * 32 + ln) * (RB + 16) + rt * 128 + 32 * q + 16 * lh) =
+                f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+          }
+      store_rows<RB>(g, t, rows, row0, n0 + wn * RT * 32 + h * (RT / 2) * 32, g.N);
+    }
   }
 }
 
 template <bool SL>
 __global__ void __launch_bounds__(kThreads4, 1) mx_matmul4_kernel(MatmulArgs g, int nt) {
-  __shared__ __attribute__((aligned(16))) uint8_t a0[16384], a1[16384], a2[16384], a3[16384];
-  __shared__ __attribute__((aligned(16))) uint8_t w0[16384], w1[16384], w2[16384], w3[16384];
-  __shared__ __attribute__((aligned(16))) uint8_t as[8192], ws[8192];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kLds4];
   FatItem it;
   if (!find_item(g.offsets, g.E, g.R, nt, nt, it)) return;
-  const Lds4 lds{{a0, a1, a2, a3}, {w0, w1, w2, w3}, as, ws};
+  lds8_t* lds = (lds8_t*)smem;
   if (it.wide) {
-    if (it.M > 192) tile4<SL, 8, 2, 8>(g, it, lds);
-    else tile4<SL, 8, 2, 6>(g, it, lds);
+    if (it.M > 192) tile4<SL, 4, 2, 4>(g, it, lds);
+    else tile4<SL, 4, 2, 3>(g, it, lds);
   } else {
-    if (it.M > 96) tile4<SL, 4, 1, 8>(g, it, lds);
-    else if (it.M > 64) tile4<SL, 4, 1, 6>(g, it, lds);
-    else if (it.M > 32) tile4<SL, 4, 1, 4>(g, it, lds);
-    else if (it.M > 16) tile4<SL, 4, 1, 2>(g, it, lds);
-    else tile4<SL, 4, 1, 1>(g, it, lds);
+    if (it.M > 96) tile4<SL, 2, 1, 4>(g, it, lds);
+    else if (it.M > 64) tile4<SL, 2, 1, 3>(g, it, lds);
+    else if (it.M > 32) tile4<SL, 2, 1, 2>(g, it, lds);
+    else tile4<SL, 2, 1, 1>(g, it, lds);
   }
 }
 

@@ -97,7 +97,7 @@ hipError_t launch_mx_matmul(const MatmulArgs& g, bool a_mxfp4, hipStream_t s) {
   const int64_t ldb = a_mxfp4 ? g.K / 2 : g.lda * 2;
   const int64_t span = (g.index ? (int64_t)g.a_rows : kFatRows) * ldb;
   if (g.R >= 8 * (int64_t)g.E && (int64_t)g.R * g.N >= 64 * 256 * 256 && span < (int64_t)kOutside)
-    return a_mxfp4 ? launch_mx_matmul4_large(g, s) : launch_mx_matmul_large(g, a_mxfp4, s);
+    return a_mxfp4 ? launch_mx_matmul4_large(g, s) : launch_mx_matmul_large(g, s);
   const int nt = (g.N + 63) / 64;
   const dim3 grid((unsigned)(max_units(g, 16) * nt));
   if (a_mxfp4) hipLaunchKernelGGL(mx_matmul_kernel<true>, grid, dim3(256), 0, s, g, nt);

@@ -1,12 +1,18 @@
 // Device helpers of the MXFP4 products: runs of rows, work items, operands and
 // stores.
 //
-// MFMA operands (a wave of 64, lane = 16 lq + lr): of a 16 x 16 tile, lane
-// (lr, lq) feeds row lr of A and column lr of B with the same inputs, any
-// assignment of inputs to (step, lq, element) being valid as long as A and B
-// share it, and holds rows 4 lq .. 4 lq + 3 of column lr of the result.  A is
-// the weights (rows: output features) and B the rows of `a`, so a lane ends up
-// with four consecutive outputs of one row.
+// MFMA operands: of a 16 x 16 tile, lane 16 lq + lr feeds row lr of A and
+// column lr of B with the same inputs, any assignment of inputs to (step, lq,
+// element) being valid as long as A and B share it, and holds rows 4 lq ..
+// 4 lq + 3 of column lr of the result; of a 32 x 32 tile, lane 32 lh + ln row
+// and column ln, and rows 8 q + 4 lh .. + 3 of column ln.  A is the weights
+// (rows: output features) and B the rows of `a`, so a lane ends up with four
+// consecutive outputs of one row.
+//
+// One wave alone issues the 32 x 32 shapes at the matrix units' rate, but the
+// 16 x 16 ones at 60% of it; two waves of a SIMD reach it with either
+// (measured, registers only: bf16 2.30 / 1.46 and 2.37 / 2.35 PFLOP/s, MXFP4
+// 8.3 / 4.8 and 8.5 / 7.9).
 #pragma once
 
 #include "operators_internal.h"
@@ -16,6 +22,7 @@ namespace qmoe {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 struct RowUnit {
   int e, r0, M;   // expert, first row, rows (0: no such unit)
@@ -157,24 +164,88 @@ __device__ __forceinline__ void to_lds16(const rsrc_t& r, uint8_t* dst, uint32_t
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, off, 0, 0, 0);
 }
 
-// Stores four consecutive outputs of one row (col % 4 == 0).
-__device__ __forceinline__ void store4(const MatmulArgs& g, bool vec, int row, int col, const f32x4& v) {
-  const int64_t i = (int64_t)row * g.ldo + col;
-  if (vec && col + 4 <= g.N) {
-    if (g.out_bf16) {
-      typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-      bf16x4 o = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-      *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(g.out) + i) = o;
-    } else {
-      *reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + i) = v;
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (col + j < g.N) store_out(g, row, col + j, v[j]);
+// A buffer descriptor as four words, for inline assembly.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i32x4 raw_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
+               __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)),
+               __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+// 16 bytes per lane from buffer offset `off` into LDS address dst + 16 lane, past
+// the compiler's bookkeeping: it tells only a few such loads apart and waits
+// for all of them before LDS reads that it cannot prove apart, where this
+// pipeline counts its loads itself.  The load has no register result.
+__device__ __forceinline__ void to_lds16_raw(const i32x4& r, uint32_t dst, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(__builtin_amdgcn_readfirstlane(dst)), "v"(off), "s"(r) : "m0");
+}
+// LDS by 32-bit address.
+typedef __attribute__((address_space(3))) uint8_t lds8_t;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint32_t lds_addr(const lds8_t* p) { return (uint32_t)(uintptr_t)p; }
+__device__ __forceinline__ u32x4 lds_read16(const lds8_t* p) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(p);
 }
 
+// 16 scale bytes of a row starting at byte `off` of a descriptor whose base is
+// 4-byte aligned.
+struct ScaleWords {
+  uint32_t w[5];
+  __device__ __forceinline__ void load(const rsrc_t& r, uint32_t off) {
+    uint32_t v[4];
+    bload16(v, r, off & ~3u, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = v[i];
+    w[4] = __builtin_amdgcn_raw_buffer_load_b32(r, (off & ~3u) + 16u, 0, 0);
+  }
+  // keeps the first `valid` bytes, the others 0
+  __device__ __forceinline__ u32x4 bytes(uint32_t off, int valid) const {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = __builtin_amdgcn_alignbyte(w[i + 1], w[i], off & 3u);
+      const int left = valid - 4 * i;
+      o[i] = left >= 4 ? x : left > 0 ? x & (0xffffffffu >> (32 - 8 * left)) : 0u;
+    }
+    return u32x4{o[0], o[1], o[2], o[3]};
+  }
+};
+
+// Results leave through LDS: the lanes of a store from the accumulators hold 4
+// outputs of as many rows, 16-byte requests, where the vector cache takes a
+// line in one.  A wave lays its rows out at RB + 16 bytes each (rows 16 apart
+// in the bank row, so that neither side of the exchange has conflicts) and
+// writes them out RB bytes at a time.  `out_cols` bounds the columns.
+template <int RB>
+__device__ __forceinline__ void store_rows(const MatmulArgs& g, const lds8_t* t, int rows, int row0, int col0, int out_cols) {
+  constexpr int LPR = RB / 16, RPI = 64 / LPR;   // lanes per row, rows per instruction
+  const int lane = threadIdx.x & 63, c = lane % LPR;
+  const int es = g.out_bf16 ? 2 : 4, per = 16 / es;
+  const int col = col0 + c * per;
+  const bool vec = g.ldo % per == 0 && col + per <= out_cols;
+  uint8_t* o = static_cast<uint8_t*>(g.out) + ((int64_t)row0 * g.ldo + col) * es;
+  for (int r = lane / LPR; r < rows; r += RPI) {
+    const u32x4 v = lds_read16(t + r * (RB + 16) + c * 16);
+    uint8_t* p = o + (int64_t)r * g.ldo * es;
+    if (vec) {
+      *reinterpret_cast<u32x4*>(p) = v;
+    } else if (g.out_bf16) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col + j < out_cols) reinterpret_cast<uint16_t*>(p)[j] = (uint16_t)(v[j / 2] >> (16 * (j & 1)));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (col + j < out_cols) reinterpret_cast<uint32_t*>(p)[j] = v[j];
+    }
+  }
+}
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const bf16x2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
 
 // s_waitcnt immediate: all but the n most recent vector memory ops, and every
 // LDS read (gfx9 encoding: vmcnt in bits 3-0 and 15-14, lgkmcnt in 11-8).

@@ -32,7 +32,7 @@ struct MatmulArgs {
   bool out_bf16;
 };
 hipError_t launch_mx_matmul(const MatmulArgs& a, bool a_mxfp4, hipStream_t s);
-hipError_t launch_mx_matmul_large(const MatmulArgs& a, bool a_mxfp4, hipStream_t s);
+hipError_t launch_mx_matmul_large(const MatmulArgs& a, hipStream_t s);
 hipError_t launch_mx_matmul4_large(const MatmulArgs& a, hipStream_t s);
 hipError_t launch_mx_matmul_dx_large(const MatmulArgs& a, hipStream_t s);
 hipError_t launch_mx_matmul_dx(const MatmulArgs& a, hipStream_t s);
@@ -51,7 +51,8 @@ struct BalanceArgs {
   float coef;
   // workspace of the forward pass
   uint32_t* ticket;         // [1]
-  double* seq_loss;         // [S]
+  double* seq_loss;         // [S][slices]
+  int32_t* seq_picks;       // [S][slices]
   float* part_p;            // [slots][E]
   int32_t* part_c;          // [slots][E]
   int32_t* part_n;          // [slots]
@@ -59,6 +60,8 @@ struct BalanceArgs {
 // Token chunks of the forward pass: one partial sum per (chunk, sequence)
 // pair that share a token, at slot chunk + sequence.
 int balance_chunk(int T);
+// Workgroups per sequence of its second launch.
+int balance_slices(int E);
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);
 hipError_t launch_balance_grad(const BalanceArgs& a, hipStream_t s);
 
