@@ -3,15 +3,15 @@
 // One workgroup of eight waves per CU; a work item is up to 256 rows of one
 // expert times 256 outputs (waves 4 x 2), or up to 128 rows times 512 outputs
 // (8 x 1): either way a wave holds 64 outputs x 128 rows in its accumulators,
-// and 128 inputs cost the CU 256 KB of LDS reads for 8192 cycles of MFMAs per
-// pair of waves.  The weights go from global memory straight into registers
-// and become bf16 there, four conversions per eight codes, in the shadow of
-// the MFMAs; the rows of `a` go through LDS by direct loads.  128 inputs per
-// stage, two stages: a K block's MFMAs take longer than the next block's loads.
+// and 128 inputs cost the CU 256 KB of LDS reads for 4096 cycles of MFMAs on
+// every SIMD.  The weights go from global memory straight into registers and
+// become bf16 there, four conversions per eight codes, between the MFMAs; the
+// rows of `a` go through LDS by direct loads.  128 inputs per stage, two
+// stages: a K block's MFMAs take longer than the next block's loads.
 //
-// The hand-over between stages comes before a block's last step, whose
-// operands are in registers by then, so that the first reads of the next block
-// and its first conversion run beside those MFMAs.
+// The next block's requests are spread over the first half of a block: issued
+// at once they stall every wave until the address units have taken them all
+// (1.94 against 1.59 ms for gate and up of 256 experts over 4096 tokens).
 #include <algorithm>
 
 #include "mxfp4_tile.h"
@@ -22,27 +22,30 @@ namespace {
 constexpr int kBlk = 128;                        // inputs per stage
 constexpr int kStage = kFatRows * kBlk * 2;      // 64 KB
 
-// LDS: two stages, rows of 256 bytes, 16-byte chunk c of row r at c ^ (r mod
-// 16); then two groups of weight scales, 16 bytes per output.
-constexpr int kLdsS = 2 * kStage, kLds = kLdsS + 2 * 512 * 16;
-static_assert(8 * 128 * (128 + 16) <= kLds, "the results fit");
+struct LdsL {
+  uint8_t *st0, *st1;   // stages: rows of 256 bytes, 16-byte chunk c of row r at c ^ (r mod 16)
+  uint8_t* ws;          // weight scales: two groups of 16 bytes per output
+};
+// the results take the place of the stages, four waves in each, half of a wave's rows at a time
+static_assert(4 * 64 * (128 + 16) <= kStage, "half of the results fits");
 
-// SL: K % 128 == 0.  Every stage is full, and 16 scales of an output are
-// aligned words, which come into LDS by direct loads; otherwise they pass
-// through registers, which shift them into place.
+// SL: the scales of 16 blocks of an output are 16 aligned bytes (K % 128 ==
+// 0), which come into LDS one group ahead: a scale byte per lane costs the
+// address units as much as 16 bytes of codes.  Otherwise lanes load bytes.
 template <bool SL, int WT, int CT>
-__device__ __forceinline__ void large_tile(const MatmulArgs& g, const FatItem& it, lds8_t* lds) {
-  constexpr int WN = 8 / WT, RT = 2, ROWS = 32 * CT * WT, NA = ROWS * 16 / kFatThreads;
-  const int tid = threadIdx.x, lane = tid & 63, ln = lane & 31, lh = lane >> 5;
+__device__ __forceinline__ void large_tile(const MatmulArgs& g, const FatItem& it, const LdsL& lds) {
+  constexpr int WN = 8 / WT, RT = 4, ROWS = 16 * CT * WT;
+  constexpr int SLOTS = ROWS * 16, NA = (SLOTS + kFatThreads - 1) / kFatThreads;
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wv % WN, wt = wv / WN;
   const int n0 = it.tile * (64 * WN);
   const int nb = g.K / kMxBlock, nkb = (g.K + kBlk - 1) / kBlk;
 
-  // rows of `a`: load i brings row i * 32 + tid / 16, this thread always the same chunk of it
-  const int64_t ldb = g.lda * 2;
-  const i32x4 ar = raw_rsrc(static_cast<const uint8_t*>(g.a) + (g.index ? 0 : (int64_t)it.r0 * ldb), kOutside);
+  // load i brings rows 32 i + tid / 16, this thread always the same chunk of its row
   const int chunk = (tid & 15) ^ ((tid >> 4) & 15);
+  const int64_t ldb = g.lda * 2;
+  const rsrc_t ar = make_rsrc(static_cast<const uint8_t*>(g.a) + (g.index ? 0 : (int64_t)it.r0 * ldb), kOutside);
   uint32_t aoff[NA];
 #pragma unroll
   for (int i = 0; i < NA; ++i) {
@@ -50,176 +53,163 @@ __device__ __forceinline__ void large_tile(const MatmulArgs& g, const FatItem& i
     const int64_t src = row < it.M ? (g.index ? source_row(g, it.r0 + row) : (int64_t)row) : (int64_t)-1;
     aoff[i] = src >= 0 ? (uint32_t)(src * ldb) + 16u * chunk : kOutside;
   }
-  // weights: rows past N lie past the descriptors
+  // weights: lane (lr, lq) takes block lq of row lr; rows past N lie past the descriptors
   const int64_t erow = (int64_t)it.e * g.N;
-  const rsrc_t wr = make_rsrc(g.w_codes + erow * (g.K / 2), (uint32_t)g.N * (uint32_t)(g.K / 2));
-  const uint32_t woff = (uint32_t)(n0 + wn * 64 + ln) * (uint32_t)(g.K / 2) + 16u * lh;
-  // scales: thread t < 64 WN carries those of output n0 + t
-  const uint8_t* sbase = g.w_scale + erow * nb;
-  const uint32_t mis = (uint32_t)(reinterpret_cast<uintptr_t>(sbase) & 3);
-  const i32x4 sr_raw = raw_rsrc(sbase - mis, ((uint32_t)g.N * (uint32_t)nb + mis + 3u) & ~3u);
-  const rsrc_t sr = make_rsrc(sbase - mis, ((uint32_t)g.N * (uint32_t)nb + mis + 3u) & ~3u);
-  const uint32_t soff = n0 + tid < g.N ? mis + (uint32_t)(n0 + tid) * (uint32_t)nb : kOutside;
+  const uint32_t wld = (uint32_t)(g.K / 2);
+  const rsrc_t wr = make_rsrc(g.w_codes + erow * wld, (uint32_t)g.N * wld);
+  const uint32_t woff = (uint32_t)(n0 + wn * 64 + lr) * wld + 16u * lq;
+  const rsrc_t sr = make_rsrc(g.w_scale + erow * nb, (uint32_t)g.N * (uint32_t)nb);
+  const uint32_t soff = (uint32_t)(n0 + wn * 64 + (SL ? lane : lr)) * (uint32_t)nb + (SL ? 0u : (uint32_t)lq);
 
-  ScaleWords sw;
-  auto issue_s = [&](int grp) {
-    if (wv >= WN) return;
-    if constexpr (SL) to_lds16_raw(sr_raw, lds_addr(lds) + kLdsS + (grp & 1) * 8192 + wv * 1024, soff + 16u * (uint32_t)grp);
-    else sw.load(sr, soff + 16u * (uint32_t)grp);
-  };
-  auto write_s = [&](int grp) {
-    if constexpr (!SL) {
-      if (wv < WN)
-        *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(lds + kLdsS + (grp & 1) * 8192 + tid * 16) =
-            sw.bytes(soff, soff < kOutside ? nb - 16 * grp : 0);
-    }
-  };
-  uint32_t wq[2][RT][2][4];   // chunk 2 c + lh of the block, c = 0, 1
-  uint32_t sc[2][RT][2];
+  uint32_t wq[2][RT][4], wsc[2][RT];
   auto issue_a = [&](auto P, int kb, int i) {
-    constexpr int p = decltype(P)::value;
+    if (i * kFatThreads + wv * 64 >= SLOTS) return;
     const bool past = !SL && kb * kBlk + chunk * 8 >= g.K;
-    to_lds16_raw(ar, lds_addr(lds) + p * kStage + (i * kFatThreads + wv * 64) * 16,
+    to_lds16(ar, (decltype(P)::value ? lds.st1 : lds.st0) + (i * kFatThreads + wv * 64) * 16,
              past ? kOutside : aoff[i] + (uint32_t)kb * (kBlk * 2));
   };
-  auto issue_w = [&](auto P, int kb, int i) {   // i < 4
+  auto issue_w = [&](auto P, int kb, int rt) {
     constexpr int p = decltype(P)::value;
-    bload16(wq[p][i >> 1][i & 1], wr, woff + (uint32_t)(i >> 1) * 32u * (uint32_t)(g.K / 2) + (uint32_t)kb * 64u + 32u * (i & 1), 0);
+    bload16(wq[p][rt], wr, woff + (uint32_t)rt * 16u * wld + (uint32_t)kb * 64u, 0);
+    // blocks past K: the next row's scales, which may be NaN, times zeros
+    if constexpr (!SL)
+      wsc[p][rt] = __builtin_amdgcn_raw_buffer_load_b8(
+          sr, kb * 4 + lq < nb ? soff + (uint32_t)rt * 16u * (uint32_t)nb + (uint32_t)kb * 4u : kOutside, 0, 0);
+  };
+  auto issue_s = [&](int kb) {   // the scales of block kb's group, if it starts one
+    if constexpr (SL) {
+      if (wt == 0 && (kb & 3) == 0)
+        to_lds16(sr, lds.ws + ((kb >> 2) & 1) * 8192 + wn * 1024, soff + (uint32_t)kb * 4u);
+    }
   };
   auto read_s = [&](auto P, int kb) {
-    constexpr int p = decltype(P)::value;
-    const lds8_t* b = lds + kLdsS + ((kb >> 2) & 1) * 8192 + (wn * 64 + ln) * 16 + (kb & 3) * 4 + lh;
+    if constexpr (SL) {
+      const uint8_t* b = lds.ws + ((kb >> 2) & 1) * 8192 + (wn * 64 + lr) * 16 + (kb & 3) * 4 + lq;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sc[p][i >> 1][i & 1] = b[(i >> 1) * 512 + 2 * (i & 1)];
+      for (int rt = 0; rt < RT; ++rt) wsc[decltype(P)::value][rt] = b[rt * 256];
+    }
   };
 
-  f32x16 acc[RT][CT];
+  f32x4 acc[RT][CT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[rt][c][i] = 0.0f;
+    for (int c = 0; c < CT; ++c) acc[rt][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // step j < 8 of a block: word j % 4 of chunk 2 (j / 4) + lh, eight inputs a lane
-  bf16x8 A[2][RT], B[2][CT];
-  auto read_b = [&](auto P, int j) {
-    const lds8_t* st = lds + decltype(P)::value * kStage;
-    const int c = (2 * (j >> 2) + lh) * 4 + (j & 3);
-#pragma unroll
-    for (int t = 0; t < CT; ++t)
-      B[j & 1][t] = __builtin_bit_cast(bf16x8, lds_read16(st + ((wt * CT + t) * 32 + ln) * 256 + 16 * (c ^ (ln & 15))));
-  };
-  auto convert = [&](auto P, int j) {
-    constexpr int p = decltype(P)::value;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-      A[j & 1][rt] = bf16_of(wq[p][rt][j >> 2][j & 3], __uint_as_float(sc[p][rt][j >> 2] << 23));
-  };
+  // Sub-step j of a block: HB column tiles, from HB (j % SUB) on, of step j /
+  // SUB, which takes word j / SUB of every lane's 32 inputs.
+  constexpr int HB = CT < 2 ? 1 : 2, SUB = CT / HB, NSUB = 4 * SUB, IS = NSUB / 2;
   auto block = [&](auto P, int kb) {
     constexpr int p = decltype(P)::value;
     using Q = std::integral_constant<int, 1 - p>;
-    const int kn = min(kb + 1, nkb - 1);   // past the end: the last block again, never used
-    const int grp = (kb >> 2) + 1;
-    if ((kb & 3) == 0) issue_s(grp);
-    if ((kb & 3) == 2) write_s(grp);
-    static_for<8>([&](auto J) {
-      constexpr int j = decltype(J)::value;
-      if constexpr (j < 7) {
-        read_b(P, j + 1);
-      } else {
-        // this wave has read block kb and its loads of block kb + 1 have
-        // landed; past the barrier both hold for every wave
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(0));
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-        read_s(Q{}, kb + 1);
-        read_b(Q{}, 0);
-      }
-      if constexpr (j < 4) {
+    const uint8_t* st = p ? lds.st1 : lds.st0;
+    // block kb has landed, in every wave; nobody reads the other stage any more
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    read_s(P, kb);
+    __builtin_amdgcn_sched_barrier(0);
+    const int kn = min(kb + 1, nkb - 1);   // the last block is requested twice: no branch
+    bf16x8 A[RT];
+    uint4 B[2][HB];
+    auto read_b = [&](int j) {
+#pragma unroll
+      for (int c = 0; c < HB; ++c)
+        B[j & 1][c] = *reinterpret_cast<const uint4*>(st + ((wt * CT + HB * (j % SUB) + c) * 16 + lr) * 256 + 16 * ((4 * lq + j / SUB) ^ lr));
+    };
+    read_b(0);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) A[rt] = bf16_of(wq[p][rt][0], __uint_as_float(wsc[p][rt] << 23));
+#pragma unroll
+    for (int j = 0; j < NSUB; ++j) {
+      const int s = j / SUB;
+      if (j + 1 < NSUB) read_b(j + 1);
+      if (j < IS) {
 #pragma unroll
         for (int i = 0; i < NA; ++i)
-          if (i % 4 == j) issue_a(Q{}, kn, i);
-        issue_w(Q{}, kn, j);
-      }
-      if constexpr (j < 7) convert(P, j + 1);
-#pragma unroll
-      for (int t = 0; t < CT; ++t)
+          if (i % IS == j) issue_a(Q{}, kn, i);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
-          acc[rt][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(A[j & 1][rt], B[j & 1][t], acc[rt][t], 0, 0, 0);
-      if constexpr (j == 7) convert(Q{}, 0);
+          if (rt % IS == j) issue_w(Q{}, kn, rt);
+        if (j == 0) issue_s(kn);
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+        for (int c = 0; c < HB; ++c) {
+          const int ct = HB * (j % SUB) + c;
+          acc[rt][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[rt], __builtin_bit_cast(bf16x8, B[j & 1][c]), acc[rt][ct], 0, 0, 0);
+        }
+        // the next step's operand, in the registers that these MFMAs are done with
+        if (j % SUB == SUB - 1 && s < 3) A[rt] = bf16_of(wq[p][rt][s + 1], __uint_as_float(wsc[p][rt] << 23));
+      }
+      // the next reads first, then the next codes' conversion between the MFMAs
+      __builtin_amdgcn_sched_group_barrier(0x100, HB, 0);
+#pragma unroll
+      for (int i = 0; i < HB * RT; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
+      }
       __builtin_amdgcn_sched_barrier(0);
-    });
+    }
   };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
   issue_s(0);
 #pragma unroll
-  for (int i = 0; i < NA; ++i) issue_a(std::integral_constant<int, 0>{}, 0, i);
+  for (int i = 0; i < NA; ++i) issue_a(I0{}, 0, i);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) issue_w(std::integral_constant<int, 0>{}, 0, i);
-  write_s(0);
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lds(0));
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  read_s(std::integral_constant<int, 0>{}, 0);
-  read_b(std::integral_constant<int, 0>{}, 0);
-  convert(std::integral_constant<int, 0>{}, 0);
+  for (int rt = 0; rt < RT; ++rt) issue_w(I0{}, 0, rt);
   for (int kb = 0; kb < nkb; kb += 2) {
-    block(std::integral_constant<int, 0>{}, kb);
-    if (kb + 1 < nkb) block(std::integral_constant<int, 1>{}, kb + 1);
+    block(I0{}, kb);
+    if (kb + 1 < nkb) block(I1{}, kb + 1);
   }
 
   // every wave's reads and loads are done: LDS takes the results
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  lds8_t* t = lds + wv * (CT * 32 * (RT * 64 + 16));
-  const int row0 = it.r0 + wt * CT * 32, rows = min(it.M - wt * CT * 32, CT * 32);
-  if (g.out_bf16) {
-    constexpr int RB = RT * 64;
+  lds8_t* t = (lds8_t*)(wv < 4 ? lds.st0 : lds.st1) + (wv & 3) * (64 * 144);
+  constexpr int HC = (CT + 1) / 2;   // column tiles at a time
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
+  for (int c0 = 0; c0 < CT; c0 += HC) {
+    const int row0 = (wt * CT + c0) * 16, rows = min(it.M - row0, HC * 16);
+    if (g.out_bf16) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+      for (int c = 0; c < HC; ++c)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<__attribute__((address_space(3))) u32x2*>(t + (c * 32 + ln) * (RB + 16) + rt * 64 + 16 * q + 8 * lh) =
-              u32x2{pack_bf16(acc[rt][c][4 * q], acc[rt][c][4 * q + 1]), pack_bf16(acc[rt][c][4 * q + 2], acc[rt][c][4 * q + 3])};
-    store_rows<RB>(g, t, rows, row0, n0 + wn * 64, g.N);
-  } else {
-    // half of the outputs at a time
-    constexpr int RB = RT * 64;
+        for (int rt = 0; rt < RT; ++rt)
+          if (c0 + c < CT)
+            lds_write8(t + (c * 16 + lr) * 144 + rt * 32 + lq * 8,
+                       u32x2{pack_bf16(acc[rt][c0 + c][0], acc[rt][c0 + c][1]), pack_bf16(acc[rt][c0 + c][2], acc[rt][c0 + c][3])});
+      store_rows<128>(g, t, rows, it.r0 + row0, n0 + wn * 64, g.N);
+    } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 2; ++h) {   // half of the outputs
 #pragma unroll
-      for (int c = 0; c < CT; ++c)
+        for (int c = 0; c < HC; ++c)
 #pragma unroll
-        for (int rt = 0; rt < RT / 2; ++rt)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f32x16& v = acc[h * (RT / 2) + rt][c];
-            *reinterpret_cast<__attribute__((address_space(3))) f32x4*>(t + (c * 32 + ln) * (RB + 16) + rt * 128 + 32 * q + 16 * lh) =
-                f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-          }
-      store_rows<RB>(g, t, rows, row0, n0 + wn * 64 + h * (RT / 2) * 32, g.N);
+          for (int rt = 0; rt < 2; ++rt)
+            if (c0 + c < CT) lds_write16(t + (c * 16 + lr) * 144 + rt * 64 + lq * 16, __builtin_bit_cast(u32x4, acc[2 * h + rt][c0 + c]));
+        store_rows<128>(g, t, rows, it.r0 + row0, n0 + wn * 64 + h * 32, g.N);
+      }
     }
   }
 }
 
 template <bool SL>
 __global__ void __launch_bounds__(kFatThreads, 2) mx_matmul_large_kernel(MatmulArgs g, int ntw, int ntn) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
+  __shared__ __attribute__((aligned(16))) uint8_t st0[kStage], st1[kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t ws[SL ? 2 * 512 * 16 : 16];
   FatItem it;
   if (!find_item(g.offsets, g.E, g.R, ntw, ntn, it)) return;
-  lds8_t* lds = (lds8_t*)smem;
+  const LdsL lds{st0, st1, ws};
   if (it.wide) {
-    if (it.M > 192) large_tile<SL, 2, 4>(g, it, lds);
-    else large_tile<SL, 2, 3>(g, it, lds);
+    if (it.M > 192) large_tile<SL, 2, 8>(g, it, lds);
+    else large_tile<SL, 2, 6>(g, it, lds);
   } else {
-    if (it.M > 96) large_tile<SL, 1, 4>(g, it, lds);
-    else if (it.M > 64) large_tile<SL, 1, 3>(g, it, lds);
-    else if (it.M > 32) large_tile<SL, 1, 2>(g, it, lds);
+    if (it.M > 96) large_tile<SL, 1, 8>(g, it, lds);
+    else if (it.M > 64) large_tile<SL, 1, 6>(g, it, lds);
+    else if (it.M > 32) large_tile<SL, 1, 4>(g, it, lds);
+    else if (it.M > 16) large_tile<SL, 1, 2>(g, it, lds);
     else large_tile<SL, 1, 1>(g, it, lds);
   }
 }

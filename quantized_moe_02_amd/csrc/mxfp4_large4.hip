@@ -91,8 +91,8 @@ __device__ __forceinline__ void tile4(const MatmulArgs& g, const FatItem& it, ld
   auto write_s = [&](int grp) {
     if constexpr (SL) return;
     const int valid = nb - 16 * grp;
-    *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(lds + kLdsWs + (grp & 1) * 4096 + tid * 16) = sw[0].bytes(soff[0], soff[0] < kOutside ? valid : 0);
-    *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(lds + kLdsAs + (grp & 1) * 4096 + tid * 16) = sw[1].bytes(soff[1], soff[1] < kOutside ? valid : 0);
+    lds_write16(lds + kLdsWs + (grp & 1) * 4096 + tid * 16, sw[0].bytes(soff[0], soff[0] < kOutside ? valid : 0));
+    lds_write16(lds + kLdsAs + (grp & 1) * 4096 + tid * 16, sw[1].bytes(soff[1], soff[1] < kOutside ? valid : 0));
   };
   // load i < NV of block kb into the stage at byte p (0 or 32768) of each side
   auto issue = [&](uint32_t p, int kb, int i) {
@@ -208,8 +208,8 @@ __device__ __forceinline__ void tile4(const MatmulArgs& g, const FatItem& it, ld
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<__attribute__((address_space(3))) u32x2*>(t + (c * 32 + ln) * (RB + 16) + rt * 64 + 16 * q + 8 * lh) =
-              u32x2{pack_bf16(acc[rt][c][4 * q], acc[rt][c][4 * q + 1]), pack_bf16(acc[rt][c][4 * q + 2], acc[rt][c][4 * q + 3])};
+          lds_write8(t + (c * 32 + ln) * (RB + 16) + rt * 64 + 16 * q + 8 * lh,
+                   u32x2{pack_bf16(acc[rt][c][4 * q], acc[rt][c][4 * q + 1]), pack_bf16(acc[rt][c][4 * q + 2], acc[rt][c][4 * q + 3])});
     store_rows<RB>(g, t, rows, row0, n0 + wn * RT * 32, g.N);
   } else {
     // half of the outputs at a time
@@ -223,8 +223,7 @@ __device__ __forceinline__ void tile4(const MatmulArgs& g, const FatItem& it, ld
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f32x16& v = acc[h * (RT / 2) + rt][c];
-            *reinterpret_cast<__attribute__((address_space(3))) f32x4*>(t + (c * 32 + ln) * (RB + 16) + rt * 128 + 32 * q + 16 * lh) =
-                f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            lds_write16(t + (c * 32 + ln) * (RB + 16) + rt * 128 + 32 * q + 16 * lh, __builtin_bit_cast(u32x4, f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]}));
           }
       store_rows<RB>(g, t, rows, row0, n0 + wn * RT * 32 + h * (RT / 2) * 32, g.N);
     }

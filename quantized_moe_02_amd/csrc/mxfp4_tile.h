@@ -183,10 +183,15 @@ __device__ __forceinline__ void to_lds16_raw(const i32x4& r, uint32_t dst, uint3
 // LDS by 32-bit address.
 typedef __attribute__((address_space(3))) uint8_t lds8_t;
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3), may_alias)) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3), may_alias)) u32x2 lds_u32x2;
 __device__ __forceinline__ uint32_t lds_addr(const lds8_t* p) { return (uint32_t)(uintptr_t)p; }
 __device__ __forceinline__ u32x4 lds_read16(const lds8_t* p) {
-  return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(p);
+  return *reinterpret_cast<const lds_u32x4*>(p);
 }
+__device__ __forceinline__ void lds_write16(lds8_t* p, u32x4 v) { *reinterpret_cast<lds_u32x4*>(p) = v; }
+__device__ __forceinline__ void lds_write8(lds8_t* p, u32x2 v) { *reinterpret_cast<lds_u32x2*>(p) = v; }
 
 // 16 scale bytes of a row starting at byte `off` of a descriptor whose base is
 // 4-byte aligned.
@@ -212,6 +217,14 @@ struct ScaleWords {
   }
 };
 
+// Orders this wave's LDS accesses between lanes: the hardware keeps a wave's
+// accesses in order, the compiler only each lane's.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
 // Results leave through LDS: the lanes of a store from the accumulators hold 4
 // outputs of as many rows, 16-byte requests, where the vector cache takes a
 // line in one.  A wave lays its rows out at RB + 16 bytes each (rows 16 apart
@@ -225,6 +238,7 @@ __device__ __forceinline__ void store_rows(const MatmulArgs& g, const lds8_t* t,
   const int col = col0 + c * per;
   const bool vec = g.ldo % per == 0 && col + per <= out_cols;
   uint8_t* o = static_cast<uint8_t*>(g.out) + ((int64_t)row0 * g.ldo + col) * es;
+  wave_sync();
   for (int r = lane / LPR; r < rows; r += RPI) {
     const u32x4 v = lds_read16(t + r * (RB + 16) + c * 16);
     uint8_t* p = o + (int64_t)r * g.ldo * es;
@@ -240,8 +254,8 @@ __device__ __forceinline__ void store_rows(const MatmulArgs& g, const lds8_t* t,
         if (col + j < out_cols) reinterpret_cast<uint32_t*>(p)[j] = v[j];
     }
   }
+  wave_sync();   // the next results may take their place
 }
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const bf16x2 v = {(__bf16)a, (__bf16)b};
   return __builtin_bit_cast(uint32_t, v);
