@@ -1,10 +1,11 @@
-// Grouped products over MXFP4 expert weights for few rows, and the choice of
-// the kernel.
+// Grouped products over MXFP4 expert weights for few rows, their gradient for
+// few rows, and the choice of the kernel.
 //
-// A block of 32 inputs is one lane's share: 16 bytes of codes and one scale
-// byte.  Rows in bf16: the codes become bf16 with their scale (exact: E2M1
-// times a power of two) in four 16x16x32 steps.  Rows in MXFP4: the codes go
-// into one 16x16x128 scaled step as they are.
+// A few rows per expert: the weights are read once and bound the call (HBM),
+// or the call is a few microseconds of latency.  So the rows come into LDS, the
+// weights straight from global memory into the matrix units' operands, whole
+// lines per row, and the four waves of a workgroup split the sum and add their
+// parts up in LDS, in a fixed order.
 #include <algorithm>
 
 #include "mxfp4_tile.h"
@@ -12,104 +13,246 @@
 namespace qmoe {
 namespace {
 
+constexpr int kThinRows = 16;            // rows of a unit
+constexpr int kThinLds = 16 * (4 * 512 + 16);   // four steps of them
+
 // At most this many units for R rows of E experts.
 long max_units(const MatmulArgs& g, int BM) {
-  return (long)g.R / BM + (g.offsets ? (long)min(g.E, g.R) : 1);
+  return (long)g.R / BM + (g.offsets ? (long)std::min(g.E, g.R) : 1);
 }
 
-// One wave: 16 outputs x 16 rows.
-template <bool MX>
-__global__ void __launch_bounds__(256) mx_matmul_kernel(MatmulArgs g, int nt) {
-  const int ub = blockIdx.x / nt, tile = blockIdx.x - ub * nt;
-  const RowUnit u = find_unit(g.offsets, g.E, g.R, 16, ub);
-  if (u.M <= 0) return;
-  const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4, wv = threadIdx.x >> 6;
-  const int n0 = tile * 64 + wv * 16;
-  if (n0 >= g.N) return;
-  const int nb = g.K / kMxBlock;
-  const int64_t wrow = (int64_t)u.e * g.N + n0 + lr;
-  const bool wok = n0 + lr < g.N;
-  const int64_t arow = lr < u.M ? source_row(g, u.r0 + lr) : -1;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int b0 = 0; b0 < nb; b0 += 4) {
-    const int b = b0 + lq;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    uint32_t sb = 0;
-    if (wok && b < nb) {
-      w = reinterpret_cast<const uint4*>(g.w_codes)[wrow * nb + b];
-      sb = g.w_scale[wrow * nb + b];
-    }
-    if constexpr (MX) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      uint32_t xb = 0;
-      if (arow >= 0 && b < nb) {
-        x = static_cast<const uint4*>(g.a)[arow * nb + b];
-        xb = g.a_scale[arow * nb + b];
-      }
-      const i32x8 A = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
-      const i32x8 B = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc, 4, 4, 0, (int)sb, 0, (int)xb);
-    } else {
-      const float s = __uint_as_float(sb << 23);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+// ---------------------------------------------------------------------------
+// RT x 16 outputs x up to 16 rows.  A step is 256 inputs, a line of a row's
+// codes: lane (lr, lq) takes blocks 2 lq and 2 lq + 1 of row lr.  Wave w takes
+// steps w, w + 4, ... of a slab, the steps whose rows fit LDS.
+// ---------------------------------------------------------------------------
+// 16-byte chunk c (8 bf16 inputs) of row r of a slab of S steps: rows of 512 S
+// bytes, and 16 more, so that the rows of one operand read lie on distinct banks.
+__device__ __forceinline__ int slab_at(int r, int S, int c) { return r * (512 * S + 16) + c * 16; }
+
+template <bool MX, int RT>
+__device__ __forceinline__ void thin_tile(const MatmulArgs& g, const RowUnit& u, int n0, lds8_t* lds) {
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nb = g.K / kMxBlock, steps = (g.K + 255) / 256;
+  f32x4 acc[RT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+  for (int rt = 0; rt < RT; ++rt) acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int64_t erow = (int64_t)u.e * g.N;
+  const rsrc_t wr = make_rsrc(g.w_codes + erow * (g.K / 2), (uint32_t)g.N * (uint32_t)(g.K / 2));
+  const rsrc_t sr = make_rsrc(g.w_scale + erow * nb, (uint32_t)g.N * (uint32_t)nb);
+  const uint32_t row = (uint32_t)(n0 + lr);
+  // both chunks of a step and their scales (low byte: the first); blocks past
+  // K get zero codes and the scale 2^-127
+  auto load_w = [&](int s, int rt, uint32_t (&w)[2][4], uint32_t& sb) {
+    const int b = s * 8 + 2 * lq;
+    const uint32_t at = (row + 16u * rt) * (uint32_t)(g.K / 2) + 16u * b, st = (row + 16u * rt) * (uint32_t)nb + (uint32_t)b;
+    bload16(w[0], wr, b < nb ? at : kOutside, 0);
+    bload16(w[1], wr, b + 1 < nb ? at + 16u : kOutside, 0);
+    sb = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(sr, b < nb ? st : kOutside, 0, 0) |
+         (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(sr, b + 1 < nb ? st + 1u : kOutside, 0, 0) << 8;
+  };
+
+  if constexpr (MX) {
+    // rows in MXFP4: as small as the weights, read by every wave directly
+    const int64_t arow = lr < u.M ? source_row(g, u.r0 + lr) : -1;
+    for (int s = wv; s < steps; s += 4) {
+      uint32_t w[RT][2][4], sb[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) load_w(s, rt, w[rt], sb[rt]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int b = s * 8 + 2 * lq + h;
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (arow >= 0 && b < nb)
-          x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.a) + arow * g.lda + b * kMxBlock + 8 * i);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_of(ww[i], s), __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
+        uint32_t xs = 0;
+        if (arow >= 0 && b < nb) {
+          x = static_cast<const uint4*>(g.a)[arow * nb + b];
+          xs = g.a_scale[arow * nb + b];
+        }
+        const i32x8 X = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const i32x8 W = {(int)w[rt][h][0], (int)w[rt][h][1], (int)w[rt][h][2], (int)w[rt][h][3], 0, 0, 0, 0};
+          acc[rt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(W, X, acc[rt], 4, 4, 0, (int)(sb[rt] >> (8 * h)), 0, (int)xs);
+        }
       }
     }
+  } else {
+    // steps per slab: a multiple of the four waves, or all of them
+    const int fit = (kThinLds / u.M - 16) / 512, slab = fit >= steps ? steps : fit & ~3;
+    for (int s0 = 0; s0 < steps; s0 += slab) {
+      const int S = min(slab, steps - s0);
+      // the wave's first codes are on their way while the rows are staged
+      uint32_t w[RT][2][4], sb[RT];
+      if (wv < S) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) load_w(s0 + wv, rt, w[rt], sb[rt]);
+      }
+      if (s0 > 0) __syncthreads();
+      for (int i = tid; i < u.M * S * 32; i += 256) {
+        const int r = i / (S * 32), c = i - r * (S * 32), k = s0 * 256 + c * 8;
+        const int64_t src = source_row(g, u.r0 + r);
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (src >= 0 && k < g.K) v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(g.a) + src * g.lda + k);
+        lds_write16(lds + slab_at(r, S, c), v);
+      }
+      __syncthreads();
+      for (int s = wv; s < S; s += 4) {
+        uint32_t wn[RT][2][4], sn[RT];
+        if (s + 4 < S) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) load_w(s0 + s + 4, rt, wn[rt], sn[rt]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            bf16x8 A[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) A[rt] = bf16_of(w[rt][h][i], __uint_as_float((sb[rt] >> (8 * h)) << 23));
+            // lanes past the rows repeat the last one; their results are dropped
+            const bf16x8 x = __builtin_bit_cast(bf16x8, lds_read16(lds + slab_at(min(lr, u.M - 1), S, s * 32 + (2 * lq + h) * 4 + i)));
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) acc[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[rt], x, acc[rt], 0, 0, 0);
+          }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          sb[rt] = sn[rt];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[rt][h][i] = wn[rt][h][i];
+        }
+      }
+    }
+  }
+  // the waves' parts, added in order
+  static_assert(4 * RT * 1024 <= kThinLds, "the parts fit");
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < RT; ++t) lds_write16(lds + ((wv * RT + t) * 64 + lane) * 16, __builtin_bit_cast(u32x4, acc[t]));
+  __syncthreads();
+  const bool vec = g.ldo % 4 == 0;
+  for (int t = wv; t < RT; t += 4) {
+    f32x4 v = __builtin_bit_cast(f32x4, lds_read16(lds + (t * 64 + lane) * 16));
+#pragma unroll
+    for (int p = 1; p < 4; ++p) v += __builtin_bit_cast(f32x4, lds_read16(lds + ((p * RT + t) * 64 + lane) * 16));
+    if (lr < u.M) store4(g, vec, u.r0 + lr, n0 + 16 * t + 4 * lq, g.N, v);
+  }
+}
+
+template <bool MX, int RT>
+__global__ void __launch_bounds__(256) mx_matmul_thin_kernel(MatmulArgs g, int nt) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kThinLds];
+  const int ub = blockIdx.x / nt, tile = blockIdx.x - ub * nt;
+  const RowUnit u = find_unit(g.offsets, g.E, g.R, kThinRows, ub);
+  if (u.M <= 0) return;
+  thin_tile<MX, RT>(g, u, tile * 16 * RT, (lds8_t*)smem);
+}
+
+// ---------------------------------------------------------------------------
+// The gradient: 256 columns x up to 16 rows.  As in the kernel for many rows, a
+// lane takes words of eight rows of the weights and regroups them along the
+// sum; here two words, 16 columns, so that a row's share is a whole line.  Wave
+// w takes every fourth step of 32 terms.
+// ---------------------------------------------------------------------------
+constexpr int kDxThinLds = 64 * 1024;
+
+__device__ __forceinline__ void dx_thin_tile(const MatmulArgs& g, const RowUnit& u, int k0, lds8_t* lds) {
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nb = g.K / kMxBlock, steps = g.N / 32;
+  f32x4 acc[16];
+#pragma unroll
+  for (int t = 0; t < 16; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int64_t erow = (int64_t)u.e * g.N;
+  const rsrc_t wr = make_rsrc(g.w_codes + erow * (g.K / 2), (uint32_t)g.N * (uint32_t)(g.K / 2));
+  const rsrc_t sr = make_rsrc(g.w_scale + erow * nb, (uint32_t)g.N * (uint32_t)nb);
+  const int k = k0 + 16 * lr;
+  const uint32_t wat = (uint32_t)(8 * lq) * (uint32_t)(g.K / 2) + (uint32_t)(k / 2);
+  const uint32_t sat = (uint32_t)(8 * lq) * (uint32_t)nb + (uint32_t)(k / 32);
+  // lanes past the rows repeat the last one
+  const uint16_t* dy = static_cast<const uint16_t*>(g.a) + (int64_t)(u.r0 + min(lr, u.M - 1)) * g.lda + 8 * lq;
+  for (int s = wv; s < steps; s += 4) {
+    uint32_t w[8][2];
+    float sc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t o = (uint32_t)(32 * s + j);
+      bload8(w[j], wr, k < g.K ? wat + o * (uint32_t)(g.K / 2) : kOutside, 0);
+      sc[j] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b8(sr, k < g.K ? sat + o * (uint32_t)nb : kOutside, 0, 0) << 23);
+    }
+    const bf16x8 B = *reinterpret_cast<const bf16x8*>(dy + 32 * s);
+    static_for<8>([&](auto T) {
+      constexpr int t = decltype(T)::value;
+      union {
+        uint32_t x[4];
+        bf16x8 v;
+      } lo, hi;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[2 * m][t / 4], sc[2 * m], t % 4));
+        const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[2 * m + 1][t / 4], sc[2 * m + 1], t % 4));
+        lo.x[m] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+        hi.x[m] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+      }
+      acc[2 * t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo.v, B, acc[2 * t], 0, 0, 0);
+      acc[2 * t + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi.v, B, acc[2 * t + 1], 0, 0, 0);
+    });
+  }
+  // the waves' parts, added in order; wave w takes tiles 4 w .. 4 w + 3
+  const bool vec = g.ldo % 4 == 0;
+#pragma unroll
+  for (int t = 0; t < 16; ++t) lds_write16(lds + ((wv * 16 + t) * 64 + lane) * 16, __builtin_bit_cast(u32x4, acc[t]));
+  __syncthreads();
+  f32x4 v[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    v[t] = __builtin_bit_cast(f32x4, lds_read16(lds + ((4 * wv + t) * 64 + lane) * 16));
+#pragma unroll
+    for (int p = 1; p < 4; ++p) v[t] += __builtin_bit_cast(f32x4, lds_read16(lds + ((p * 16 + 4 * wv + t) * 64 + lane) * 16));
   }
   if (lr >= u.M) return;
+  // tile 4 wv + t, result row 4 lq + i: column 16 (4 lq + i) + 4 wv + t
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (n0 + 4 * lq + i < g.N) store_out(g, u.r0 + lr, n0 + 4 * lq + i, acc[i]);
+    store4(g, vec, u.r0 + lr, k0 + 16 * (4 * lq + i) + 4 * wv, g.K, f32x4{v[0][i], v[1][i], v[2][i], v[3][i]});
 }
 
-// One thread: two neighbouring inputs of one row.
-__global__ void __launch_bounds__(256) mx_matmul_dx_kernel(MatmulArgs g, int nt) {
+__global__ void __launch_bounds__(256) mx_matmul_dx_thin_kernel(MatmulArgs g, int nt) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kDxThinLds];
   const int ub = blockIdx.x / nt, tile = blockIdx.x - ub * nt;
-  const RowUnit u = find_unit(g.offsets, g.E, g.R, 1, ub);
-  const int k = (tile * 256 + threadIdx.x) * 2;
-  if (u.M <= 0 || k >= g.K) return;
-  const int nb = g.K / kMxBlock;
-  const uint16_t* dy = static_cast<const uint16_t*>(g.a) + u.r0 * g.lda;
-  float a0 = 0.f, a1 = 0.f;
-  for (int j = 0; j < g.N; ++j) {
-    const int64_t wrow = (int64_t)u.e * g.N + j;
-    const float d = __uint_as_float((uint32_t)dy[j] << 16);
-    const uint32_t w = g.w_codes[wrow * (g.K / 2) + k / 2];
-    const float s = __uint_as_float((uint32_t)g.w_scale[wrow * nb + k / kMxBlock] << 23);
-    const auto v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0);
-    a0 = fmaf(d, v[0], a0);
-    a1 = fmaf(d, v[1], a1);
-  }
-  store_out(g, u.r0, k, a0);
-  store_out(g, u.r0, k + 1, a1);
+  const RowUnit u = find_unit(g.offsets, g.E, g.R, kThinRows, ub);
+  if (u.M <= 0) return;
+  dx_thin_tile(g, u, tile * 256, (lds8_t*)smem);
 }
 
 }  // namespace
 
 hipError_t launch_mx_matmul(const MatmulArgs& g, bool a_mxfp4, hipStream_t s) {
   // few rows per expert, or too few outputs to give a quarter of the CUs an
-  // item: the small kernel; sources past 32-bit offsets too
+  // item of 256 x 256: the thin kernel; sources past 32-bit offsets too
   const int64_t ldb = a_mxfp4 ? g.K / 2 : g.lda * 2;
   const int64_t span = (g.index ? (int64_t)g.a_rows : kFatRows) * ldb;
   if (g.R >= 8 * (int64_t)g.E && (int64_t)g.R * g.N >= 64 * 256 * 256 && span < (int64_t)kOutside)
     return a_mxfp4 ? launch_mx_matmul4_large(g, s) : launch_mx_matmul_large(g, s);
-  const int nt = (g.N + 63) / 64;
-  const dim3 grid((unsigned)(max_units(g, 16) * nt));
-  if (a_mxfp4) hipLaunchKernelGGL(mx_matmul_kernel<true>, grid, dim3(256), 0, s, g, nt);
-  else hipLaunchKernelGGL(mx_matmul_kernel<false>, grid, dim3(256), 0, s, g, nt);
+  const long units = max_units(g, kThinRows);
+  // 64 outputs a workgroup (a row's inputs are then read for four row tiles)
+  // where that leaves every CU several, else 32 or 16
+  const int rt = units * ((g.N + 63) / 64) >= 1024 ? 4 : units * ((g.N + 31) / 32) >= 512 ? 2 : 1;
+  const int nt = (g.N + 16 * rt - 1) / (16 * rt);
+  auto* k = a_mxfp4 ? (rt == 4 ? mx_matmul_thin_kernel<true, 4> : rt == 2 ? mx_matmul_thin_kernel<true, 2> : mx_matmul_thin_kernel<true, 1>)
+                    : (rt == 4 ? mx_matmul_thin_kernel<false, 4> : rt == 2 ? mx_matmul_thin_kernel<false, 2> : mx_matmul_thin_kernel<false, 1>);
+  hipLaunchKernelGGL(k, dim3((unsigned)(units * nt)), dim3(256), 0, s, g, nt);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_matmul_dx(const MatmulArgs& g, hipStream_t s) {
   if (g.R >= 8 * (int64_t)g.E && (int64_t)g.R * g.K >= 64 * 256 * 256 && kFatRows * g.lda * 2 < (int64_t)kOutside)
     return launch_mx_matmul_dx_large(g, s);
-  const int nt = (g.K + 511) / 512;
-  hipLaunchKernelGGL(mx_matmul_dx_kernel, dim3((unsigned)(max_units(g, 1) * nt)), dim3(256), 0, s, g, nt);
+  const int nt = (g.K + 255) / 256;
+  hipLaunchKernelGGL(mx_matmul_dx_thin_kernel, dim3((unsigned)(max_units(g, kThinRows) * nt)), dim3(256), 0, s, g, nt);
   return hipGetLastError();
 }
 

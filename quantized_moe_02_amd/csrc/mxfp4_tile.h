@@ -66,10 +66,25 @@ __device__ __forceinline__ RowUnit find_unit(const int32_t* offsets, int E, int 
                  __builtin_amdgcn_readfirstlane(hit[2])};
 }
 
-__device__ __forceinline__ void store_out(const MatmulArgs& g, int row, int col, float v) {
+// Stores four consecutive outputs of one row (col % 4 == 0; vec: ldo % 4 == 0).
+__device__ __forceinline__ void store4(const MatmulArgs& g, bool vec, int row, int col, int cols, const f32x4& v) {
   const int64_t i = (int64_t)row * g.ldo + col;
-  if (g.out_bf16) static_cast<__bf16*>(g.out)[i] = (__bf16)v;
-  else static_cast<float*>(g.out)[i] = v;
+  if (vec && col + 4 <= cols) {
+    if (g.out_bf16) {
+      typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+      *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(g.out) + i) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    } else {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + i) = v;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (col + j < cols) {
+      if (g.out_bf16) static_cast<__bf16*>(g.out)[i + j] = (__bf16)v[j];
+      else static_cast<float*>(g.out)[i + j] = v[j];
+    }
+  }
 }
 
 // Row of `a` behind output row r, or -1 where the index points outside.
