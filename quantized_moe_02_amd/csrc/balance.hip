@@ -141,24 +141,43 @@ __device__ __forceinline__ void shares(const float4& l4, float (&p)[4], float (&
   for (int j = 0; j < 4; ++j) p[j] *= z;
 }
 
-template <int LPT, bool SIGMOID, bool BF16, bool VEC>
+// Sum of v over the workgroup's 256 threads, to every thread.
+__device__ __forceinline__ double block_sum(double v, double* buf) {
+  v = wave_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (buf[0] + buf[1]) + (buf[2] + buf[3]);
+}
+
+// ONE: a single chunk; the workgroup goes through every sequence and writes
+// the results themselves.
+template <int LPT, bool SIGMOID, bool BF16, bool VEC, bool ONE>
 __global__ void __launch_bounds__(256) balance_partial_kernel(BalanceArgs a, int chunk) {
   constexpr int TPW = 64 / LPT;   // tokens per wave
   __shared__ __attribute__((aligned(16))) float sp[4 * TPW][LPT * 4];
-  __shared__ int sc[kMaxE], sn;
+  __shared__ int sc[kMaxE], sn, sk;
   __shared__ uint8_t routed[kMaxChunk];
+  __shared__ double buf[4];
+  double loss = 0.0;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int group = wv * TPW + lane / LPT, e0 = (lane % LPT) * 4;
-  if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;
   const int t0 = blockIdx.x * chunk, t1 = min(a.T, t0 + chunk);
-  if (t0 >= t1) return;
-  for (int s = seq_of(a, t0); s < a.S; ++s) {
+  for (int s = ONE ? 0 : seq_of(a, t0); s < a.S; ++s) {
     const int lo = max(t0, seq_at(a, s)), hi = min(t1, seq_at(a, s + 1));
-    if (lo >= t1) break;
-    if (lo >= hi) continue;
+    if constexpr (ONE) {
+      if (lo >= hi) {   // no tokens
+        if (tid < a.E) a.counts[(int64_t)s * a.E + tid] = 0;
+        if (tid == 0) a.tokens[s] = 0;
+        continue;
+      }
+    } else {
+      if (lo >= t1) break;
+      if (lo >= hi) continue;
+    }
     sc[tid] = 0;
     routed[tid] = 0;
-    if (tid == 0) sn = 0;
+    if (tid == 0) sn = sk = 0;
     __syncthreads();
     const int picks = (hi - lo) * a.K;
     for (int i = tid; i < picks; i += 256) {
@@ -169,7 +188,16 @@ __global__ void __launch_bounds__(256) balance_partial_kernel(BalanceArgs a, int
       }
     }
     __syncthreads();
-    if (tid < hi - lo && routed[tid]) atomicAdd(&sn, 1);
+    {
+      const uint64_t on = __ballot(tid < hi - lo && routed[tid]);
+      int k = tid < a.E ? sc[tid] : 0;
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) k += __shfl_xor(k, o, 64);
+      if (lane == 0) {
+        atomicAdd(&sn, __popcll(on));
+        atomicAdd(&sk, k);
+      }
+    }
     float acc[4] = {};
     for (int b = lo; b < hi; b += 4 * TPW * kRows) {
       float4 l[kRows];
@@ -187,35 +215,49 @@ __global__ void __launch_bounds__(256) balance_partial_kernel(BalanceArgs a, int
     }
     *reinterpret_cast<float4*>(&sp[group][e0]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
     __syncthreads();
-    const int64_t slot = (int64_t)blockIdx.x + s;
+    float t = 0.0f;
     if (tid < a.E) {
-      float t = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4 * TPW; ++i) t += sp[i][tid];
-      a.part_p[slot * a.E + tid] = t;
-      a.part_c[slot * a.E + tid] = sc[tid];
     }
-    if (tid == 0) a.part_n[slot] = sn;
+    if constexpr (ONE) {
+      if (tid < a.E) a.counts[(int64_t)s * a.E + tid] = sc[tid];
+      if (tid == 0) a.tokens[s] = sn;
+      const double v = block_sum(tid < a.E ? (double)t * sc[tid] : 0.0, buf);
+      if (sn > 0) loss += v * a.E / ((double)sn * sk);
+    } else {
+      const int64_t slot = (int64_t)blockIdx.x + s;
+      if (tid < a.E) {
+        a.part_p[slot * a.E + tid] = t;
+        a.part_c[slot * a.E + tid] = sc[tid];
+      }
+      if (tid == 0) {
+        a.part_n[slot] = sn;
+        a.part_k[slot] = sk;
+      }
+    }
     __syncthreads();
+  }
+  if constexpr (ONE) {
+    if (tid == 0) *a.loss = (float)(loss * a.coef / a.S);
   }
 }
 
 // One workgroup: 32 experts of one sequence, eight threads per expert, each a
 // range of the chunks.
 __global__ void __launch_bounds__(256) balance_reduce_kernel(BalanceArgs a, int chunk, int slices) {
-  __shared__ double rp[kSlices][kSliceE], rs[256];
-  __shared__ int rc[kSlices][kSliceE], rn[256];
-  __shared__ bool last;
+  __shared__ double rp[kSlices][kSliceE];
+  __shared__ int rc[kSlices][kSliceE], rn[256], rk[256];
   const int s = blockIdx.x / slices, part = blockIdx.x - s * slices;
   const int tid = threadIdx.x, x = tid % kSliceE, y = tid / kSliceE;
   const int e = part * kSliceE + x;
   const int lo = seq_at(a, s), hi = seq_at(a, s + 1);
   const int c0 = lo / chunk, nc = hi > lo ? (hi - 1) / chunk - c0 + 1 : 0;
   double p = 0.0;
-  int c = 0, n = 0;
+  int c = 0, n = 0, picks = 0;
+  const int64_t first = (int64_t)c0 + s;
   if (e < a.E) {
     const int per = (nc + kSlices - 1) / kSlices;
-    const int64_t first = (int64_t)c0 + s;
     const int k1 = min(nc, (y + 1) * per);
 #pragma unroll 8
     for (int k = y * per; k < k1; ++k) {
@@ -223,13 +265,20 @@ __global__ void __launch_bounds__(256) balance_reduce_kernel(BalanceArgs a, int 
       c += a.part_c[(first + k) * a.E + e];
     }
   }
-  for (int k = tid; k < nc; k += 256) n += a.part_n[(int64_t)c0 + s + k];
+  for (int k = tid; k < nc; k += 256) {
+    n += a.part_n[first + k];
+    picks += a.part_k[first + k];
+  }
   rp[y][x] = p;
   rc[y][x] = c;
   rn[tid] = n;
+  rk[tid] = picks;
   __syncthreads();
   for (int o = 128; o > 0; o >>= 1) {
-    if (tid < o) rn[tid] += rn[tid + o];
+    if (tid < o) {
+      rn[tid] += rn[tid + o];
+      rk[tid] += rk[tid + o];
+    }
     __syncthreads();
   }
   if (y == 0) {
@@ -240,41 +289,26 @@ __global__ void __launch_bounds__(256) balance_reduce_kernel(BalanceArgs a, int 
     }
     if (e < a.E) a.counts[(int64_t)s * a.E + e] = c;
     rp[0][x] = p * c;
-    rc[0][x] = c;
   }
   __syncthreads();
   if (tid == 0) {
     double t = 0.0;
-    int picks = 0;
-    for (int i = 0; i < kSliceE; ++i) {
-      t += rp[0][i];
-      picks += rc[0][i];
-    }
+    for (int i = 0; i < kSliceE; ++i) t += rp[0][i];
     if (part == 0) a.tokens[s] = rn[0];
-    // sum of c p over these experts, scaled by 1 / n; the picks join in the last workgroup
-    __hip_atomic_store(&a.seq_loss[blockIdx.x], rn[0] > 0 ? t / rn[0] : 0.0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(&a.seq_picks[blockIdx.x], picks, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    // these experts' part of sum f P
+    t = rn[0] > 0 ? t * a.E / ((double)rn[0] * rk[0]) : 0.0;
+    a.seq_loss[blockIdx.x] = t;
   }
-  __syncthreads();
-  if (!last) return;
+}
+
+// One workgroup: the loss from its n parts.
+__global__ void __launch_bounds__(256) balance_loss_kernel(BalanceArgs a, int n) {
+  __shared__ double buf[4];
   double t = 0.0;
-  for (int i = tid; i < a.S; i += 256) {
-    double v = 0.0;
-    int picks = 0;
-    for (int j = 0; j < slices; ++j) {
-      v += __hip_atomic_load(&a.seq_loss[i * slices + j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      picks += __hip_atomic_load(&a.seq_picks[i * slices + j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    if (picks > 0) t += v * a.E / picks;
-  }
-  rs[tid] = t;
-  __syncthreads();
-  for (int o = 128; o > 0; o >>= 1) {
-    if (tid < o) rs[tid] += rs[tid + o];
-    __syncthreads();
-  }
-  if (tid == 0) *a.loss = (float)(rs[0] * a.coef / a.S);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += 256) t += a.seq_loss[i];
+  t = block_sum(t, buf);
+  if (threadIdx.x == 0) *a.loss = (float)(t * a.coef / a.S);
 }
 
 // A wave takes `per` consecutive tokens (a multiple of TPW * kRows).
@@ -380,15 +414,26 @@ int balance_chunk(int T) { return std::min(kMaxChunk, std::max(32, (T + 1023) / 
 int balance_slices(int E) { return (E + kSliceE - 1) / kSliceE; }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
+  // up to 128 tokens: the launches would take longer than one workgroup does
+  if (a.T <= 128 && a.S <= 256) {
+    dispatch(a, [&](auto L, auto S, auto B, auto V) {
+      hipLaunchKernelGGL((balance_partial_kernel<decltype(L)::value, decltype(S)::value, decltype(B)::value, decltype(V)::value, true>),
+                         dim3(1), dim3(256), 0, s, a, kMaxChunk);
+    });
+    return hipGetLastError();
+  }
   const int chunk = balance_chunk(a.T), slices = balance_slices(a.E);
-  const int nc = std::max(1, (a.T + chunk - 1) / chunk);   // at least one workgroup: it clears the ticket
-  dispatch(a, [&](auto L, auto S, auto B, auto V) {
-    hipLaunchKernelGGL((balance_partial_kernel<decltype(L)::value, decltype(S)::value, decltype(B)::value, decltype(V)::value>),
-                       dim3(nc), dim3(256), 0, s, a, chunk);
-  });
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  hipError_t e;
+  if (a.T > 0) {
+    dispatch(a, [&](auto L, auto S, auto B, auto V) {
+      hipLaunchKernelGGL((balance_partial_kernel<decltype(L)::value, decltype(S)::value, decltype(B)::value, decltype(V)::value, false>),
+                         dim3((a.T + chunk - 1) / chunk), dim3(256), 0, s, a, chunk);
+    });
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(balance_reduce_kernel, dim3((unsigned)a.S * slices), dim3(256), 0, s, a, chunk, slices);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(256), 0, s, a, a.S * slices);
   return hipGetLastError();
 }
 

@@ -13,7 +13,7 @@
 namespace qmoe {
 namespace {
 
-constexpr int kThinRows = 16;            // rows of a unit
+constexpr int kThinRows = 16;                   // rows of a unit
 constexpr int kThinLds = 16 * (4 * 512 + 16);   // four steps of them
 
 // At most this many units for R rows of E experts.
@@ -22,45 +22,52 @@ long max_units(const MatmulArgs& g, int BM) {
 }
 
 // ---------------------------------------------------------------------------
-// RT x 16 outputs x up to 16 rows.  A step is 256 inputs, a line of a row's
-// codes: lane (lr, lq) takes blocks 2 lq and 2 lq + 1 of row lr.  Wave w takes
-// steps w, w + 4, ... of a slab, the steps whose rows fit LDS.
+// RT x 16 outputs x up to 16 rows, for one or several neighbouring tiles of
+// outputs.  A step is 256 inputs, a line of a row's codes: lane (lr, lq) takes
+// blocks 2 lq and 2 lq + 1 of row lr.  Wave w takes steps w, w + 4, ... of a
+// slab, the steps whose rows fit LDS (most calls have one slab, whose rows then
+// stay for every tile).  D of a wave's steps are in flight.
 // ---------------------------------------------------------------------------
 // 16-byte chunk c (8 bf16 inputs) of row r of a slab of S steps: rows of 512 S
 // bytes, and 16 more, so that the rows of one operand read lie on distinct banks.
 __device__ __forceinline__ int slab_at(int r, int S, int c) { return r * (512 * S + 16) + c * 16; }
 
-template <bool MX, int RT>
-__device__ __forceinline__ void thin_tile(const MatmulArgs& g, const RowUnit& u, int n0, lds8_t* lds) {
+// EV: an even number of blocks per row, whose scales come in pairs.
+template <bool MX, int RT, bool EV>
+__device__ __forceinline__ void thin_tiles(const MatmulArgs& g, const RowUnit& u, int tile, int tiles, lds8_t* lds, lds8_t* parts) {
+  constexpr int D = RT == 4 ? 2 : 3;
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nb = g.K / kMxBlock, steps = (g.K + 255) / 256;
-  f32x4 acc[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int64_t erow = (int64_t)u.e * g.N;
-  const rsrc_t wr = make_rsrc(g.w_codes + erow * (g.K / 2), (uint32_t)g.N * (uint32_t)(g.K / 2));
+  const uint32_t wld = (uint32_t)(g.K / 2);
+  const rsrc_t wr = make_rsrc(g.w_codes + erow * wld, (uint32_t)g.N * wld);
   const rsrc_t sr = make_rsrc(g.w_scale + erow * nb, (uint32_t)g.N * (uint32_t)nb);
-  const uint32_t row = (uint32_t)(n0 + lr);
   // both chunks of a step and their scales (low byte: the first); blocks past
   // K get zero codes and the scale 2^-127
-  auto load_w = [&](int s, int rt, uint32_t (&w)[2][4], uint32_t& sb) {
+  uint32_t w[D][RT][2][4], sb[D][RT];
+  auto load_w = [&](int d, int n0, int s) {
     const int b = s * 8 + 2 * lq;
-    const uint32_t at = (row + 16u * rt) * (uint32_t)(g.K / 2) + 16u * b, st = (row + 16u * rt) * (uint32_t)nb + (uint32_t)b;
-    bload16(w[0], wr, b < nb ? at : kOutside, 0);
-    bload16(w[1], wr, b + 1 < nb ? at + 16u : kOutside, 0);
-    sb = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(sr, b < nb ? st : kOutside, 0, 0) |
-         (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(sr, b + 1 < nb ? st + 1u : kOutside, 0, 0) << 8;
-  };
-
-  if constexpr (MX) {
-    // rows in MXFP4: as small as the weights, read by every wave directly
-    const int64_t arow = lr < u.M ? source_row(g, u.r0 + lr) : -1;
-    for (int s = wv; s < steps; s += 4) {
-      uint32_t w[RT][2][4], sb[RT];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) load_w(s, rt, w[rt], sb[rt]);
+    for (int rt = 0; rt < RT; ++rt) {
+      const uint32_t row = (uint32_t)(n0 + 16 * rt + lr);
+      const uint32_t at = row * wld + 16u * b, st = row * (uint32_t)nb + (uint32_t)b;
+      bload16(w[d][rt][0], wr, b < nb ? at : kOutside, 0);
+      bload16(w[d][rt][1], wr, b + 1 < nb ? at + 16u : kOutside, 0);
+      if constexpr (EV)
+        sb[d][rt] = bload_u16(sr, b < nb ? st : kOutside, 0);
+      else
+        sb[d][rt] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(sr, b < nb ? st : kOutside, 0, 0) |
+                    (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(sr, b + 1 < nb ? st + 1u : kOutside, 0, 0) << 8;
+    }
+  };
+  f32x4 acc[RT];
+  const int64_t arow = MX && lr < u.M ? source_row(g, u.r0 + lr) : -1;
+  // step s of the call, S steps from s0 on being in LDS (bf16 rows)
+  auto multiply = [&](int d, int s, int s0, int S) {
+    if constexpr (MX) {
+      // rows in MXFP4: as small as the weights, read by every wave directly
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int b = s * 8 + 2 * lq + h;
@@ -73,23 +80,26 @@ __device__ __forceinline__ void thin_tile(const MatmulArgs& g, const RowUnit& u,
         const i32x8 X = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          const i32x8 W = {(int)w[rt][h][0], (int)w[rt][h][1], (int)w[rt][h][2], (int)w[rt][h][3], 0, 0, 0, 0};
-          acc[rt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(W, X, acc[rt], 4, 4, 0, (int)(sb[rt] >> (8 * h)), 0, (int)xs);
+          const i32x8 W = {(int)w[d][rt][h][0], (int)w[d][rt][h][1], (int)w[d][rt][h][2], (int)w[d][rt][h][3], 0, 0, 0, 0};
+          acc[rt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(W, X, acc[rt], 4, 4, 0, (int)(sb[d][rt] >> (8 * h)), 0, (int)xs);
         }
       }
-    }
-  } else {
-    // steps per slab: a multiple of the four waves, or all of them
-    const int fit = (kThinLds / u.M - 16) / 512, slab = fit >= steps ? steps : fit & ~3;
-    for (int s0 = 0; s0 < steps; s0 += slab) {
-      const int S = min(slab, steps - s0);
-      // the wave's first codes are on their way while the rows are staged
-      uint32_t w[RT][2][4], sb[RT];
-      if (wv < S) {
+    } else {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) load_w(s0 + wv, rt, w[rt], sb[rt]);
-      }
-      if (s0 > 0) __syncthreads();
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // lanes past the rows repeat the last one; their results are dropped
+          const bf16x8 x = __builtin_bit_cast(bf16x8, lds_read16(lds + slab_at(min(lr, u.M - 1), S, (s - s0) * 32 + (2 * lq + h) * 4 + i)));
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            acc[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                bf16_of(w[d][rt][h][i], __uint_as_float((sb[d][rt] >> (8 * h)) << 23)), x, acc[rt], 0, 0, 0);
+        }
+    }
+  };
+  auto stage = [&](int s0, int S) {
+    if constexpr (!MX) {
       for (int i = tid; i < u.M * S * 32; i += 256) {
         const int r = i / (S * 32), c = i - r * (S * 32), k = s0 * 256 + c * 8;
         const int64_t src = source_row(g, u.r0 + r);
@@ -98,57 +108,85 @@ __device__ __forceinline__ void thin_tile(const MatmulArgs& g, const RowUnit& u,
         lds_write16(lds + slab_at(r, S, c), v);
       }
       __syncthreads();
-      for (int s = wv; s < S; s += 4) {
-        uint32_t wn[RT][2][4], sn[RT];
-        if (s + 4 < S) {
+    }
+  };
+  // steps per slab: all of them, or a multiple of the four waves
+  const int fit = MX ? steps : (kThinLds / u.M - 16) / 512, slab = fit >= steps ? steps : fit & ~3;
+  const bool vec = g.ldo % 4 == 0;
+  auto first_steps = [&](int n0, int s0, int S) {
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) load_w(s0 + s + 4, rt, wn[rt], sn[rt]);
-        }
+    for (int d = 0; d < D; ++d)
+      if (wv + 4 * d < S) load_w(d, n0, s0 + wv + 4 * d);
+  };
+  if (slab == steps) {
+    first_steps(tile * 16 * RT, 0, steps);
+    stage(0, steps);
+  }
+  for (int t = tile; t < tile + tiles; ++t) {
+    const int n0 = t * 16 * RT;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+    for (int rt = 0; rt < RT; ++rt) acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < steps; s0 += slab) {
+      const int S = min(slab, steps - s0);
+      if (slab != steps) {
+        first_steps(n0, s0, S);
+        __syncthreads();   // the last slab is read
+        stage(s0, S);
+      }
+      for (int s = s0 + wv; s < s0 + S; s += 4 * D) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            bf16x8 A[RT];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) A[rt] = bf16_of(w[rt][h][i], __uint_as_float((sb[rt] >> (8 * h)) << 23));
-            // lanes past the rows repeat the last one; their results are dropped
-            const bf16x8 x = __builtin_bit_cast(bf16x8, lds_read16(lds + slab_at(min(lr, u.M - 1), S, s * 32 + (2 * lq + h) * 4 + i)));
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) acc[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[rt], x, acc[rt], 0, 0, 0);
+        for (int d = 0; d < D; ++d) {
+          if (s + 4 * d < s0 + S) {
+            multiply(d, s + 4 * d, s0, S);
+            if (s + 4 * (d + D) < s0 + S) load_w(d, n0, s + 4 * (d + D));
           }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          sb[rt] = sn[rt];
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[rt][h][i] = wn[rt][h][i];
         }
       }
     }
-  }
-  // the waves' parts, added in order
-  static_assert(4 * RT * 1024 <= kThinLds, "the parts fit");
-  __syncthreads();
+    // the next tile's first steps
+    if (slab == steps && t + 1 < tile + tiles) first_steps(n0 + 16 * RT, 0, steps);
+    // the waves' parts, added in order
 #pragma unroll
-  for (int t = 0; t < RT; ++t) lds_write16(lds + ((wv * RT + t) * 64 + lane) * 16, __builtin_bit_cast(u32x4, acc[t]));
-  __syncthreads();
-  const bool vec = g.ldo % 4 == 0;
-  for (int t = wv; t < RT; t += 4) {
-    f32x4 v = __builtin_bit_cast(f32x4, lds_read16(lds + (t * 64 + lane) * 16));
+    for (int i = 0; i < RT; ++i) lds_write16(parts + ((wv * RT + i) * 64 + lane) * 16, __builtin_bit_cast(u32x4, acc[i]));
+    __syncthreads();
+    for (int i = wv; i < RT; i += 4) {
+      f32x4 v = __builtin_bit_cast(f32x4, lds_read16(parts + (i * 64 + lane) * 16));
 #pragma unroll
-    for (int p = 1; p < 4; ++p) v += __builtin_bit_cast(f32x4, lds_read16(lds + ((p * RT + t) * 64 + lane) * 16));
-    if (lr < u.M) store4(g, vec, u.r0 + lr, n0 + 16 * t + 4 * lq, g.N, v);
+      for (int p = 1; p < 4; ++p) v += __builtin_bit_cast(f32x4, lds_read16(parts + ((p * RT + i) * 64 + lane) * 16));
+      if (lr < u.M) store4(g, vec, u.r0 + lr, n0 + 16 * i + 4 * lq, g.N, v);
+    }
+    if (t + 1 < tile + tiles) __syncthreads();   // the parts are read
   }
 }
 
-template <bool MX, int RT>
-__global__ void __launch_bounds__(256) mx_matmul_thin_kernel(MatmulArgs g, int nt) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kThinLds];
-  const int ub = blockIdx.x / nt, tile = blockIdx.x - ub * nt;
+template <bool MX, int RT, bool EV>
+__global__ void __launch_bounds__(256) mx_matmul_thin_kernel(MatmulArgs g, int nt, int per) {
+  __shared__ __attribute__((aligned(16))) uint8_t rows[MX ? 16 : kThinLds], parts[4 * RT * 1024];
+  const int runs = (nt + per - 1) / per;
+  const int ub = blockIdx.x / runs, tile = (blockIdx.x - ub * runs) * per;
   const RowUnit u = find_unit(g.offsets, g.E, g.R, kThinRows, ub);
   if (u.M <= 0) return;
-  thin_tile<MX, RT>(g, u, tile * 16 * RT, (lds8_t*)smem);
+  thin_tiles<MX, RT, EV>(g, u, tile, min(per, nt - tile), (lds8_t*)rows, (lds8_t*)parts);
+}
+
+template <bool MX>
+void launch_thin(const MatmulArgs& g, hipStream_t s) {
+  const long units = max_units(g, kThinRows);
+  // 64 outputs a tile (a row's inputs are then read for four row tiles) where
+  // that leaves every CU several, else 32 or 16; with many tiles, four to a
+  // workgroup, which looks its rows up and brings them into LDS once
+  const int rt = units * ((g.N + 63) / 64) >= 1024 ? 4 : units * ((g.N + 31) / 32) >= 512 ? 2 : 1;
+  const int nt = (g.N + 16 * rt - 1) / (16 * rt);
+  const int per = units * nt >= 16384 ? 4 : units * nt >= 8192 ? 2 : 1;
+  const dim3 grid((unsigned)(units * ((nt + per - 1) / per)));
+  auto go = [&](auto RT) {
+    constexpr int r = decltype(RT)::value;
+    if (g.K % 64 == 0) hipLaunchKernelGGL((mx_matmul_thin_kernel<MX, r, true>), grid, dim3(256), 0, s, g, nt, per);
+    else hipLaunchKernelGGL((mx_matmul_thin_kernel<MX, r, false>), grid, dim3(256), 0, s, g, nt, per);
+  };
+  if (rt == 4) go(std::integral_constant<int, 4>{});
+  else if (rt == 2) go(std::integral_constant<int, 2>{});
+  else go(std::integral_constant<int, 1>{});
 }
 
 // ---------------------------------------------------------------------------
@@ -237,14 +275,8 @@ hipError_t launch_mx_matmul(const MatmulArgs& g, bool a_mxfp4, hipStream_t s) {
   const int64_t span = (g.index ? (int64_t)g.a_rows : kFatRows) * ldb;
   if (g.R >= 8 * (int64_t)g.E && (int64_t)g.R * g.N >= 64 * 256 * 256 && span < (int64_t)kOutside)
     return a_mxfp4 ? launch_mx_matmul4_large(g, s) : launch_mx_matmul_large(g, s);
-  const long units = max_units(g, kThinRows);
-  // 64 outputs a workgroup (a row's inputs are then read for four row tiles)
-  // where that leaves every CU several, else 32 or 16
-  const int rt = units * ((g.N + 63) / 64) >= 1024 ? 4 : units * ((g.N + 31) / 32) >= 512 ? 2 : 1;
-  const int nt = (g.N + 16 * rt - 1) / (16 * rt);
-  auto* k = a_mxfp4 ? (rt == 4 ? mx_matmul_thin_kernel<true, 4> : rt == 2 ? mx_matmul_thin_kernel<true, 2> : mx_matmul_thin_kernel<true, 1>)
-                    : (rt == 4 ? mx_matmul_thin_kernel<false, 4> : rt == 2 ? mx_matmul_thin_kernel<false, 2> : mx_matmul_thin_kernel<false, 1>);
-  hipLaunchKernelGGL(k, dim3((unsigned)(units * nt)), dim3(256), 0, s, g, nt);
+  if (a_mxfp4) launch_thin<true>(g, s);
+  else launch_thin<false>(g, s);
   return hipGetLastError();
 }
 

@@ -97,21 +97,19 @@ size_t carve_balance(const moe_balance_config& c, void* base, BalanceArgs* a) {
     off = round_up(off + bytes, kAlign);
     return o;
   };
-  const size_t o_ticket = take(sizeof(uint32_t));
   const size_t parts = (size_t)c.n_seq * balance_slices(c.n_experts);
   const size_t o_loss = take(parts * sizeof(double));
-  const size_t o_picks = take(parts * sizeof(int32_t));
   const size_t o_p = take(slots * E * sizeof(float));
   const size_t o_c = take(slots * E * sizeof(int32_t));
   const size_t o_n = take(slots * sizeof(int32_t));
+  const size_t o_k = take(slots * sizeof(int32_t));
   if (a) {
     char* b = static_cast<char*>(base);
-    a->ticket = reinterpret_cast<uint32_t*>(b + o_ticket);
     a->seq_loss = reinterpret_cast<double*>(b + o_loss);
-    a->seq_picks = reinterpret_cast<int32_t*>(b + o_picks);
     a->part_p = reinterpret_cast<float*>(b + o_p);
     a->part_c = reinterpret_cast<int32_t*>(b + o_c);
     a->part_n = reinterpret_cast<int32_t*>(b + o_n);
+    a->part_k = reinterpret_cast<int32_t*>(b + o_k);
   }
   return off;
 }

@@ -50,12 +50,11 @@ struct BalanceArgs {
   bool sigmoid, bf16;
   float coef;
   // workspace of the forward pass
-  uint32_t* ticket;         // [1]
   double* seq_loss;         // [S][slices]
-  int32_t* seq_picks;       // [S][slices]
   float* part_p;            // [slots][E]
   int32_t* part_c;          // [slots][E]
-  int32_t* part_n;          // [slots]
+  int32_t* part_n;          // [slots] routed tokens
+  int32_t* part_k;          // [slots] picks
 };
 // Token chunks of the forward pass: one partial sum per (chunk, sequence)
 // pair that share a token, at slot chunk + sequence.
