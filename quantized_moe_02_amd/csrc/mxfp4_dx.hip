@@ -203,38 +203,35 @@ __device__ __forceinline__ void dx_tile(const MatmulArgs& g, const FatItem& it, 
     static_for<3>([&](auto J) {
       if (kb + decltype(J)::value < nkb) block(J, kb + decltype(J)::value);
     });
-  __builtin_amdgcn_s_waitcnt(0);   // the loads past the end
-
-  const int col = k0 + wn * 128 + 32 * lq;
-  if (col >= g.K) return;
-  const bool vec = g.ldo % (g.out_bf16 ? 8 : 4) == 0;
+  // every wave's reads and loads are done: LDS takes the results, a wave's
+  // 16 rows x 128 columns at a time
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  lds8_t* t = (lds8_t*)(wv < 4 ? lds.dy[0] : lds.dy[1]) + (wv & 3) * (16 * (256 + 16));
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
-    const int row = (wt * CT + c) * 16 + lr;
-    if (row >= it.M) continue;
-    const int64_t at = (int64_t)(it.r0 + row) * g.ldo + col;
+    const int row0 = (wt * CT + c) * 16, rows = min(it.M - row0, 16);
+    if (g.out_bf16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (g.out_bf16) {
-        __bf16* o = static_cast<__bf16*>(g.out) + at + 8 * i;
-        bf16x8 v;
+      for (int i = 0; i < 4; ++i)
+        lds_write16(t + lr * 272 + lq * 64 + i * 16,
+                    u32x4{pack_bf16(acc[0][c][i], acc[1][c][i]), pack_bf16(acc[2][c][i], acc[3][c][i]),
+                          pack_bf16(acc[4][c][i], acc[5][c][i]), pack_bf16(acc[6][c][i], acc[7][c][i])});
+      store_rows<256>(g, t, rows, it.r0 + row0, k0 + wn * 128, g.K);
+    } else {
+      // 64 columns at a time: lanes lq 0 and 1, then 2 and 3
 #pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] = (__bf16)acc[t][c][i];
-        if (vec) {
-          *reinterpret_cast<bf16x8*>(o) = v;
-        } else {
+      for (int h = 0; h < 2; ++h) {
+        if ((lq >> 1) == h) {
 #pragma unroll
-          for (int t = 0; t < 8; ++t) o[t] = v[t];
+          for (int i = 0; i < 4; ++i) {
+            lds_write16(t + lr * 272 + (lq & 1) * 128 + i * 32,
+                        __builtin_bit_cast(u32x4, f32x4{acc[0][c][i], acc[1][c][i], acc[2][c][i], acc[3][c][i]}));
+            lds_write16(t + lr * 272 + (lq & 1) * 128 + i * 32 + 16,
+                        __builtin_bit_cast(u32x4, f32x4{acc[4][c][i], acc[5][c][i], acc[6][c][i], acc[7][c][i]}));
+          }
         }
-      } else {
-        float* o = static_cast<float*>(g.out) + at + 8 * i;
-        if (vec) {
-          reinterpret_cast<f32x4*>(o)[0] = f32x4{acc[0][c][i], acc[1][c][i], acc[2][c][i], acc[3][c][i]};
-          reinterpret_cast<f32x4*>(o)[1] = f32x4{acc[4][c][i], acc[5][c][i], acc[6][c][i], acc[7][c][i]};
-        } else {
-#pragma unroll
-          for (int t = 0; t < 8; ++t) o[t] = acc[t][c][i];
-        }
+        store_rows<256>(g, t, rows, it.r0 + row0, k0 + wn * 128 + h * 64, g.K);
       }
     }
   }

@@ -14,7 +14,7 @@ namespace qmoe {
 namespace {
 
 constexpr int kThinRows = 16;                   // rows of a unit
-constexpr int kThinLds = 16 * (4 * 512 + 16);   // four steps of them
+constexpr int kThinLds = kThinRows * 4 * 512;   // four steps of them
 
 // At most this many units for R rows of E experts.
 long max_units(const MatmulArgs& g, int BM) {
@@ -26,16 +26,18 @@ long max_units(const MatmulArgs& g, int BM) {
 // outputs.  A step is 256 inputs, a line of a row's codes: lane (lr, lq) takes
 // blocks 2 lq and 2 lq + 1 of row lr.  Wave w takes steps w, w + 4, ... of a
 // slab, the steps whose rows fit LDS (most calls have one slab, whose rows then
-// stay for every tile).  D of a wave's steps are in flight.
+// stay for every tile).  Two of a wave's steps are in flight: with three or
+// four, one token's gate and up (8 experts) took 24.3 and 27.6 us instead of
+// 23.4, the registers costing more waves than the loads gain.
 // ---------------------------------------------------------------------------
-// 16-byte chunk c (8 bf16 inputs) of row r of a slab of S steps: rows of 512 S
-// bytes, and 16 more, so that the rows of one operand read lie on distinct banks.
-__device__ __forceinline__ int slab_at(int r, int S, int c) { return r * (512 * S + 16) + c * 16; }
+// 16-byte chunk c (8 bf16 inputs) of row r of a slab of S steps, at c ^ r of its
+// row, so that the rows of one operand read lie on distinct banks.
+__device__ __forceinline__ int slab_at(int r, int S, int c) { return r * (512 * S) + (c ^ r) * 16; }
 
 // EV: an even number of blocks per row, whose scales come in pairs.
 template <bool MX, int RT, bool EV>
 __device__ __forceinline__ void thin_tiles(const MatmulArgs& g, const RowUnit& u, int tile, int tiles, lds8_t* lds, lds8_t* parts) {
-  constexpr int D = RT == 4 ? 2 : 3;
+  constexpr int D = 2;
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nb = g.K / kMxBlock, steps = (g.K + 255) / 256;
@@ -111,7 +113,7 @@ __device__ __forceinline__ void thin_tiles(const MatmulArgs& g, const RowUnit& u
     }
   };
   // steps per slab: all of them, or a multiple of the four waves
-  const int fit = MX ? steps : (kThinLds / u.M - 16) / 512, slab = fit >= steps ? steps : fit & ~3;
+  const int fit = MX ? steps : kThinLds / (u.M * 512), slab = fit >= steps ? steps : fit & ~3;
   const bool vec = g.ldo % 4 == 0;
   auto first_steps = [&](int n0, int s0, int S) {
 #pragma unroll
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(256) mx_matmul_thin_kernel(MatmulArgs g, int n
   __shared__ __attribute__((aligned(16))) uint8_t rows[MX ? 16 : kThinLds], parts[4 * RT * 1024];
   const int runs = (nt + per - 1) / per;
   const int ub = blockIdx.x / runs, tile = (blockIdx.x - ub * runs) * per;
-  const RowUnit u = find_unit(g.offsets, g.E, g.R, kThinRows, ub);
+  const RowUnit u = find_unit(g.offsets, g.E, g.R, kThinRows, ub, reinterpret_cast<int*>(parts));
   if (u.M <= 0) return;
   thin_tiles<MX, RT, EV>(g, u, tile, min(per, nt - tile), (lds8_t*)rows, (lds8_t*)parts);
 }
@@ -261,7 +263,7 @@ __device__ __forceinline__ void dx_thin_tile(const MatmulArgs& g, const RowUnit&
 __global__ void __launch_bounds__(256) mx_matmul_dx_thin_kernel(MatmulArgs g, int nt) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[kDxThinLds];
   const int ub = blockIdx.x / nt, tile = blockIdx.x - ub * nt;
-  const RowUnit u = find_unit(g.offsets, g.E, g.R, kThinRows, ub);
+  const RowUnit u = find_unit(g.offsets, g.E, g.R, kThinRows, ub, reinterpret_cast<int*>(smem));
   if (u.M <= 0) return;
   dx_thin_tile(g, u, tile * 256, (lds8_t*)smem);
 }

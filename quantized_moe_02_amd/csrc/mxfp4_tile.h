@@ -32,12 +32,13 @@ struct RowUnit {
 // i counts the units of expert i, a scan over the 256 threads finds the expert
 // that holds unit b.  Called by all 256 threads; offsets are clamped to
 // ascending values in [0, R], so no row outside the output is ever touched.
-__device__ __forceinline__ RowUnit find_unit(const int32_t* offsets, int E, int R, int BM, int b) {
+// `sh` is eight words of LDS, free again when it returns.
+__device__ __forceinline__ RowUnit find_unit(const int32_t* offsets, int E, int R, int BM, int b, int* sh) {
   if (!offsets) {
     const int r0 = b * BM;
     return RowUnit{0, r0, max(0, min(BM, R - r0))};
   }
-  __shared__ int wave_sum[4], hit[3];
+  int *wave_sum = sh, *hit = sh + 4;
   const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
   int lo = 0, cnt = 0;
   if (t < E) {
@@ -62,8 +63,10 @@ __device__ __forceinline__ RowUnit find_unit(const int32_t* offsets, int E, int 
     hit[2] = min(BM, cnt - k * BM);
   }
   __syncthreads();
-  return RowUnit{__builtin_amdgcn_readfirstlane(hit[0]), __builtin_amdgcn_readfirstlane(hit[1]),
-                 __builtin_amdgcn_readfirstlane(hit[2])};
+  const RowUnit found{__builtin_amdgcn_readfirstlane(hit[0]), __builtin_amdgcn_readfirstlane(hit[1]),
+                  __builtin_amdgcn_readfirstlane(hit[2])};
+  __syncthreads();
+  return found;
 }
 
 // Stores four consecutive outputs of one row (col % 4 == 0; vec: ldo % 4 == 0).
