@@ -175,11 +175,12 @@ template <bool MX>
 void launch_thin(const MatmulArgs& g, hipStream_t s) {
   const long units = max_units(g, kThinRows);
   // 64 outputs a tile (a row's inputs are then read for four row tiles) where
-  // that leaves every CU several, else 32 or 16; with many tiles, four to a
-  // workgroup, which looks its rows up and brings them into LDS once
+  // that leaves every CU several, else 32 or 16; with many tiles, two to a
+  // workgroup, which looks its rows up and brings them into LDS once (64 tokens,
+  // down projection: one 168 us, two 153, four 158)
   const int rt = units * ((g.N + 63) / 64) >= 1024 ? 4 : units * ((g.N + 31) / 32) >= 512 ? 2 : 1;
   const int nt = (g.N + 16 * rt - 1) / (16 * rt);
-  const int per = units * nt >= 16384 ? 4 : units * nt >= 8192 ? 2 : 1;
+  const int per = units * nt >= 8192 ? 2 : 1;
   const dim3 grid((unsigned)(units * ((nt + per - 1) / per)));
   auto go = [&](auto RT) {
     constexpr int r = decltype(RT)::value;
