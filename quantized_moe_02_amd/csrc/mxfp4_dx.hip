@@ -24,18 +24,19 @@ namespace qmoe {
 namespace {
 
 constexpr int kDxTerms = 64;   // terms of the sum per stage
+constexpr int kMidRows = 64;
 
 struct DxLds {
   uint8_t *dy[3], *cd[3], *sc[3];
 };
 
-template <int WT, int CT>
+template <int NW, int WT, int CT>
 __device__ __forceinline__ void dx_tile(const MatmulArgs& g, const FatItem& it, const DxLds& lds) {
-  constexpr int WN = 8 / WT, ROWS = 16 * CT * WT;
+  constexpr int WN = NW / WT, ROWS = 16 * CT * WT, THREADS = 64 * NW;
   constexpr int CB = 64 * WN;              // bytes of codes per weight row of the tile
   constexpr int SB = 4 * WN;               // scales per weight row of the tile
-  constexpr int DSLOTS = ROWS * 8, NA = (DSLOTS + kFatThreads - 1) / kFatThreads;
-  constexpr int NC = kDxTerms * CB / 16 / kFatThreads, NV = NA + NC;
+  constexpr int DSLOTS = ROWS * 8, NA = (DSLOTS + THREADS - 1) / THREADS;
+  constexpr int NC = kDxTerms * CB / 16 / THREADS, NV = NA + NC;
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wv % WN, wt = wv / WN;
@@ -44,14 +45,14 @@ __device__ __forceinline__ void dx_tile(const MatmulArgs& g, const FatItem& it, 
 
   // Every wave issues the same NV loads per block, which the waits count on;
   // slots past the tile's rows lie in the stage too.
-  static_assert(NA * kFatThreads * 16 <= 32768, "a stage holds every slot");
+  static_assert(NA * THREADS * 16 <= NW * 4096 && (NW == 8 || WT == 2), "a stage holds every slot");
   // dy: rows of 128 bytes, 16-byte chunk c of row r at c ^ (r / 2 mod 8)
   const uint8_t* abase = static_cast<const uint8_t*>(g.a) + (int64_t)it.r0 * g.lda * 2;
   const rsrc_t ar = make_rsrc(abase, kOutside);
   uint32_t aoff[NA];
 #pragma unroll
   for (int i = 0; i < NA; ++i) {
-    const int slot = i * kFatThreads + tid, row = slot >> 3, c = (slot & 7) ^ ((row >> 1) & 7);
+    const int slot = i * THREADS + tid, row = slot >> 3, c = (slot & 7) ^ ((row >> 1) & 7);
     aoff[i] = row < it.M ? (uint32_t)((int64_t)row * g.lda * 2) + 16u * c : kOutside;
   }
   const int ac = (tid & 7) ^ ((tid >> 4) & 7);   // this thread's chunk, the same for each load
@@ -66,7 +67,7 @@ __device__ __forceinline__ void dx_tile(const MatmulArgs& g, const FatItem& it, 
   uint32_t coff[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    const int slot = i * kFatThreads + tid;
+    const int slot = i * THREADS + tid;
     const int jr = slot / (CB / 16), p = slot % (CB / 16);       // row and chunk in LDS
     const int j = WN == 4 ? jr : jr ^ ((jr >> 4) & 1);
     const int u = WN == 4 ? ((p >> 2) ^ (j >> 3)) & 3 : ((p >> 2) ^ (j >> 3)) & 1;
@@ -98,10 +99,10 @@ __device__ __forceinline__ void dx_tile(const MatmulArgs& g, const FatItem& it, 
   };
   auto issue_a = [&](auto P, int kb, int i) {
     const uint32_t off = kb * kDxTerms + ac * 8 >= g.N ? kOutside : aoff[i] + (uint32_t)kb * (kDxTerms * 2);
-    to_lds16(ar, lds.dy[decltype(P)::value] + (i * kFatThreads + wv * 64) * 16, off);
+    to_lds16(ar, lds.dy[decltype(P)::value] + (i * THREADS + wv * 64) * 16, off);
   };
   auto issue_c = [&](auto P, int kb, int i) {
-    to_lds16(wr, lds.cd[decltype(P)::value] + (i * kFatThreads + wv * 64) * 16,
+    to_lds16(wr, lds.cd[decltype(P)::value] + (i * THREADS + wv * 64) * 16,
              coff[i] + (uint32_t)kb * (kDxTerms * (uint32_t)(g.K / 2)));
   };
 
@@ -207,7 +208,9 @@ __device__ __forceinline__ void dx_tile(const MatmulArgs& g, const FatItem& it, 
   // 16 rows x 128 columns at a time
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  lds8_t* t = (lds8_t*)(wv < 4 ? lds.dy[0] : lds.dy[1]) + (wv & 3) * (16 * (256 + 16));
+  lds8_t* t;
+  if constexpr (NW == 8) t = (lds8_t*)(wv < 4 ? lds.dy[0] : lds.dy[1]) + (wv & 3) * (16 * (256 + 16));
+  else t = (lds8_t*)(wv < 1 ? lds.dy[0] : wv < 2 ? lds.dy[1] : wv < 3 ? lds.dy[2] : lds.cd[0]);
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
     const int row0 = (wt * CT + c) * 16, rows = min(it.M - row0, 16);
@@ -245,17 +248,40 @@ __global__ void __launch_bounds__(kFatThreads, 2) mx_matmul_dx_fat_kernel(Matmul
   if (!find_item(g.offsets, g.E, g.R, ntw, ntn, it)) return;
   const DxLds lds{{dy0, dy1, dy2}, {cd0, cd1, cd2}, {sc0, sc1, sc2}};
   if (it.wide) {
-    if (it.M > 192) dx_tile<4, 4>(g, it, lds);
-    else dx_tile<4, 3>(g, it, lds);
+    if (it.M > 192) dx_tile<8, 4, 4>(g, it, lds);
+    else dx_tile<8, 4, 3>(g, it, lds);
   } else {
-    if (it.M > 96) dx_tile<2, 4>(g, it, lds);
-    else if (it.M > 64) dx_tile<2, 3>(g, it, lds);
-    else if (it.M > 32) dx_tile<2, 2>(g, it, lds);
-    else dx_tile<2, 1>(g, it, lds);
+    if (it.M > 96) dx_tile<8, 2, 4>(g, it, lds);
+    else if (it.M > 64) dx_tile<8, 2, 3>(g, it, lds);
+    else if (it.M > 32) dx_tile<8, 2, 2>(g, it, lds);
+    else dx_tile<8, 2, 1>(g, it, lds);
   }
 }
 
+// Results too few to give every CU an item of 256 x 256: 256 columns x 64 rows
+// on four waves, three workgroups per CU.  8 experts, 4096 rows, 512 x 4096: 32
+// us, in units of 16 rows 70, in items of 256 x 256 40.  A wave alone on its SIMD
+// has an instruction of its conversions issued every 9 cycles, two together one
+// every 5: a workgroup alone on its CU takes 0.78 us per 64 terms.
+__global__ void __launch_bounds__(256, 3) mx_matmul_dx_mid_kernel(MatmulArgs g, int nt) {
+  __shared__ __attribute__((aligned(16))) uint8_t dy0[8192], dy1[8192], dy2[8192];
+  __shared__ __attribute__((aligned(16))) uint8_t cd0[8192], cd1[8192], cd2[8192];
+  __shared__ __attribute__((aligned(16))) uint8_t sc0[512], sc1[512], sc2[512];
+  FatItem it;
+  if (!find_item<kMidRows>(g.offsets, g.E, g.R, nt, nt, it)) return;
+  const DxLds lds{{dy0, dy1, dy2}, {cd0, cd1, cd2}, {sc0, sc1, sc2}};
+  if (it.wide) dx_tile<4, 2, 2>(g, it, lds);
+  else dx_tile<4, 2, 1>(g, it, lds);
+}
+
 }  // namespace
+
+hipError_t launch_mx_matmul_dx_mid(const MatmulArgs& g, hipStream_t s) {
+  const int nt = (g.K + 255) / 256;
+  const dim3 grid((unsigned)(((long)g.R / kMidRows + std::min(g.E, g.R)) * nt));
+  hipLaunchKernelGGL(mx_matmul_dx_mid_kernel, grid, dim3(256), 0, s, g, nt);
+  return hipGetLastError();
+}
 
 hipError_t launch_mx_matmul_dx_large(const MatmulArgs& g, hipStream_t s) {
   const int ntw = (g.K + 255) / 256, ntn = (g.K + 511) / 512;

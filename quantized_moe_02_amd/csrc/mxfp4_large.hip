@@ -21,6 +21,8 @@ namespace {
 
 constexpr int kBlk = 128;                        // inputs per stage
 constexpr int kStage = kFatRows * kBlk * 2;      // 64 KB
+constexpr int kMidRows = 64, kMidOut = 128, kMidThreads = 256;
+constexpr int kMidStage = kMidRows * kBlk * 2;   // 16 KB
 
 struct LdsL {
   uint8_t *st0, *st1;   // stages: rows of 256 bytes, 16-byte chunk c of row r at c ^ (r mod 16)
@@ -32,24 +34,25 @@ static_assert(4 * 64 * (128 + 16) <= kStage, "half of the results fits");
 // SL: the scales of 16 blocks of an output are 16 aligned bytes (K % 128 ==
 // 0), which come into LDS one group ahead: a scale byte per lane costs the
 // address units as much as 16 bytes of codes.  Otherwise lanes load bytes.
-template <bool SL, int WT, int CT>
+// NW waves, NW / WT x WT; a wave's tile is 16 RT outputs x 16 CT rows.
+template <bool SL, int NW, int WT, int RT, int CT>
 __device__ __forceinline__ void large_tile(const MatmulArgs& g, const FatItem& it, const LdsL& lds) {
-  constexpr int WN = 8 / WT, RT = 4, ROWS = 16 * CT * WT;
-  constexpr int SLOTS = ROWS * 16, NA = (SLOTS + kFatThreads - 1) / kFatThreads;
+  constexpr int WN = NW / WT, ROWS = 16 * CT * WT, THREADS = 64 * NW, WOUT = 16 * RT;
+  constexpr int SLOTS = ROWS * 16, NA = (SLOTS + THREADS - 1) / THREADS;
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wv % WN, wt = wv / WN;
-  const int n0 = it.tile * (64 * WN);
+  const int n0 = it.tile * (WOUT * WN);
   const int nb = g.K / kMxBlock, nkb = (g.K + kBlk - 1) / kBlk;
 
-  // load i brings rows 32 i + tid / 16, this thread always the same chunk of its row
+  // load i brings rows THREADS / 16 i + tid / 16, this thread always the same chunk of its row
   const int chunk = (tid & 15) ^ ((tid >> 4) & 15);
   const int64_t ldb = g.lda * 2;
   const rsrc_t ar = make_rsrc(static_cast<const uint8_t*>(g.a) + (g.index ? 0 : (int64_t)it.r0 * ldb), kOutside);
   uint32_t aoff[NA];
 #pragma unroll
   for (int i = 0; i < NA; ++i) {
-    const int row = i * 32 + (tid >> 4);
+    const int row = i * (THREADS / 16) + (tid >> 4);
     const int64_t src = row < it.M ? (g.index ? source_row(g, it.r0 + row) : (int64_t)row) : (int64_t)-1;
     aoff[i] = src >= 0 ? (uint32_t)(src * ldb) + 16u * chunk : kOutside;
   }
@@ -57,15 +60,15 @@ __device__ __forceinline__ void large_tile(const MatmulArgs& g, const FatItem& i
   const int64_t erow = (int64_t)it.e * g.N;
   const uint32_t wld = (uint32_t)(g.K / 2);
   const rsrc_t wr = make_rsrc(g.w_codes + erow * wld, (uint32_t)g.N * wld);
-  const uint32_t woff = (uint32_t)(n0 + wn * 64 + lr) * wld + 16u * lq;
+  const uint32_t woff = (uint32_t)(n0 + wn * WOUT + lr) * wld + 16u * lq;
   const rsrc_t sr = make_rsrc(g.w_scale + erow * nb, (uint32_t)g.N * (uint32_t)nb);
-  const uint32_t soff = (uint32_t)(n0 + wn * 64 + (SL ? lane : lr)) * (uint32_t)nb + (SL ? 0u : (uint32_t)lq);
+  const uint32_t soff = (uint32_t)(n0 + (SL ? wv * 64 + lane : wn * WOUT + lr)) * (uint32_t)nb + (SL ? 0u : (uint32_t)lq);
 
   uint32_t wq[2][RT][4], wsc[2][RT];
   auto issue_a = [&](auto P, int kb, int i) {
-    if (i * kFatThreads + wv * 64 >= SLOTS) return;
+    if (i * THREADS + wv * 64 >= SLOTS) return;
     const bool past = !SL && kb * kBlk + chunk * 8 >= g.K;
-    to_lds16(ar, (decltype(P)::value ? lds.st1 : lds.st0) + (i * kFatThreads + wv * 64) * 16,
+    to_lds16(ar, (decltype(P)::value ? lds.st1 : lds.st0) + (i * THREADS + wv * 64) * 16,
              past ? kOutside : aoff[i] + (uint32_t)kb * (kBlk * 2));
   };
   auto issue_w = [&](auto P, int kb, int rt) {
@@ -78,13 +81,13 @@ __device__ __forceinline__ void large_tile(const MatmulArgs& g, const FatItem& i
   };
   auto issue_s = [&](int kb) {   // the scales of block kb's group, if it starts one
     if constexpr (SL) {
-      if (wt == 0 && (kb & 3) == 0)
-        to_lds16(sr, lds.ws + ((kb >> 2) & 1) * 8192 + wn * 1024, soff + (uint32_t)kb * 4u);
+      if (wv < WOUT * WN / 64 && (kb & 3) == 0)
+        to_lds16(sr, lds.ws + ((kb >> 2) & 1) * 8192 + wv * 1024, soff + (uint32_t)kb * 4u);
     }
   };
   auto read_s = [&](auto P, int kb) {
     if constexpr (SL) {
-      const uint8_t* b = lds.ws + ((kb >> 2) & 1) * 8192 + (wn * 64 + lr) * 16 + (kb & 3) * 4 + lq;
+      const uint8_t* b = lds.ws + ((kb >> 2) & 1) * 8192 + (wn * WOUT + lr) * 16 + (kb & 3) * 4 + lq;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) wsc[decltype(P)::value][rt] = b[rt * 256];
     }
@@ -167,8 +170,8 @@ __device__ __forceinline__ void large_tile(const MatmulArgs& g, const FatItem& i
   // every wave's reads and loads are done: LDS takes the results
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  lds8_t* t = (lds8_t*)(wv < 4 ? lds.st0 : lds.st1) + (wv & 3) * (64 * 144);
-  constexpr int HC = (CT + 1) / 2;   // column tiles at a time
+  constexpr int HC = (CT + 1) / 2, RB = 32 * RT;   // column tiles at a time, bytes of a row
+  lds8_t* t = (lds8_t*)(wv < NW / 2 ? lds.st0 : lds.st1) + (wv % (NW / 2)) * (HC * 16 * (RB + 16));
 #pragma unroll
   for (int c0 = 0; c0 < CT; c0 += HC) {
     const int row0 = (wt * CT + c0) * 16, rows = min(it.M - row0, HC * 16);
@@ -178,18 +181,18 @@ __device__ __forceinline__ void large_tile(const MatmulArgs& g, const FatItem& i
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
           if (c0 + c < CT)
-            lds_write8(t + (c * 16 + lr) * 144 + rt * 32 + lq * 8,
+            lds_write8(t + (c * 16 + lr) * (RB + 16) + rt * 32 + lq * 8,
                        u32x2{pack_bf16(acc[rt][c0 + c][0], acc[rt][c0 + c][1]), pack_bf16(acc[rt][c0 + c][2], acc[rt][c0 + c][3])});
-      store_rows<128>(g, t, rows, it.r0 + row0, n0 + wn * 64, g.N);
+      store_rows<RB>(g, t, rows, it.r0 + row0, n0 + wn * WOUT, g.N);
     } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {   // half of the outputs
 #pragma unroll
         for (int c = 0; c < HC; ++c)
 #pragma unroll
-          for (int rt = 0; rt < 2; ++rt)
-            if (c0 + c < CT) lds_write16(t + (c * 16 + lr) * 144 + rt * 64 + lq * 16, __builtin_bit_cast(u32x4, acc[2 * h + rt][c0 + c]));
-        store_rows<128>(g, t, rows, it.r0 + row0, n0 + wn * 64 + h * 32, g.N);
+          for (int rt = 0; rt < RT / 2; ++rt)
+            if (c0 + c < CT) lds_write16(t + (c * 16 + lr) * (RB + 16) + rt * 64 + lq * 16, __builtin_bit_cast(u32x4, acc[RT / 2 * h + rt][c0 + c]));
+        store_rows<RB>(g, t, rows, it.r0 + row0, n0 + wn * WOUT + h * (WOUT / 2), g.N);
       }
     }
   }
@@ -203,15 +206,33 @@ __global__ void __launch_bounds__(kFatThreads, 2) mx_matmul_large_kernel(MatmulA
   if (!find_item(g.offsets, g.E, g.R, ntw, ntn, it)) return;
   const LdsL lds{st0, st1, ws};
   if (it.wide) {
-    if (it.M > 192) large_tile<SL, 2, 8>(g, it, lds);
-    else large_tile<SL, 2, 6>(g, it, lds);
+    if (it.M > 192) large_tile<SL, 8, 2, 4, 8>(g, it, lds);
+    else large_tile<SL, 8, 2, 4, 6>(g, it, lds);
   } else {
-    if (it.M > 96) large_tile<SL, 1, 8>(g, it, lds);
-    else if (it.M > 64) large_tile<SL, 1, 6>(g, it, lds);
-    else if (it.M > 32) large_tile<SL, 1, 4>(g, it, lds);
-    else if (it.M > 16) large_tile<SL, 1, 2>(g, it, lds);
-    else large_tile<SL, 1, 1>(g, it, lds);
+    if (it.M > 96) large_tile<SL, 8, 1, 4, 8>(g, it, lds);
+    else if (it.M > 64) large_tile<SL, 8, 1, 4, 6>(g, it, lds);
+    else if (it.M > 32) large_tile<SL, 8, 1, 4, 4>(g, it, lds);
+    else if (it.M > 16) large_tile<SL, 8, 1, 4, 2>(g, it, lds);
+    else large_tile<SL, 8, 1, 4, 1>(g, it, lds);
   }
+}
+
+// Products too small to give every CU an item of 256 x 256: 128 outputs x 64
+// rows on four waves, three workgroups per CU.  Twice the LDS reads per MFMA,
+// but eight times the items: 512 rows, 4096 x 4096 in 29 us (600 TFLOP/s), where
+// units of 16 rows take 87, and 8 experts, 4096 rows, 512 x 4096 in 32 instead
+// of 100.  Bound by the latency of the next block's loads, where a CU has one
+// workgroup, else by the LDS.
+template <bool SL>
+__global__ void __launch_bounds__(kMidThreads, 2) mx_matmul_mid_kernel(MatmulArgs g, int nt) {
+  __shared__ __attribute__((aligned(16))) uint8_t st0[kMidStage], st1[kMidStage];
+  __shared__ __attribute__((aligned(16))) uint8_t ws[SL ? 8192 + kMidOut * 16 : 16];
+  FatItem it;
+  if (!find_item<kMidRows>(g.offsets, g.E, g.R, nt, nt, it)) return;
+  const LdsL lds{st0, st1, ws};
+  if (it.M > 32) large_tile<SL, 4, 1, 2, 4>(g, it, lds);
+  else if (it.M > 16) large_tile<SL, 4, 1, 2, 2>(g, it, lds);
+  else large_tile<SL, 4, 1, 2, 1>(g, it, lds);
 }
 
 }  // namespace
@@ -221,6 +242,14 @@ hipError_t launch_mx_matmul_large(const MatmulArgs& g, hipStream_t s) {
   const dim3 grid((unsigned)(((long)g.R / kFatRows + std::min(g.E, g.R)) * ntw));
   hipLaunchKernelGGL(g.K % kBlk == 0 ? mx_matmul_large_kernel<true> : mx_matmul_large_kernel<false>, grid,
                      dim3(kFatThreads), 0, s, g, ntw, ntn);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_matmul_mid(const MatmulArgs& g, hipStream_t s) {
+  const int nt = (g.N + kMidOut - 1) / kMidOut;
+  const dim3 grid((unsigned)(((long)g.R / kMidRows + std::min(g.E, g.R)) * nt));
+  hipLaunchKernelGGL(g.K % kBlk == 0 ? mx_matmul_mid_kernel<true> : mx_matmul_mid_kernel<false>, grid,
+                     dim3(kMidThreads), 0, s, g, nt);
   return hipGetLastError();
 }
 

@@ -7,6 +7,7 @@
 // lines per row, and the four waves of a workgroup split the sum and add their
 // parts up in LDS, in a fixed order.
 #include <algorithm>
+#include <cmath>
 
 #include "mxfp4_tile.h"
 
@@ -114,7 +115,6 @@ __device__ __forceinline__ void thin_tiles(const MatmulArgs& g, const RowUnit& u
   };
   // steps per slab: all of them, or a multiple of the four waves
   const int fit = MX ? steps : kThinLds / (u.M * 512), slab = fit >= steps ? steps : fit & ~3;
-  const bool vec = g.ldo % 4 == 0;
   auto first_steps = [&](int n0, int s0, int S) {
 #pragma unroll
     for (int d = 0; d < D; ++d)
@@ -155,7 +155,7 @@ __device__ __forceinline__ void thin_tiles(const MatmulArgs& g, const RowUnit& u
       f32x4 v = __builtin_bit_cast(f32x4, lds_read16(parts + (i * 64 + lane) * 16));
 #pragma unroll
       for (int p = 1; p < 4; ++p) v += __builtin_bit_cast(f32x4, lds_read16(parts + ((p * RT + i) * 64 + lane) * 16));
-      if (lr < u.M) store4(g, vec, u.r0 + lr, n0 + 16 * i + 4 * lq, g.N, v);
+      if (lr < u.M) store4(g, u.r0 + lr, n0 + 16 * i + 4 * lq, g.N, v);
     }
     if (t + 1 < tile + tiles) __syncthreads();   // the parts are read
   }
@@ -193,39 +193,44 @@ void launch_thin(const MatmulArgs& g, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// The gradient: 256 columns x up to 16 rows.  As in the kernel for many rows, a
+// The gradient: 128 CW columns x up to 16 rows.  As in the kernel for many rows, a
 // lane takes words of eight rows of the weights and regroups them along the
-// sum; here two words, 16 columns, so that a row's share is a whole line.  Wave
-// w takes every fourth step of 32 terms.
+// sum; here two words, 16 columns, so that a row's share is a whole line.  Four
+// waves take every fourth step of 32 terms.  Where that gives fewer than 128
+// workgroups their address units bound the call, 17 requests per step: half the
+// columns and twice the waves then (CW = 1, NW = 8), 4096 x 512 and one row 12.1
+// us instead of 19.6, but 64 experts, 32 rows, 4096 x 4096 (512 workgroups) 91
+// instead of 51.
 // ---------------------------------------------------------------------------
-constexpr int kDxThinLds = 64 * 1024;
-
+template <int CW, int NW>
 __device__ __forceinline__ void dx_thin_tile(const MatmulArgs& g, const RowUnit& u, int k0, lds8_t* lds) {
+  constexpr int NT = 8 * CW;   // tiles of 16 columns
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nb = g.K / kMxBlock, steps = g.N / 32;
-  f32x4 acc[16];
+  f32x4 acc[NT];
 #pragma unroll
-  for (int t = 0; t < 16; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int64_t erow = (int64_t)u.e * g.N;
   const rsrc_t wr = make_rsrc(g.w_codes + erow * (g.K / 2), (uint32_t)g.N * (uint32_t)(g.K / 2));
   const rsrc_t sr = make_rsrc(g.w_scale + erow * nb, (uint32_t)g.N * (uint32_t)nb);
-  const int k = k0 + 16 * lr;
+  const int k = k0 + 8 * CW * lr;
   const uint32_t wat = (uint32_t)(8 * lq) * (uint32_t)(g.K / 2) + (uint32_t)(k / 2);
   const uint32_t sat = (uint32_t)(8 * lq) * (uint32_t)nb + (uint32_t)(k / 32);
   // lanes past the rows repeat the last one
   const uint16_t* dy = static_cast<const uint16_t*>(g.a) + (int64_t)(u.r0 + min(lr, u.M - 1)) * g.lda + 8 * lq;
-  for (int s = wv; s < steps; s += 4) {
-    uint32_t w[8][2];
+  for (int s = wv; s < steps; s += NW) {
+    uint32_t w[8][CW];
     float sc[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t o = (uint32_t)(32 * s + j);
-      bload8(w[j], wr, k < g.K ? wat + o * (uint32_t)(g.K / 2) : kOutside, 0);
+      const uint32_t o = (uint32_t)(32 * s + j), at = k < g.K ? wat + o * (uint32_t)(g.K / 2) : kOutside;
+      if constexpr (CW == 2) bload8(w[j], wr, at, 0);
+      else w[j][0] = __builtin_amdgcn_raw_buffer_load_b32(wr, at, 0, 0);
       sc[j] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b8(sr, k < g.K ? sat + o * (uint32_t)nb : kOutside, 0, 0) << 23);
     }
     const bf16x8 B = *reinterpret_cast<const bf16x8*>(dy + 32 * s);
-    static_for<8>([&](auto T) {
+    static_for<NT / 2>([&](auto T) {
       constexpr int t = decltype(T)::value;
       union {
         uint32_t x[4];
@@ -242,53 +247,97 @@ __device__ __forceinline__ void dx_thin_tile(const MatmulArgs& g, const RowUnit&
       acc[2 * t + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi.v, B, acc[2 * t + 1], 0, 0, 0);
     });
   }
-  // the waves' parts, added in order; wave w takes tiles 4 w .. 4 w + 3
-  const bool vec = g.ldo % 4 == 0;
+  // the waves' parts, added in order; four tiles to each of the first waves
 #pragma unroll
-  for (int t = 0; t < 16; ++t) lds_write16(lds + ((wv * 16 + t) * 64 + lane) * 16, __builtin_bit_cast(u32x4, acc[t]));
+  for (int t = 0; t < NT; ++t) lds_write16(lds + ((wv * NT + t) * 64 + lane) * 16, __builtin_bit_cast(u32x4, acc[t]));
   __syncthreads();
+  if (4 * wv >= NT || lr >= u.M) return;
   f32x4 v[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     v[t] = __builtin_bit_cast(f32x4, lds_read16(lds + ((4 * wv + t) * 64 + lane) * 16));
 #pragma unroll
-    for (int p = 1; p < 4; ++p) v[t] += __builtin_bit_cast(f32x4, lds_read16(lds + ((p * 16 + 4 * wv + t) * 64 + lane) * 16));
+    for (int p = 1; p < NW; ++p) v[t] += __builtin_bit_cast(f32x4, lds_read16(lds + ((p * NT + 4 * wv + t) * 64 + lane) * 16));
   }
-  if (lr >= u.M) return;
-  // tile 4 wv + t, result row 4 lq + i: column 16 (4 lq + i) + 4 wv + t
+  // tile 4 wv + t, result row 4 lq + i: column NT (4 lq + i) + 4 wv + t
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    store4(g, vec, u.r0 + lr, k0 + 16 * (4 * lq + i) + 4 * wv, g.K, f32x4{v[0][i], v[1][i], v[2][i], v[3][i]});
+    store4(g, u.r0 + lr, k0 + NT * (4 * lq + i) + 4 * wv, g.K, f32x4{v[0][i], v[1][i], v[2][i], v[3][i]});
 }
 
-__global__ void __launch_bounds__(256) mx_matmul_dx_thin_kernel(MatmulArgs g, int nt) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kDxThinLds];
+template <int CW, int NW>
+__global__ void __launch_bounds__(64 * NW) mx_matmul_dx_thin_kernel(MatmulArgs g, int nt) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[NW * CW * 8192];
   const int ub = blockIdx.x / nt, tile = blockIdx.x - ub * nt;
   const RowUnit u = find_unit(g.offsets, g.E, g.R, kThinRows, ub, reinterpret_cast<int*>(smem));
   if (u.M <= 0) return;
-  dx_thin_tile(g, u, tile * 256, (lds8_t*)smem);
+  dx_thin_tile<CW, NW>(g, u, tile * (128 * CW), (lds8_t*)smem);
+}
+
+template <int CW, int NW>
+hipError_t launch_dx_thin(const MatmulArgs& g, hipStream_t s) {
+  const int nt = (g.K + 128 * CW - 1) / (128 * CW);
+  hipLaunchKernelGGL((mx_matmul_dx_thin_kernel<CW, NW>), dim3((unsigned)(max_units(g, kThinRows) * nt)), dim3(64 * NW), 0, s, g, nt);
+  return hipGetLastError();
+}
+
+
+// ---------------------------------------------------------------------------
+// The choice.  The offsets lie on the device, so the host goes by R / E rows per
+// expert and half a run more for each.  Measured both ways on log-uniform draws
+// (1 to 256 experts, 16 to 6144 outputs, 32 to 6144 inputs):
+//
+// - An item of 64 rows needs four rows per expert and 128 in all to be worth its
+//   place (256 experts, 1024 rows, 2048 x 1024: 64 us against 71 with few-row
+//   units; 8 experts, 32 rows, 4096 x 4096: 24 against 20), and items enough to
+//   make up for its slower start: 32 of them forwards (512 rows, 512 x 4096: 20
+//   against 23; 14 experts, 825 rows, 54 x 4768: 26 against 22), for the gradient
+//   as many as there are in 512 few-row units (8 experts, 4096 rows, 512 x 512:
+//   11 against 16; 1024 rows, 4096 x 512: 51 against 30).
+// - Items of 256 x 256, one to a CU, take two thirds of the time per result, but
+//   leave CUs idle in the last round of them: 4096 rows, 4096 x 4096, one expert
+//   (256 items), 109 us against 165; eight experts (more than 256) 175 against
+//   150.
+// ---------------------------------------------------------------------------
+double runs_of(const MatmulArgs& g, double rows) { return g.R / rows + (g.offsets ? 0.5 * g.E : 0.0); }
+
+// Whether items of 64 rows x 128 outputs, 1350 of which the chip ends in the time
+// of one item of 256 x 256, end before those.  Up to 128 rows per expert lie in
+// one run of the narrow form, 512 outputs wide, which takes less time, but not
+// less than half of it.
+bool mid_is_faster(const MatmulArgs& g, int outputs) {
+  const double rows = (double)g.R / g.E;
+  const double large = rows <= 128 ? std::ceil(g.E * std::ceil(outputs / 512.0) / 256) * std::max(rows, 64.0) / 128
+                                   : std::ceil(runs_of(g, 256) * std::ceil(outputs / 256.0) / 256);
+  return runs_of(g, 64) * std::ceil(outputs / 128.0) / 1350 < large;
 }
 
 }  // namespace
 
 hipError_t launch_mx_matmul(const MatmulArgs& g, bool a_mxfp4, hipStream_t s) {
-  // few rows per expert, or too few outputs to give a quarter of the CUs an
-  // item of 256 x 256: the thin kernel; sources past 32-bit offsets too
+  // sources past 32-bit offsets: the few-row kernel, which has 64-bit addresses
   const int64_t ldb = a_mxfp4 ? g.K / 2 : g.lda * 2;
   const int64_t span = (g.index ? (int64_t)g.a_rows : kFatRows) * ldb;
-  if (g.R >= 8 * (int64_t)g.E && (int64_t)g.R * g.N >= 64 * 256 * 256 && span < (int64_t)kOutside)
-    return a_mxfp4 ? launch_mx_matmul4_large(g, s) : launch_mx_matmul_large(g, s);
-  if (a_mxfp4) launch_thin<true>(g, s);
-  else launch_thin<false>(g, s);
+  const bool near = span < (int64_t)kOutside;
+  if (a_mxfp4) {
+    // sixteen items of 256 x 256, of eight rows per expert or more (8 experts, 256
+    // rows, 4096 x 4096: 26 us against 43; 8 items, 512 rows, 1024 x 4096, and fewer
+    // rows per expert alike within 1 us either way)
+    if (near && g.R >= 8 * (int64_t)g.E && (int64_t)g.R * g.N >= 16 * 256 * 256) return launch_mx_matmul4_large(g, s);
+    launch_thin<true>(g, s);
+    return hipGetLastError();
+  }
+  if (near && g.R >= 128 && g.R >= 4 * (int64_t)g.E && runs_of(g, 64) * std::ceil(g.N / 128.0) >= 32)
+    return mid_is_faster(g, g.N) ? launch_mx_matmul_mid(g, s) : launch_mx_matmul_large(g, s);
+  launch_thin<false>(g, s);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_matmul_dx(const MatmulArgs& g, hipStream_t s) {
-  if (g.R >= 8 * (int64_t)g.E && (int64_t)g.R * g.K >= 64 * 256 * 256 && kFatRows * g.lda * 2 < (int64_t)kOutside)
-    return launch_mx_matmul_dx_large(g, s);
-  const int nt = (g.K + 255) / 256;
-  hipLaunchKernelGGL(mx_matmul_dx_thin_kernel, dim3((unsigned)(max_units(g, kThinRows) * nt)), dim3(256), 0, s, g, nt);
-  return hipGetLastError();
+  if (g.R >= 4 * (int64_t)g.E && g.R >= 128 && kFatRows * g.lda * 2 < (int64_t)kOutside &&
+      runs_of(g, 16) * std::ceil(g.K / 256.0) >= 512)
+    return mid_is_faster(g, g.K) ? launch_mx_matmul_dx_mid(g, s) : launch_mx_matmul_dx_large(g, s);
+  return max_units(g, kThinRows) * ((g.K + 255) / 256) < 128 ? launch_dx_thin<1, 8>(g, s) : launch_dx_thin<2, 4>(g, s);
 }
 
 }  // namespace qmoe

@@ -30,7 +30,7 @@ struct RowUnit {
 
 // Unit `b` of the rows cut into runs of at most BM rows of one expert: thread
 // i counts the units of expert i, a scan over the 256 threads finds the expert
-// that holds unit b.  Called by all 256 threads; offsets are clamped to
+// that holds unit b.  Called by every thread, 256 or more; offsets are clamped to
 // ascending values in [0, R], so no row outside the output is ever touched.
 // `sh` is eight words of LDS, free again when it returns.
 __device__ __forceinline__ RowUnit find_unit(const int32_t* offsets, int E, int R, int BM, int b, int* sh) {
@@ -52,11 +52,12 @@ __device__ __forceinline__ RowUnit find_unit(const int32_t* offsets, int E, int 
     const int v = __shfl_up(inc, d, 64);
     if (lane >= d) inc += v;
   }
-  if (lane == 63) wave_sum[wv] = inc;
+  if (lane == 63 && wv < 4) wave_sum[wv] = inc;
   if (t == 0) hit[2] = 0;
   __syncthreads();
-  for (int i = 0; i < wv; ++i) inc += wave_sum[i];
-  if (b >= inc - u && b < inc) {
+  if (wv < 4)
+    for (int i = 0; i < wv; ++i) inc += wave_sum[i];
+  if (wv < 4 && b >= inc - u && b < inc) {
     const int k = b - (inc - u);
     hit[0] = t;
     hit[1] = lo + k * BM;
@@ -69,15 +70,17 @@ __device__ __forceinline__ RowUnit find_unit(const int32_t* offsets, int E, int 
   return found;
 }
 
-// Stores four consecutive outputs of one row (col % 4 == 0; vec: ldo % 4 == 0).
-__device__ __forceinline__ void store4(const MatmulArgs& g, bool vec, int row, int col, int cols, const f32x4& v) {
+// Stores four consecutive outputs of one row, at whatever alignment its pitch
+// leaves them (global stores need none on this target).
+__device__ __forceinline__ void store4(const MatmulArgs& g, int row, int col, int cols, const f32x4& v) {
   const int64_t i = (int64_t)row * g.ldo + col;
-  if (vec && col + 4 <= cols) {
+  if (col + 4 <= cols) {
     if (g.out_bf16) {
-      typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+      typedef __bf16 bf16x4 __attribute__((ext_vector_type(4), aligned(2)));
       *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(g.out) + i) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
     } else {
-      *reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + i) = v;
+      typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+      *reinterpret_cast<f32x4_any*>(static_cast<float*>(g.out) + i) = v;
     }
     return;
   }
@@ -127,9 +130,11 @@ struct FatItem {
   bool wide;   // 4 x 2 waves: 256 outputs; else 8 x 1: 512
 };
 
-// Items in order of expert, output tile, run of up to 256 rows, so that what an
+// Items in order of expert, output tile, run of up to RUN rows, so that what an
 // XCD works on at a time shares weights as well as rows; a last run of at most
-// 128 rows takes the narrow form, after the others.  All 512 threads call it.
+// half of that takes the narrow form, after the others.  Every thread calls it,
+// 256 of them or more.
+template <int RUN = kFatRows>
 __device__ __forceinline__ bool find_item(const int32_t* offsets, int E, int R, int ntw, int ntn, FatItem& it) {
   __shared__ int ws[4], hit[4], tot;
   const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
@@ -140,9 +145,9 @@ __device__ __forceinline__ bool find_item(const int32_t* offsets, int E, int R, 
     lo = min(max(offsets[t], 0), R);
     cnt = min(max(offsets[t + 1], lo), R) - lo;
   }
-  const int rem = cnt & (kFatRows - 1);
-  const int wide = cnt / kFatRows + (rem > kFatRows / 2);   // runs of the wide form
-  const int u = wide * ntw + (rem > 0 && rem <= kFatRows / 2 ? ntn : 0);
+  const int rem = cnt & (RUN - 1);
+  const int wide = cnt / RUN + (rem > RUN / 2);   // runs of the wide form
+  const int u = wide * ntw + (rem > 0 && rem <= RUN / 2 ? ntn : 0);
   int inc = u;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -162,8 +167,8 @@ __device__ __forceinline__ bool find_item(const int32_t* offsets, int E, int R, 
     const int k = w - (inc - u);
     const int run = k < wide * ntw ? k % wide : wide;
     hit[0] = t;
-    hit[1] = lo + run * kFatRows;
-    hit[2] = min(kFatRows, cnt - run * kFatRows);
+    hit[1] = lo + run * RUN;
+    hit[2] = min(RUN, cnt - run * RUN);
     hit[3] = k < wide * ntw ? k / wide : k - wide * ntw;
   }
   __syncthreads();
@@ -171,7 +176,7 @@ __device__ __forceinline__ bool find_item(const int32_t* offsets, int E, int R, 
   it.r0 = __builtin_amdgcn_readfirstlane(hit[1]);
   it.M = __builtin_amdgcn_readfirstlane(hit[2]);
   it.tile = __builtin_amdgcn_readfirstlane(hit[3]);
-  it.wide = it.M > kFatRows / 2;
+  it.wide = it.M > RUN / 2;
   return true;
 }
 
@@ -247,21 +252,23 @@ __device__ __forceinline__ void wave_sync() {
 // outputs of as many rows, 16-byte requests, where the vector cache takes a
 // line in one.  A wave lays its rows out at RB + 16 bytes each (rows 16 apart
 // in the bank row, so that neither side of the exchange has conflicts) and
-// writes them out RB bytes at a time.  `out_cols` bounds the columns.
+// writes them out RB bytes at a time, at whatever alignment the rows' pitch
+// leaves them.  `out_cols` bounds the columns.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2), may_alias));
 template <int RB>
 __device__ __forceinline__ void store_rows(const MatmulArgs& g, const lds8_t* t, int rows, int row0, int col0, int out_cols) {
   constexpr int LPR = RB / 16, RPI = 64 / LPR;   // lanes per row, rows per instruction
   const int lane = threadIdx.x & 63, c = lane % LPR;
   const int es = g.out_bf16 ? 2 : 4, per = 16 / es;
   const int col = col0 + c * per;
-  const bool vec = g.ldo % per == 0 && col + per <= out_cols;
+  const bool vec = col + per <= out_cols;
   uint8_t* o = static_cast<uint8_t*>(g.out) + ((int64_t)row0 * g.ldo + col) * es;
   wave_sync();
   for (int r = lane / LPR; r < rows; r += RPI) {
     const u32x4 v = lds_read16(t + r * (RB + 16) + c * 16);
     uint8_t* p = o + (int64_t)r * g.ldo * es;
     if (vec) {
-      *reinterpret_cast<u32x4*>(p) = v;
+      *reinterpret_cast<u32x4_any*>(p) = v;
     } else if (g.out_bf16) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)

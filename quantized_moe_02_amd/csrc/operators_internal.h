@@ -33,7 +33,9 @@ struct MatmulArgs {
 };
 hipError_t launch_mx_matmul(const MatmulArgs& a, bool a_mxfp4, hipStream_t s);
 hipError_t launch_mx_matmul_large(const MatmulArgs& a, hipStream_t s);
+hipError_t launch_mx_matmul_mid(const MatmulArgs& a, hipStream_t s);
 hipError_t launch_mx_matmul4_large(const MatmulArgs& a, hipStream_t s);
+hipError_t launch_mx_matmul_dx_mid(const MatmulArgs& a, hipStream_t s);
 hipError_t launch_mx_matmul_dx_large(const MatmulArgs& a, hipStream_t s);
 hipError_t launch_mx_matmul_dx(const MatmulArgs& a, hipStream_t s);
 

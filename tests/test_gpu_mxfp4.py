@@ -450,3 +450,46 @@ def test_offsets_that_do_not_ascend_stay_inside():
     assert (o[P.R:] == 77.0).all()
     want, mag = ref.grouped_matmul(P.a.double().numpy(), P.w64, [0, 12, 30])
     _close(o[:P.R], want, mag, 64, False)
+
+
+# Rows, outputs and sums that reach every kernel: items of 64 rows, of 256 x 256
+# and of 128 x 512, with runs of every length.
+MANY = [300, 0, 500, 290, 129, 170, 200, 257, 511, 640, 33, 193, 192, 800]
+NARROW = [(7 * i) % 129 for i in range(256)]
+FORMS = [([64, 3, 17, 33, 0, 130, 100, 81], 701, 160, 0), ([257, 1], 2050, 1056, 1), ([40] * 32, 513, 128, 2),
+         ([300, 16, 33], 1000, 288, 0), (MANY, 2555, 160, 1), (MANY, 2559, 256, 0), (NARROW, 1021, 96, 3)]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("gather", [0, 77])
+@pytest.mark.parametrize("counts,n,k,extra", FORMS)
+def test_forms(counts, n, k, extra, gather, out):
+    _run(Problem(counts, n, k, seed=n, extra=extra, gather=gather), "bf16", out)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("counts,n,k,extra", [
+    ([250, 1, 300, 64, 0, 885], 64, 1440, 0), ([33] * 64, 32, 1056, 1), ([700, 800], 352, 1504, 0),
+    (MANY, 96, 2528, 1), (NARROW, 64, 992, 0)])
+def test_forms_of_dx(counts, n, k, extra, out):
+    test_dx(counts, n, k, extra, out)
+
+
+@pytest.mark.parametrize("counts,n", [([200, 300], 1001), (MANY, 2555)])
+@pytest.mark.parametrize("k", [128, 352])
+def test_forms_keep_nan_in_place(counts, n, k):
+    P = Problem(counts, n, k, seed=k, gather=200)
+    c0 = counts[0]
+    P.index[3], P.index[c0 + 9] = -1, 200
+    P.index[7] = 7
+    P.a[7, k - 1] = float("nan")
+    P.ws[2 if counts[1] == 0 else 1, n - 1, 0] = 255
+    P.ws[0, 77, k // 32 - 1] = 255
+    o = torch.empty(P.R, n, device="cuda")
+    q.moe_mxfp4_matmul(P.a.cuda(), P.wq.cuda(), P.ws.cuda(), o, expert_offsets=P.offsets(), row_index=P.index.cuda())
+    e2 = slice(c0, c0 + max(counts[1], counts[2] if counts[1] == 0 else 0))
+    want = torch.zeros(P.R, n, dtype=torch.bool)
+    want[P.index == 7] = True
+    want[:c0, 77] = True
+    want[e2, n - 1] = True
+    assert torch.equal(torch.isnan(o).cpu(), want)
