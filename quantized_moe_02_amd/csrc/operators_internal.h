@@ -60,7 +60,7 @@ struct BalanceArgs {
 };
 // Token chunks of the forward pass: one partial sum per (chunk, sequence)
 // pair that share a token, at slot chunk + sequence.
-int balance_chunk(int T);
+int balance_chunk(int T, int S);
 // Workgroups per sequence of its second launch.
 int balance_slices(int E);
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);

@@ -226,3 +226,12 @@ def test_repeats_bit_for_bit_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(u, v) for u, v in zip(want, out)), i
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,k,S", [(60, 16, 4, 4), (64, 130, 8, 4), (128, 64, 8, 2), (100, 40, 2, 4), (40, 33, 3, 60),
+                                     (300, 256, 8, 90), (1500, 12, 2, 47)])
+def test_short_sequences(T, E, k, S, score):
+    """One workgroup, small chunks, sequences without a token."""
+    x, ids = _inputs(T, E, k, T + S, "f32", 0.1, 0.1)
+    _check(x, ids, _seqs(T, S, S), 1e-3, score)
