@@ -24,8 +24,14 @@ constexpr int kStage = kFatRows * kBlk * 2;      // 64 KB
 constexpr int kMidRows = 64, kMidOut = 128, kMidThreads = 256;
 constexpr int kMidStage = kMidRows * kBlk * 2;   // 16 KB
 
+// A wave's 16-byte reads go in four groups, one of them lanes 0 to 3, 12 to 15 and
+// 20 to 27 (two chunks, four apart, of eight rows each): with this they lie on
+// distinct banks, while at chunk c ^ r they would meet in pairs.
+__device__ __forceinline__ int turn(int r) { return (r & 15) ^ ((r << 1) & 8); }
+
 struct LdsL {
-  uint8_t *st0, *st1;   // stages: rows of 256 bytes, 16-byte chunk c of row r at c ^ (r mod 16)
+  // stages: rows of 256 bytes, 16-byte chunk c of row r at c ^ turn(r)
+  uint8_t *st0, *st1;
   uint8_t* ws;          // weight scales: two groups of 16 bytes per output
 };
 // the results take the place of the stages, four waves in each, half of a wave's rows at a time
@@ -46,7 +52,7 @@ __device__ __forceinline__ void large_tile(const MatmulArgs& g, const FatItem& i
   const int nb = g.K / kMxBlock, nkb = (g.K + kBlk - 1) / kBlk;
 
   // load i brings rows THREADS / 16 i + tid / 16, this thread always the same chunk of its row
-  const int chunk = (tid & 15) ^ ((tid >> 4) & 15);
+  const int chunk = (tid & 15) ^ turn(tid >> 4);
   const int64_t ldb = g.lda * 2;
   const rsrc_t ar = make_rsrc(static_cast<const uint8_t*>(g.a) + (g.index ? 0 : (int64_t)it.r0 * ldb), kOutside);
   uint32_t aoff[NA];
@@ -117,7 +123,7 @@ __device__ __forceinline__ void large_tile(const MatmulArgs& g, const FatItem& i
     auto read_b = [&](int j) {
 #pragma unroll
       for (int c = 0; c < HB; ++c)
-        B[j & 1][c] = *reinterpret_cast<const uint4*>(st + ((wt * CT + HB * (j % SUB) + c) * 16 + lr) * 256 + 16 * ((4 * lq + j / SUB) ^ lr));
+        B[j & 1][c] = *reinterpret_cast<const uint4*>(st + ((wt * CT + HB * (j % SUB) + c) * 16 + lr) * 256 + 16 * ((4 * lq + j / SUB) ^ turn(lr)));
     };
     read_b(0);
 #pragma unroll

@@ -119,18 +119,21 @@ __device__ __forceinline__ void tile4(const MatmulArgs& g, const FatItem& it, ld
   auto read = [&](uint32_t p, auto T, int kb, int i) {
     constexpr int t = decltype(T)::value, s = t & 1;
     const int at = ln * 128 + 16 * ((2 * t + lh) ^ ((ln >> 1) & 7));
-    const int grp = ((kb >> 1) & 1) * 4096 + (kb & 1) * 8 + 2 * t + lh + ln * 16;
+    // scales of steps t and t + 1, from an even step on: bytes 0 and 2 of the word,
+    // in the upper half of the wave bytes 1 and 3
+    constexpr int m = t >> 1;
+    const int grp = ((kb >> 1) & 1) * 4096 + (kb & 1) * 8 + 4 * m + ln * 16;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
       if (rt == i) {
         W[s][rt] = lds_read16(lds + kLdsW + p + (wn * RT + rt) * 4096 + at);
-        ws[s][rt] = lds[kLdsWs + grp + (wn * RT + rt) * 512];
+        if constexpr (s == 0) ws[m][rt] = lds_read4(lds + kLdsWs + grp + (wn * RT + rt) * 512) >> (8 * lh);
       }
 #pragma unroll
     for (int c = 0; c < CT; ++c)
       if (c == i) {
         A[s][c] = lds_read16(lds + kLdsA + p + (wt * CT + c) * 4096 + at);
-        as[s][c] = lds[kLdsAs + grp + (wt * CT + c) * 512];
+        if constexpr (s == 0) as[m][c] = lds_read4(lds + kLdsAs + grp + (wt * CT + c) * 512) >> (8 * lh);
       }
   };
   auto handover = [&]() {
@@ -176,7 +179,7 @@ __device__ __forceinline__ void tile4(const MatmulArgs& g, const FatItem& it, ld
             const u32x4 w = W[s][rt], x = A[s][c];
             const i32x8 wv8 = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
             const i32x8 xv8 = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
-            acc[rt][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv8, xv8, acc[rt][c], 4, 4, 0, (int)ws[s][rt], 0, (int)as[s][c]);
+            acc[rt][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv8, xv8, acc[rt][c], 4, 4, 2 * s, (int)ws[t >> 1][rt], 2 * s, (int)as[t >> 1][c]);
           }
         __builtin_amdgcn_sched_barrier(0);
       });

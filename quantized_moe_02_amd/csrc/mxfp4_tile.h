@@ -114,7 +114,6 @@ __device__ __forceinline__ bf16x8 bf16_of(uint32_t w, float s) {
 }
 
 constexpr int kFatRows = 256, kFatThreads = 512;
-constexpr int kStageBytes = 64 * 1024;
 
 // Work item of workgroup b: workgroups go round-robin over the 8 XCDs, and
 // each XCD's share is a contiguous range, so that the output tiles of one run
@@ -212,6 +211,10 @@ typedef __attribute__((address_space(3), may_alias)) u32x2 lds_u32x2;
 __device__ __forceinline__ uint32_t lds_addr(const lds8_t* p) { return (uint32_t)(uintptr_t)p; }
 __device__ __forceinline__ u32x4 lds_read16(const lds8_t* p) {
   return *reinterpret_cast<const lds_u32x4*>(p);
+}
+__device__ __forceinline__ uint32_t lds_read4(const lds8_t* p) {
+  typedef __attribute__((address_space(3), may_alias)) uint32_t word;
+  return *reinterpret_cast<const word*>(p);
 }
 __device__ __forceinline__ void lds_write16(lds8_t* p, u32x4 v) { *reinterpret_cast<lds_u32x4*>(p) = v; }
 __device__ __forceinline__ void lds_write8(lds8_t* p, u32x2 v) { *reinterpret_cast<lds_u32x2*>(p) = v; }
