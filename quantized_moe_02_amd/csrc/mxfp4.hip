@@ -9,7 +9,7 @@
 // they round to nearest even and saturate at 6.
 //
 // Both directions move bytes and are bound by HBM (small calls: by the
-// launch).  A lane takes a chunk of eight inputs, four lanes a block, so a
+// launch: a row of 6144 takes 1.5 us each way).  A lane takes a chunk of eight inputs, four lanes a block, so a
 // wave reads (16-bit types) and writes whole lines; the four meet in two
 // cross-lane maxima.  Magnitudes compare as integers, two 16-bit ones per
 // instruction.  Rows may start at any element: the loads are declared
@@ -181,15 +181,20 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(MxQuantArgs a, Chunk
   }
 }
 
-// Calls f(dtype, chunks per lane) as integral constants: four chunks in flight
-// per lane where that still gives every CU several workgroups, else one.
+// Calls f(dtype, chunks per lane) as integral constants.  One chunk per lane:
+// small workgroups in order suit HBM (fp32, 98304 x 2048: 191 us to codes and 173
+// back, 4.8 and 5.3 TB/s; with four in flight 205 and 219).  16-bit values that the
+// 256 MB cache behind L2 holds, eight workgroups to a CU and more, come faster than
+// a wave asks for them: four chunks in flight (fp16, 32768 x 2048, both ways: 53 us
+// against 58; bf16, 16384 x 6144: 94 against 90; fp16, 4099 x 2057: 12.1 against 11.2).
 template <class F>
 hipError_t dispatch(const MxQuantArgs& a, uint64_t chunks, F&& f) {
+  const bool four = chunks >= 1u << 21 && chunks <= 1u << 23;
   auto by_u = [&](auto D) {
-    if (chunks >= 256 * 4 * 1024) f(D, std::integral_constant<int, 4>{});
+    if (four) f(D, std::integral_constant<int, 4>{});
     else f(D, std::integral_constant<int, 1>{});
   };
-  if (a.dtype == MOE_DT_F32) by_u(std::integral_constant<int, MOE_DT_F32>{});
+  if (a.dtype == MOE_DT_F32) f(std::integral_constant<int, MOE_DT_F32>{}, std::integral_constant<int, 1>{});
   else if (a.dtype == MOE_DT_BF16) by_u(std::integral_constant<int, MOE_DT_BF16>{});
   else by_u(std::integral_constant<int, MOE_DT_F16>{});
   return hipGetLastError();

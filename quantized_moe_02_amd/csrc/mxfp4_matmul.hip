@@ -31,9 +31,10 @@ long max_units(const MatmulArgs& g, int BM) {
 // four, one token's gate and up (8 experts) took 24.3 and 27.6 us instead of
 // 23.4, the registers costing more waves than the loads gain.
 // ---------------------------------------------------------------------------
-// 16-byte chunk c (8 bf16 inputs) of row r of a slab of S steps, at c ^ r of its
-// row, so that the rows of one operand read lie on distinct banks.
-__device__ __forceinline__ int slab_at(int r, int S, int c) { return r * (512 * S) + (c ^ r) * 16; }
+// 16-byte chunk c (8 bf16 inputs) of row r of a slab of S steps, at c ^ r ^ (r / 2
+// and 4) of its row: the four groups of lanes in which a wave's 16-byte reads go
+// mix rows 0 to 3 and 12 to 15 of a chunk with rows 4 to 11 of the chunk eight on.
+__device__ __forceinline__ int slab_at(int r, int S, int c) { return r * (512 * S) + (c ^ r ^ ((r >> 1) & 4)) * 16; }
 
 // EV: an even number of blocks per row, whose scales come in pairs.
 template <bool MX, int RT, bool EV>
@@ -175,7 +176,9 @@ template <bool MX>
 void launch_thin(const MatmulArgs& g, hipStream_t s) {
   const long units = max_units(g, kThinRows);
   // 64 outputs a tile (a row's inputs are then read for four row tiles) where
-  // that leaves every CU several, else 32 or 16; with many tiles, two to a
+  // that leaves every CU several, else 32 or 16 (64 tokens, down projection: 317 us
+  // with 64, 331 with 32, 395 with 16; one token, gate and up: 24.4, 22.8, 27.8; 16
+  // rows, 4096 x 4096, one expert: 18.5, 14.8, 13.0); with many tiles, two to a
   // workgroup, which looks its rows up and brings them into LDS once (64 tokens,
   // down projection: one 168 us, two 153, four 158)
   const int rt = units * ((g.N + 63) / 64) >= 1024 ? 4 : units * ((g.N + 31) / 32) >= 512 ? 2 : 1;
