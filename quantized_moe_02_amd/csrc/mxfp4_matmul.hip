@@ -288,7 +288,7 @@ hipError_t launch_dx_thin(const MatmulArgs& g, hipStream_t s) {
 
 // ---------------------------------------------------------------------------
 // The choice.  The offsets lie on the device, so the host goes by R / E rows per
-// expert and half a run more for each.  Measured both ways on log-uniform draws
+// expert and part of a run more for each.  Measured both ways on log-uniform draws
 // (1 to 256 experts, 16 to 6144 outputs, 32 to 6144 inputs):
 //
 // - An item of 64 rows needs four rows per expert and 128 in all to be worth its
@@ -303,16 +303,18 @@ hipError_t launch_dx_thin(const MatmulArgs& g, hipStream_t s) {
 //   (256 items), 109 us against 165; eight experts (more than 256) 175 against
 //   150.
 // ---------------------------------------------------------------------------
-double runs_of(const MatmulArgs& g, double rows) { return g.R / rows + (g.offsets ? 0.5 * g.E : 0.0); }
+double runs_of(const MatmulArgs& g, double rows, double part = 0.5) {
+  return g.E == 1 ? std::ceil(g.R / rows) : g.R / rows + part * g.E;
+}
 
 // Whether items of 64 rows x 128 outputs, 1350 of which the chip ends in the time
 // of one item of 256 x 256, end before those.  Up to 128 rows per expert lie in
 // one run of the narrow form, 512 outputs wide, which takes less time, but not
-// less than half of it.
+// less than half of it; a last run in that form is half as many items.
 bool mid_is_faster(const MatmulArgs& g, int outputs) {
   const double rows = (double)g.R / g.E;
   const double large = rows <= 128 ? std::ceil(g.E * std::ceil(outputs / 512.0) / 256) * std::max(rows, 64.0) / 128
-                                   : std::ceil(runs_of(g, 256) * std::ceil(outputs / 256.0) / 256);
+                                   : std::ceil(runs_of(g, 256, 0.25) * std::ceil(outputs / 256.0) / 256);
   return runs_of(g, 64) * std::ceil(outputs / 128.0) / 1350 < large;
 }
 

@@ -204,7 +204,7 @@ def test_matmul(counts, n, k, extra, gather, act, out):
     _run(Problem(counts, n, k, seed=n + k, extra=extra, gather=gather), act, out)
 
 
-LARGE = [  # large enough for the tiles of 256 and 512 outputs; every count of column tiles
+LARGE = [  # large enough for the tiles of 256 outputs with MXFP4 rows; every count of column tiles
     ([1100], 4097, 128, 0, 0), ([300, 0, 129, 17, 33, 65, 97, 1, 257, 150], 4100, 160, 3, 77), ([513, 512], 4608, 672, 0, 0),
     ([190, 70, 200, 256, 90, 40, 10, 20], 5000, 1152, 0, 500), ([200, 5, 120, 255, 30], 6300, 2112, 2, 33)]
 
