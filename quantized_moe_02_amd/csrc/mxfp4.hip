@@ -14,6 +14,8 @@
 // cross-lane maxima.  Magnitudes compare as integers, two 16-bit ones per
 // instruction.  Rows may start at any element: the loads are declared
 // unaligned, which costs nothing where they are aligned.
+#include <algorithm>
+
 #include "operators_internal.h"
 #include "qmoe_device.h"
 
@@ -200,34 +202,48 @@ hipError_t dispatch(const MxQuantArgs& a, uint64_t chunks, F&& f) {
   return hipGetLastError();
 }
 
-ChunkMap chunk_map(const MxQuantArgs& a, uint64_t& chunks) {
+// Calls launch(part, map, chunks) for runs of whole rows of at most 2^31 chunks (a
+// row has 2^21 at most): a launch has to stay below 2^32 work items, and larger
+// matrices fit the card.
+template <class F>
+hipError_t by_rows(const MxQuantArgs& a, F&& launch) {
+  const int64_t nb = (a.cols + kMxBlock - 1) / kMxBlock;
   ChunkMap m;
-  m.cpr = (uint32_t)((a.cols + kMxBlock - 1) / kMxBlock * (kMxBlock / kChunk));
+  m.cpr = (uint32_t)(nb * (kMxBlock / kChunk));
   m.magic64 = ~0ull / m.cpr + 1;
   m.magic32 = ~0u / m.cpr + 1;
-  chunks = (uint64_t)a.rows * m.cpr;
-  return m;
+  const int64_t most = (int64_t)((1u << 31) / m.cpr), size = a.dtype == MOE_DT_F32 ? 4 : 2;
+  for (int64_t r = 0; r < a.rows; r += most) {
+    MxQuantArgs part = a;
+    part.x = static_cast<uint8_t*>(a.x) + r * a.ld * size;
+    part.codes = a.codes + r * nb * (kMxBlock / 2);
+    part.scale = a.scale + r * nb;
+    part.rows = std::min(most, a.rows - r);
+    const hipError_t e = launch(part, m, (uint64_t)part.rows * m.cpr);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
 
 hipError_t launch_mx_quantize(const MxQuantArgs& a, hipStream_t s) {
-  uint64_t chunks;
-  const ChunkMap m = chunk_map(a, chunks);
-  return dispatch(a, chunks, [&](auto D, auto U) {
-    constexpr int u = decltype(U)::value;
-    hipLaunchKernelGGL((mx_quantize_kernel<decltype(D)::value, u>), dim3((unsigned)((chunks + 256 * u - 1) / (256 * u))),
-                       dim3(256), 0, s, a, m, chunks);
+  return by_rows(a, [&](const MxQuantArgs& p, const ChunkMap& m, uint64_t chunks) {
+    return dispatch(p, chunks, [&](auto D, auto U) {
+      constexpr int u = decltype(U)::value;
+      hipLaunchKernelGGL((mx_quantize_kernel<decltype(D)::value, u>), dim3((unsigned)((chunks + 256 * u - 1) / (256 * u))),
+                         dim3(256), 0, s, p, m, chunks);
+    });
   });
 }
 
 hipError_t launch_mx_dequantize(const MxQuantArgs& a, hipStream_t s) {
-  uint64_t chunks;
-  const ChunkMap m = chunk_map(a, chunks);
-  return dispatch(a, chunks, [&](auto D, auto U) {
-    constexpr int u = decltype(U)::value;
-    hipLaunchKernelGGL((mx_dequantize_kernel<decltype(D)::value, u>), dim3((unsigned)((chunks + 256 * u - 1) / (256 * u))),
-                       dim3(256), 0, s, a, m, chunks);
+  return by_rows(a, [&](const MxQuantArgs& p, const ChunkMap& m, uint64_t chunks) {
+    return dispatch(p, chunks, [&](auto D, auto U) {
+      constexpr int u = decltype(U)::value;
+      hipLaunchKernelGGL((mx_dequantize_kernel<decltype(D)::value, u>), dim3((unsigned)((chunks + 256 * u - 1) / (256 * u))),
+                         dim3(256), 0, s, p, m, chunks);
+    });
   });
 }
 

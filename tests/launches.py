@@ -1,0 +1,58 @@
+"""Launches of the MXFP4 and router-balance operators without a GPU: their
+objects over tests/native/record_launches.cpp in place of the HIP runtime."""
+import collections
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import quantized_moe_02_amd as q
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CLANG = "/opt/rocm/llvm/bin/clang++"
+OBJECTS = ["operators_api", "mxfp4", "mxfp4_matmul", "mxfp4_large", "mxfp4_large4", "mxfp4_dx", "balance"]
+# kernel: its name and template arguments, as "mx_matmul_thin<false, 4, true>"
+Launch = collections.namedtuple("Launch", "kernel blocks threads rows x codes scale")
+
+
+def _kernel(mangled: str) -> str:
+    """Name and template arguments of a mangled `..._kernel` (booleans and
+    integers alone)."""
+    m = re.search(r"_GLOBAL__N_1\d+([a-z]\w*?)_kernel(?:I((?:L[bi]\d+E)+)E)?", mangled)
+    args = re.findall(r"L([bi])(\d+)E", m[2] or "")
+    text = ", ".join(("false", "true")[int(v)] if t == "b" else v for t, v in args)
+    return m[1] + (f"<{text}>" if text else "")
+
+
+class Recorder:
+    """The operators' entry points; call them as `lib.moe_...`, then take the
+    launches they made."""
+
+    def __init__(self, folder):
+        objs = [os.path.join(ROOT, "_build", o + ".o") for o in OBJECTS]
+        so = os.path.join(str(folder), "librecord.so")
+        subprocess.run([CLANG, "-x", "c++", "-std=c++17", "-O1", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__",
+                        "-I", os.path.join(ROOT, "include"), "-I", os.path.join(ROOT, "quantized_moe_02_amd", "csrc"),
+                        "-I", "/opt/rocm/include", os.path.join(ROOT, "tests", "native", "record_launches.cpp"),
+                        "-x", "none", *objs, "-Wl,-Bsymbolic", "-o", so], check=True)
+        self.lib = ctypes.CDLL(so)
+        for name in ("moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_matmul", "moe_mxfp4_matmul_dx",
+                     "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_loss_grad"):
+            getattr(self.lib, name).argtypes = getattr(q.lib(), name).argtypes
+        self.lib.recorded_name.restype = ctypes.c_char_p
+        for name in ("blocks", "threads", "rows", "x", "codes", "scale"):
+            getattr(self.lib, "recorded_" + name).restype = ctypes.c_uint64
+
+    @staticmethod
+    def available() -> bool:
+        return bool(shutil.which(CLANG)) and all(
+            os.path.exists(os.path.join(ROOT, "_build", o + ".o")) for o in OBJECTS)
+
+    def take(self):
+        L = self.lib
+        out = [Launch(_kernel(L.recorded_name(i).decode()), L.recorded_blocks(i), L.recorded_threads(i),
+                      L.recorded_rows(i), L.recorded_x(i), L.recorded_codes(i), L.recorded_scale(i))
+               for i in range(L.recorded())]
+        L.forget()
+        return out
