@@ -23,6 +23,19 @@ long max_units(const MatmulArgs& g, int BM) {
   return (long)g.R / BM + (g.offsets ? (long)std::min(g.E, g.R) : 1);
 }
 
+// Calls launch(first unit, workgroups) for runs of units of `per` workgroups each: a
+// launch has to stay below 2^32 work items.
+template <class F>
+hipError_t by_units(long units, long per, int threads, F&& launch) {
+  const long most = (1l << 31) / (per * threads);
+  for (long u = 0; u < units; u += most) {
+    launch((int)u, dim3((unsigned)(std::min(most, units - u) * per)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 // ---------------------------------------------------------------------------
 // RT x 16 outputs x up to 16 rows, for one or several neighbouring tiles of
 // outputs.  A step is 256 inputs, a line of a row's codes: lane (lr, lq) takes
@@ -164,17 +177,17 @@ __device__ __forceinline__ void thin_tiles(const MatmulArgs& g, const RowUnit& u
 }
 
 template <bool MX, int RT, bool EV>
-__global__ void __launch_bounds__(256) mx_matmul_thin_kernel(MatmulArgs g, int nt, int per) {
+__global__ void __launch_bounds__(256) mx_matmul_thin_kernel(MatmulArgs g, int nt, int per, int first) {
   __shared__ __attribute__((aligned(16))) uint8_t rows[MX ? 16 : kThinLds], parts[4 * RT * 1024];
   const int runs = (nt + per - 1) / per;
   const int ub = blockIdx.x / runs, tile = (blockIdx.x - ub * runs) * per;
-  const RowUnit u = find_unit(g.offsets, g.E, g.R, kThinRows, ub, reinterpret_cast<int*>(parts));
+  const RowUnit u = find_unit(g.offsets, g.E, g.R, kThinRows, first + ub, reinterpret_cast<int*>(parts));
   if (u.M <= 0) return;
   thin_tiles<MX, RT, EV>(g, u, tile, min(per, nt - tile), (lds8_t*)rows, (lds8_t*)parts);
 }
 
 template <bool MX>
-void launch_thin(const MatmulArgs& g, hipStream_t s) {
+hipError_t launch_thin(const MatmulArgs& g, hipStream_t s) {
   const long units = max_units(g, kThinRows);
   // 64 outputs a tile (a row's inputs are then read for four row tiles) where
   // that leaves every CU several, else 32 or 16 (64 tokens, down projection: 317 us
@@ -185,15 +198,16 @@ void launch_thin(const MatmulArgs& g, hipStream_t s) {
   const int rt = units * ((g.N + 63) / 64) >= 1024 ? 4 : units * ((g.N + 31) / 32) >= 512 ? 2 : 1;
   const int nt = (g.N + 16 * rt - 1) / (16 * rt);
   const int per = units * nt >= 8192 ? 2 : 1;
-  const dim3 grid((unsigned)(units * ((nt + per - 1) / per)));
-  auto go = [&](auto RT) {
-    constexpr int r = decltype(RT)::value;
-    if (g.K % 64 == 0) hipLaunchKernelGGL((mx_matmul_thin_kernel<MX, r, true>), grid, dim3(256), 0, s, g, nt, per);
-    else hipLaunchKernelGGL((mx_matmul_thin_kernel<MX, r, false>), grid, dim3(256), 0, s, g, nt, per);
-  };
-  if (rt == 4) go(std::integral_constant<int, 4>{});
-  else if (rt == 2) go(std::integral_constant<int, 2>{});
-  else go(std::integral_constant<int, 1>{});
+  return by_units(units, (nt + per - 1) / per, 256, [&](int first, dim3 grid) {
+    auto go = [&](auto RT) {
+      constexpr int r = decltype(RT)::value;
+      if (g.K % 64 == 0) hipLaunchKernelGGL((mx_matmul_thin_kernel<MX, r, true>), grid, dim3(256), 0, s, g, nt, per, first);
+      else hipLaunchKernelGGL((mx_matmul_thin_kernel<MX, r, false>), grid, dim3(256), 0, s, g, nt, per, first);
+    };
+    if (rt == 4) go(std::integral_constant<int, 4>{});
+    else if (rt == 2) go(std::integral_constant<int, 2>{});
+    else go(std::integral_constant<int, 1>{});
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -270,10 +284,10 @@ __device__ __forceinline__ void dx_thin_tile(const MatmulArgs& g, const RowUnit&
 }
 
 template <int CW, int NW>
-__global__ void __launch_bounds__(64 * NW) mx_matmul_dx_thin_kernel(MatmulArgs g, int nt) {
+__global__ void __launch_bounds__(64 * NW) mx_matmul_dx_thin_kernel(MatmulArgs g, int nt, int first) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[NW * CW * 8192];
   const int ub = blockIdx.x / nt, tile = blockIdx.x - ub * nt;
-  const RowUnit u = find_unit(g.offsets, g.E, g.R, kThinRows, ub, reinterpret_cast<int*>(smem));
+  const RowUnit u = find_unit(g.offsets, g.E, g.R, kThinRows, first + ub, reinterpret_cast<int*>(smem));
   if (u.M <= 0) return;
   dx_thin_tile<CW, NW>(g, u, tile * (128 * CW), (lds8_t*)smem);
 }
@@ -281,8 +295,9 @@ __global__ void __launch_bounds__(64 * NW) mx_matmul_dx_thin_kernel(MatmulArgs g
 template <int CW, int NW>
 hipError_t launch_dx_thin(const MatmulArgs& g, hipStream_t s) {
   const int nt = (g.K + 128 * CW - 1) / (128 * CW);
-  hipLaunchKernelGGL((mx_matmul_dx_thin_kernel<CW, NW>), dim3((unsigned)(max_units(g, kThinRows) * nt)), dim3(64 * NW), 0, s, g, nt);
-  return hipGetLastError();
+  return by_units(max_units(g, kThinRows), nt, 64 * NW, [&](int first, dim3 grid) {
+    hipLaunchKernelGGL((mx_matmul_dx_thin_kernel<CW, NW>), grid, dim3(64 * NW), 0, s, g, nt, first);
+  });
 }
 
 
@@ -330,13 +345,11 @@ hipError_t launch_mx_matmul(const MatmulArgs& g, bool a_mxfp4, hipStream_t s) {
     // rows, 4096 x 4096: 26 us against 43; 8 items, 512 rows, 1024 x 4096, and fewer
     // rows per expert alike within 1 us either way)
     if (near && g.R >= 8 * (int64_t)g.E && (int64_t)g.R * g.N >= 16 * 256 * 256) return launch_mx_matmul4_large(g, s);
-    launch_thin<true>(g, s);
-    return hipGetLastError();
+    return launch_thin<true>(g, s);
   }
   if (near && g.R >= 128 && g.R >= 4 * (int64_t)g.E && runs_of(g, 64) * std::ceil(g.N / 128.0) >= 32)
     return mid_is_faster(g, g.N) ? launch_mx_matmul_mid(g, s) : launch_mx_matmul_large(g, s);
-  launch_thin<false>(g, s);
-  return hipGetLastError();
+  return launch_thin<false>(g, s);
 }
 
 hipError_t launch_mx_matmul_dx(const MatmulArgs& g, hipStream_t s) {

@@ -13,7 +13,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CLANG = "/opt/rocm/llvm/bin/clang++"
 OBJECTS = ["operators_api", "mxfp4", "mxfp4_matmul", "mxfp4_large", "mxfp4_large4", "mxfp4_dx", "balance"]
 # kernel: its name and template arguments, as "mx_matmul_thin<false, 4, true>"
-Launch = collections.namedtuple("Launch", "kernel blocks threads rows x codes scale")
+Launch = collections.namedtuple("Launch", "kernel blocks threads first rows x codes scale")
 
 
 def _kernel(mangled: str) -> str:
@@ -52,7 +52,7 @@ class Recorder:
     def take(self):
         L = self.lib
         out = [Launch(_kernel(L.recorded_name(i).decode()), L.recorded_blocks(i), L.recorded_threads(i),
-                      L.recorded_rows(i), L.recorded_x(i), L.recorded_codes(i), L.recorded_scale(i))
+                      L.recorded_first(i), L.recorded_rows(i), L.recorded_x(i), L.recorded_codes(i), L.recorded_scale(i))
                for i in range(L.recorded())]
         L.forget()
         return out

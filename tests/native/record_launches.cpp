@@ -18,7 +18,8 @@ namespace {
 struct Launch {
   std::string name;   // as the compiler mangles it
   uint64_t blocks, threads;
-  qmoe::MxQuantArgs quant;
+  qmoe::MxQuantArgs quant;   // of a conversion
+  int first;                 // of a few-row product: its first unit of rows
 };
 struct Shape {
   dim3 grid, block;
@@ -69,6 +70,8 @@ hipError_t hipLaunchKernel(const void* f, dim3 grid, dim3 block, void** args, si
   l.blocks = grid.x;
   l.threads = (uint64_t)grid.x * block.x;
   if (l.name.find("quantize_kernel") != std::string::npos) std::memcpy(&l.quant, args[0], sizeof l.quant);
+  if (l.name.find("mx_matmul_thin") != std::string::npos) l.first = *static_cast<int*>(args[3]);
+  if (l.name.find("mx_matmul_dx_thin") != std::string::npos) l.first = *static_cast<int*>(args[2]);
   launches.push_back(l);
   const bool fits = grid.x > 0 && l.threads < (1ull << 32) && grid.y == 1 && grid.z == 1 && block.x <= 1024;
   return last = fits ? hipSuccess : hipErrorInvalidConfiguration;
@@ -84,6 +87,7 @@ void forget() { launches.clear(); }
 const char* recorded_name(int i) { return launches[i].name.c_str(); }
 uint64_t recorded_blocks(int i) { return launches[i].blocks; }
 uint64_t recorded_threads(int i) { return launches[i].threads; }
+int recorded_first(int i) { return launches[i].first; }
 int64_t recorded_rows(int i) { return launches[i].quant.rows; }
 uint64_t recorded_x(int i) { return (uint64_t) reinterpret_cast<uintptr_t>(launches[i].quant.x); }
 uint64_t recorded_codes(int i) { return (uint64_t) reinterpret_cast<uintptr_t>(launches[i].quant.codes); }

@@ -38,3 +38,50 @@ def test_quantize_launches_cover_any_matrix(record, rows, cols, dtype, size):
             assert l.threads < 1 << 32 and l.threads * per >= l.rows * 32 * nb
             at += l.rows
         assert at == rows
+
+
+F = 1 << 30                                          # 16-byte aligned, never dereferenced
+MAX_ROWS = 16 * q.MOE_MAX_TOKENS
+
+
+def _product(record, R, n, k, E, a_rows=None, act="bf16", index=False, lda=None, dx=False):
+    """The launches of one product (dx: its gradient) over fp32 outputs."""
+    c = q.MoeMatmulConfig(R, n, k, E, R if a_rows is None else a_rows, q.MOE_DT_MXFP4 if act == "mxfp4" else q.MOE_DT_BF16,
+                          q.MOE_DT_F32, lda or (n if dx else k), k if dx else n)
+    if dx:
+        s = record.lib.moe_mxfp4_matmul_dx(ctypes.byref(c), F, F, F, F, F, None)
+    else:
+        s = record.lib.moe_mxfp4_matmul(ctypes.byref(c), F, F if act == "mxfp4" else None, F, F, F, F if index else None,
+                                        F, None)
+    assert s == q.MOE_OK
+    return record.take()
+
+
+@pytest.mark.parametrize("R,n,k,E,a_rows,act,index,lda,dx", [
+    (MAX_ROWS, 65536, 2048, 256, MAX_ROWS, "bf16", True, None, False),     # inputs past 32-bit offsets: few-row units
+    (1 << 20, 65536, 2048, 256, 1 << 21, "bf16", True, None, False),
+    (MAX_ROWS, 8192, 6144, 256, MAX_ROWS, "mxfp4", True, None, False),
+    (MAX_ROWS, 65536, 65536, 1, MAX_ROWS, "mxfp4", True, None, False),
+    (MAX_ROWS, 65536, 2048, 256, None, "bf16", False, 1 << 24, False),
+    (MAX_ROWS, 65536, 65536, 256, None, "bf16", False, 1 << 24, True),
+    (MAX_ROWS, 65536, 65536, 256, None, "bf16", False, None, True),
+    (MAX_ROWS, 65536, 32, 1, None, "bf16", False, None, False)])
+def test_product_launches_cover_every_unit(record, R, n, k, E, a_rows, act, index, lda, dx):
+    ls = _product(record, R, n, k, E, a_rows, act, index, lda, dx)
+    assert all(l.threads < 1 << 32 for l in ls)
+    if "thin" not in ls[0].kernel:
+        assert len(ls) == 1
+        return
+    # workgroups of a unit: by its outputs
+    outputs = k if dx else n
+    if dx:
+        per = -(-outputs // (128 * int(ls[0].kernel.split("<")[1][0])))
+    else:
+        nt = -(-outputs // (16 * int(ls[0].kernel.split(", ")[1])))
+        units = R // 16 + min(E, R)
+        per = -(-nt // 2) if units * nt >= 8192 else nt
+    at = 0
+    for l in ls:
+        assert l.kernel == ls[0].kernel and l.first == at and l.blocks % per == 0
+        at += l.blocks // per
+    assert at >= R // 16 + (min(E, R) if E > 1 else 1)
