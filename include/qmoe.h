@@ -553,7 +553,8 @@ typedef struct {
   float coef;            /* finite */
 } moe_balance_config;
 
-/* Bytes of workspace moe_balance_loss needs (host output). */
+/* Bytes of workspace moe_balance_loss needs (host output).  Enough for every
+ * call of no more tokens, experts and sequences. */
 moe_status moe_balance_workspace_size(const moe_balance_config* cfg, size_t* bytes);
 
 /*   logits       [T][E] of logits_dtype, contiguous, 16-byte aligned

@@ -423,6 +423,12 @@ void dispatch(const BalanceArgs& a, F&& f) {
 int balance_chunk(int T, int S) {
   return std::min(kMaxChunk, std::max((T + 1023) / 1024, std::min(32, std::max(2, T / S / 4))));
 }
+// Chunks that T tokens or fewer make at most: 1024 of 32 tokens or more; of c < 32
+// tokens, which t < 4 S (c + 1) tokens come in, at most 4 S (c + 1) / c <= 6 S, and
+// no more than half of 32768.
+int balance_max_chunks(int T, int S) {
+  return std::min((T + 1) / 2, std::max(1024, std::min(16384, 6 * S)));
+}
 int balance_slices(int E) { return (E + kSliceE - 1) / kSliceE; }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {

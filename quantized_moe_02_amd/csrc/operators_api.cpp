@@ -88,8 +88,7 @@ BalanceArgs balance_args(const moe_balance_config& c, const void* logits, const 
 
 // Lays the workspace out from `base` (nullptr: only sizes it).
 size_t carve_balance(const moe_balance_config& c, void* base, BalanceArgs* a) {
-  const int chunk = balance_chunk(c.tokens, c.n_seq);
-  const size_t slots = (size_t)(c.tokens + chunk - 1) / chunk + (size_t)c.n_seq;
+  const size_t slots = (size_t)balance_max_chunks(c.tokens, c.n_seq) + (size_t)c.n_seq;
   const size_t E = (size_t)c.n_experts;
   size_t off = 0;
   auto take = [&](size_t bytes) {

@@ -61,6 +61,8 @@ struct BalanceArgs {
 // Token chunks of the forward pass: one partial sum per (chunk, sequence)
 // pair that share a token, at slot chunk + sequence.
 int balance_chunk(int T, int S);
+// Chunks of any T tokens or fewer, at most: what the workspace holds.
+int balance_max_chunks(int T, int S);
 // Workgroups per sequence of its second launch.
 int balance_slices(int E);
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);

@@ -1,0 +1,36 @@
+"""Further forms of the router's balance loss on the GPU against the float64
+oracle (bounds as in test_gpu_balance.py)."""
+import numpy as np
+import pytest
+import torch
+
+import quantized_moe_02_amd as q
+from oracle import operators as ref
+from test_gpu_balance import U, _inputs, _seqs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    q.lib()
+
+
+def test_one_workspace_for_every_smaller_batch():
+    """Sized once, used by batches of fewer tokens and sequences that cut
+    them into more chunks."""
+    ws = q.balance_workspace(600, 40, 48)
+    for T, S in ((600, 48), (575, 48), (576, 48), (300, 20), (100, 3), (129, 48), (1, 1)):
+        x, ids = _inputs(T, 40, 4, T, "f32", 0.1, 0.1)
+        seq = _seqs(T, S, T)
+        ws.fill_(0xFF)
+        counts = torch.full((S, 40), -7, dtype=torch.int32, device="cuda")
+        tokens = torch.full((S,), -7, dtype=torch.int32, device="cuda")
+        loss = torch.full((1,), 9.0, device="cuda")
+        q.moe_balance_loss(x.cuda(), ids.cuda(), counts, tokens, loss, coef=0.5,
+                           seq_offsets=torch.tensor(seq, dtype=torch.int32, device="cuda"), ws=ws)
+        rl, rc, rt, _ = ref.balance(x.double().numpy(), ids.numpy(), seq, 0.5, "sigmoid")
+        assert np.array_equal(counts.cpu().numpy(), rc) and np.array_equal(tokens.cpu().numpy(), rt)
+        assert abs(loss.item() - rl) <= (4 * x.abs().max().item() + 104) * U * rl

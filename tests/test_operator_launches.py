@@ -57,6 +57,21 @@ def _product(record, R, n, k, E, a_rows=None, act="bf16", index=False, lda=None,
     return record.take()
 
 
+@pytest.mark.parametrize("S", [1, 4, 5, 39, 48, 300, 1365, 2731, 65536])
+def test_balance_workspace_holds_every_slot(record, S):
+    """One slot of E shares and counts, a token and a pick count for each chunk
+    and sequence; a double per 32 experts of a sequence."""
+    E = 33
+    tokens = sorted({t for e in (1, 8 * S, 12 * S, 16 * S, 128 * S, 128, 32768, 262144) for t in range(e - 9, e + 9)
+                     if 0 < t <= q.MOE_MAX_TOKENS} | set(range(1, q.MOE_MAX_TOKENS, 4999)))
+    for T in tokens:
+        c, n = q.make_balance_config(T, E, 1, S), ctypes.c_size_t(0)
+        assert record.lib.moe_balance_workspace_size(ctypes.byref(c), ctypes.byref(n)) == q.MOE_OK
+        assert record.lib.moe_balance_loss(ctypes.byref(c), F, F, F, F, F, F, F, n, None) == q.MOE_OK
+        chunks = [l.blocks for l in record.take() if l.kernel.startswith("balance_partial")]
+        assert len(chunks) == 1 and n.value >= (chunks[0] + S) * (8 * E + 8) + 2 * S * 8, T
+
+
 @pytest.mark.parametrize("R,n,k,E,a_rows,act,index,lda,dx", [
     (MAX_ROWS, 65536, 2048, 256, MAX_ROWS, "bf16", True, None, False),     # inputs past 32-bit offsets: few-row units
     (1 << 20, 65536, 2048, 256, 1 << 21, "bf16", True, None, False),
