@@ -308,7 +308,10 @@ def moe_cache_slot_of(cache, expert: int) -> int:
 
 # ---- MXFP4 and router-balance operators --------------------------------------
 # Sizes, types and strides come from the tensors; one whose shape, type or
-# layout does not fit the others raises QmoeError (MOE_ERR_INVALID_ARG).
+# layout does not fit the others, or that does not lie on the current device
+# (whose kernels would read another device's memory), raises QmoeError
+# (MOE_ERR_INVALID_ARG).
+_current_device = torch._C._cuda_getDevice
 _DT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
 _SCORE = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}
 
@@ -318,17 +321,25 @@ def _require(ok: bool, where: str):
         raise QmoeError(MOE_ERR_INVALID_ARG, where)
 
 
-def _fits(where: str, t: torch.Tensor, dtype, shape: tuple):
-    """`t` is a contiguous device tensor of this type and shape."""
-    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+def _device(where: str, t: torch.Tensor) -> int:
+    """The current device, which `t` has to lie on."""
+    dev = t.get_device()
+    if dev < 0 or dev != _current_device():
+        raise QmoeError(MOE_ERR_INVALID_ARG, where)
+    return dev
+
+
+def _fits(where: str, dev: int, t: torch.Tensor, dtype, shape: tuple):
+    """`t` is a contiguous tensor of this type and shape on this device."""
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
         raise QmoeError(MOE_ERR_INVALID_ARG, where)
 
 
-def _matrix(where: str, t: torch.Tensor, dtypes):
-    """`t` is a device matrix whose rows are contiguous; returns its rows,
-    columns and row stride."""
+def _matrix(where: str, dev: int, t: torch.Tensor, dtypes):
+    """`t` is a matrix on this device whose rows are contiguous; returns its
+    rows, columns and row stride."""
     shape = t.shape
-    if not (t.is_cuda and len(shape) == 2 and t.dtype in dtypes):
+    if not (t.get_device() == dev and len(shape) == 2 and t.dtype in dtypes):
         raise QmoeError(MOE_ERR_INVALID_ARG, where)
     rows, cols = shape
     if t.is_contiguous():
@@ -338,10 +349,10 @@ def _matrix(where: str, t: torch.Tensor, dtypes):
     return rows, cols, ld if rows > 1 else max(cols, 1)
 
 
-def _queue(stream, t: torch.Tensor):
-    """The stream's handle; by default the current stream of `t`'s device."""
+def _queue(stream, dev: int):
+    """The stream's handle; by default the device's current stream."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -357,35 +368,36 @@ def mxfp4_empty(rows: int, cols: int, device="cuda"):
 
 
 def _mxfp4_rows(where, x, codes, scales):
-    rows, cols, ld = _matrix(where, x, _DT)
+    dev = _device(where, x)
+    rows, cols, ld = _matrix(where, dev, x, _DT)
     nb = (cols + 31) // 32
-    _fits(where, codes, torch.uint8, (rows, 16 * nb))
-    _fits(where, scales, torch.uint8, (rows, nb))
-    return rows, cols, ld
+    _fits(where, dev, codes, torch.uint8, (rows, 16 * nb))
+    _fits(where, dev, scales, torch.uint8, (rows, nb))
+    return rows, cols, ld, dev
 
 
 def moe_mxfp4_quantize(src, codes, scales, stream=None):
     """Rows of `src` (fp32, bf16 or fp16) to MXFP4 codes and scales."""
-    rows, cols, ld = _mxfp4_rows("moe_mxfp4_quantize", src, codes, scales)
+    rows, cols, ld, dev = _mxfp4_rows("moe_mxfp4_quantize", src, codes, scales)
     _check(lib().moe_mxfp4_quantize(src.data_ptr(), _DT[src.dtype], rows, cols, ld, codes.data_ptr(),
-                                    scales.data_ptr(), _queue(stream, src)), "moe_mxfp4_quantize")
+                                    scales.data_ptr(), _queue(stream, dev)), "moe_mxfp4_quantize")
 
 
 def moe_mxfp4_dequantize(codes, scales, dst, stream=None):
     """The values of MXFP4 rows, into `dst` (fp32, bf16 or fp16)."""
-    rows, cols, ld = _mxfp4_rows("moe_mxfp4_dequantize", dst, codes, scales)
+    rows, cols, ld, dev = _mxfp4_rows("moe_mxfp4_dequantize", dst, codes, scales)
     _check(lib().moe_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, dst.data_ptr(),
-                                      _DT[dst.dtype], ld, _queue(stream, dst)), "moe_mxfp4_dequantize")
+                                      _DT[dst.dtype], ld, _queue(stream, dev)), "moe_mxfp4_dequantize")
 
 
-def _grouped_weights(where, w_codes, w_scales, expert_offsets):
+def _grouped_weights(where, dev, w_codes, w_scales, expert_offsets):
     shape = w_codes.shape
     _require(len(shape) == 3, where)
     E, N, kb = shape
-    _fits(where, w_codes, torch.uint8, shape)
-    _fits(where, w_scales, torch.uint8, (E, N, kb // 16))
+    _fits(where, dev, w_codes, torch.uint8, shape)
+    _fits(where, dev, w_scales, torch.uint8, (E, N, kb // 16))
     if expert_offsets is not None:
-        _fits(where, expert_offsets, torch.int32, (E + 1,))
+        _fits(where, dev, expert_offsets, torch.int32, (E + 1,))
     return E, N, kb * 2
 
 
@@ -398,37 +410,39 @@ def moe_mxfp4_matmul(a, w_codes, w_scales, out, a_scale=None, expert_offsets=Non
     """out[r] = a[row_index[r]] @ W[expert of r].T over MXFP4 weights [E][n][k/2];
     `a` is bf16 [rows][k], or MXFP4 codes uint8 [rows][k/2] with `a_scale`."""
     where = "moe_mxfp4_matmul"
-    E, N, K = _grouped_weights(where, w_codes, w_scales, expert_offsets)
-    R, cols, ldo = _matrix(where, out, _OUT_DT)
+    dev = _device(where, out)
+    E, N, K = _grouped_weights(where, dev, w_codes, w_scales, expert_offsets)
+    R, cols, ldo = _matrix(where, dev, out, _OUT_DT)
     _require(cols == N, where)
     if a_scale is None:
-        a_rows, cols, lda = _matrix(where, a, _BF16)
+        a_rows, cols, lda = _matrix(where, dev, a, _BF16)
         _require(cols == K, where)
         dt = MOE_DT_BF16
     else:
         a_rows = a.shape[0]
-        _fits(where, a, torch.uint8, (a_rows, K // 2))
-        _fits(where, a_scale, torch.uint8, (a_rows, K // 32))
+        _fits(where, dev, a, torch.uint8, (a_rows, K // 2))
+        _fits(where, dev, a_scale, torch.uint8, (a_rows, K // 32))
         lda, dt = K, MOE_DT_MXFP4
     if row_index is not None:
-        _fits(where, row_index, torch.int32, (R,))
+        _fits(where, dev, row_index, torch.int32, (R,))
     cfg = MoeMatmulConfig(R, N, K, E, a_rows, dt, _DT[out.dtype], lda, ldo)
     _check(lib().moe_mxfp4_matmul(ctypes.byref(cfg), a.data_ptr(), _at(a_scale), w_codes.data_ptr(),
                                   w_scales.data_ptr(), _at(expert_offsets), _at(row_index),
-                                  out.data_ptr(), _queue(stream, out)), where)
+                                  out.data_ptr(), _queue(stream, dev)), where)
 
 
 def moe_mxfp4_matmul_dx(dy, w_codes, w_scales, dx, expert_offsets=None, stream=None):
     """dx[r] = dy[r] @ W[expert of r]: the gradient of moe_mxfp4_matmul's rows."""
     where = "moe_mxfp4_matmul_dx"
-    E, N, K = _grouped_weights(where, w_codes, w_scales, expert_offsets)
-    rows, cols, lda = _matrix(where, dy, _BF16)
-    R, dx_cols, ldo = _matrix(where, dx, _OUT_DT)
+    dev = _device(where, dx)
+    E, N, K = _grouped_weights(where, dev, w_codes, w_scales, expert_offsets)
+    rows, cols, lda = _matrix(where, dev, dy, _BF16)
+    R, dx_cols, ldo = _matrix(where, dev, dx, _OUT_DT)
     _require(rows == R and cols == N and dx_cols == K, where)
     cfg = MoeMatmulConfig(R, N, K, E, R, MOE_DT_BF16, _DT[dx.dtype], lda, ldo)
     _check(lib().moe_mxfp4_matmul_dx(ctypes.byref(cfg), dy.data_ptr(), w_codes.data_ptr(),
                                      w_scales.data_ptr(), _at(expert_offsets), dx.data_ptr(),
-                                     _queue(stream, dx)), where)
+                                     _queue(stream, dev)), where)
 
 
 def make_balance_config(tokens: int, n_experts: int, top_k: int = 1, n_seq: int = 1,
@@ -452,16 +466,17 @@ def balance_workspace(tokens: int, n_experts: int, n_seq: int = 1, device="cuda"
 
 def _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets):
     _require(logits.dim() == 2 and topk_ids.dim() == 2 and counts.dim() == 2 and score in _SCORE, where)
+    dev = _device(where, counts)
     T, E = shape = logits.shape
     S, K = counts.shape[0], topk_ids.shape[1]
     _require(logits.dtype in _OUT_DT, where)
-    _fits(where, logits, logits.dtype, shape)
-    _fits(where, topk_ids, torch.int32, (T, K))
-    _fits(where, counts, torch.int32, (S, E))
-    _fits(where, tokens, torch.int32, (S,))
+    _fits(where, dev, logits, logits.dtype, shape)
+    _fits(where, dev, topk_ids, torch.int32, (T, K))
+    _fits(where, dev, counts, torch.int32, (S, E))
+    _fits(where, dev, tokens, torch.int32, (S,))
     if seq_offsets is not None:
-        _fits(where, seq_offsets, torch.int32, (S + 1,))
-    return MoeBalanceConfig(T, E, K, S, _SCORE[score], _DT[logits.dtype], coef)
+        _fits(where, dev, seq_offsets, torch.int32, (S + 1,))
+    return MoeBalanceConfig(T, E, K, S, _SCORE[score], _DT[logits.dtype], coef), dev
 
 
 def moe_balance_loss(logits, topk_ids, counts, tokens, loss, coef, score="sigmoid", seq_offsets=None,
@@ -469,13 +484,14 @@ def moe_balance_loss(logits, topk_ids, counts, tokens, loss, coef, score="sigmoi
     """The router's balance loss (loss [1]), its picks per sequence and expert
     (counts [S][E]) and routed tokens per sequence (tokens [S])."""
     where = "moe_balance_loss"
-    cfg = _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets)
-    _fits(where, loss, torch.float32, (1,))
-    _require(ws is None or (ws.is_cuda and ws.dtype is torch.uint8 and ws.is_contiguous()), where)
+    cfg, dev = _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets)
+    _fits(where, dev, loss, torch.float32, (1,))
+    if ws is not None:
+        _fits(where, dev, ws, torch.uint8, ws.shape)
     _check(lib().moe_balance_loss(ctypes.byref(cfg), logits.data_ptr(), topk_ids.data_ptr(),
                                   _at(seq_offsets), counts.data_ptr(), tokens.data_ptr(),
                                   loss.data_ptr(), _at(ws), 0 if ws is None else ws.numel(),
-                                  _queue(stream, counts)), where)
+                                  _queue(stream, dev)), where)
 
 
 def moe_balance_loss_grad(logits, topk_ids, counts, tokens, dlogits, coef, score="sigmoid",
@@ -483,10 +499,10 @@ def moe_balance_loss_grad(logits, topk_ids, counts, tokens, dlogits, coef, score
     """dlogits [T][E]: dloss (1 if None) times the loss's gradient, from the
     counts and tokens that moe_balance_loss wrote."""
     where = "moe_balance_loss_grad"
-    cfg = _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets)
-    _fits(where, dlogits, logits.dtype, logits.shape)
+    cfg, dev = _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets)
+    _fits(where, dev, dlogits, logits.dtype, logits.shape)
     if dloss is not None:
-        _fits(where, dloss, torch.float32, (1,))
+        _fits(where, dev, dloss, torch.float32, (1,))
     _check(lib().moe_balance_loss_grad(ctypes.byref(cfg), logits.data_ptr(), topk_ids.data_ptr(),
                                        _at(seq_offsets), counts.data_ptr(), tokens.data_ptr(),
-                                       _at(dloss), dlogits.data_ptr(), _queue(stream, counts)), where)
+                                       _at(dloss), dlogits.data_ptr(), _queue(stream, dev)), where)
