@@ -482,16 +482,21 @@ def _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets):
 def moe_balance_loss(logits, topk_ids, counts, tokens, loss, coef, score="sigmoid", seq_offsets=None,
                      ws=None, stream=None):
     """The router's balance loss (loss [1]), its picks per sequence and expert
-    (counts [S][E]) and routed tokens per sequence (tokens [S])."""
+    (counts [S][E]) and routed tokens per sequence (tokens [S]).  Without `ws`
+    the call takes a workspace from torch's allocator, on its stream."""
     where = "moe_balance_loss"
     cfg, dev = _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets)
     _fits(where, dev, loss, torch.float32, (1,))
-    if ws is not None:
+    if ws is None:
+        # of the memory that belongs to the call's stream, whose order keeps it until the call has run
+        queue = _queue(stream, dev)
+        with torch.cuda.stream(torch.cuda.ExternalStream(queue) if queue else torch.cuda.default_stream()):
+            ws = torch.empty(moe_balance_workspace_size(cfg), dtype=torch.uint8, device=counts.device)
+    else:
         _fits(where, dev, ws, torch.uint8, ws.shape)
     _check(lib().moe_balance_loss(ctypes.byref(cfg), logits.data_ptr(), topk_ids.data_ptr(),
                                   _at(seq_offsets), counts.data_ptr(), tokens.data_ptr(),
-                                  loss.data_ptr(), _at(ws), 0 if ws is None else ws.numel(),
-                                  _queue(stream, dev)), where)
+                                  loss.data_ptr(), ws.data_ptr(), ws.numel(), _queue(stream, dev)), where)
 
 
 def moe_balance_loss_grad(logits, topk_ids, counts, tokens, dlogits, coef, score="sigmoid",

@@ -34,3 +34,38 @@ def test_one_workspace_for_every_smaller_batch():
         rl, rc, rt, _ = ref.balance(x.double().numpy(), ids.numpy(), seq, 0.5, "sigmoid")
         assert np.array_equal(counts.cpu().numpy(), rc) and np.array_equal(tokens.cpu().numpy(), rt)
         assert abs(loss.item() - rl) <= (4 * x.abs().max().item() + 104) * U * rl
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_a_workspace_of_its_own(graph):
+    """Without one the call takes a workspace from torch's allocator, of its
+    own stream's memory: what other streams are done with does not reach it."""
+    T, E, S = 3000, 256, 20
+    x, ids = _inputs(T, E, 8, 6, pad=0.1)
+    xd, idd, seq = x.cuda(), ids.cuda(), torch.tensor(_seqs(T, S, 1), dtype=torch.int32, device="cuda")
+    out = lambda: (torch.empty(S, E, dtype=torch.int32, device="cuda"), torch.empty(S, dtype=torch.int32, device="cuda"),
+                   torch.empty(1, device="cuda"))
+    want = out()
+    q.moe_balance_loss(xd, idd, *want, coef=1e-3, seq_offsets=seq, ws=q.balance_workspace(T, E, S))
+    torch.cuda.synchronize()
+    if graph:
+        got, g = out(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            q.moe_balance_loss(xd, idd, *got, coef=1e-3, seq_offsets=seq)
+        for _ in range(3):
+            for t in got:
+                t.zero_()
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(u, v) for u, v in zip(want, got))
+        return
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream):
+        res = [out() for _ in range(4)]
+        torch.cuda.synchronize()
+        for r in res:
+            q.moe_balance_loss(xd, idd, *r, coef=1e-3, seq_offsets=seq, stream=stream)
+            q.balance_workspace(T, E, S).fill_(0xFF)        # freed at once, on the current stream
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for r in res for u, v in zip(want, r))
