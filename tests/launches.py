@@ -40,7 +40,7 @@ class Recorder:
         for name in ("moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_matmul", "moe_mxfp4_matmul_dx",
                      "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_loss_grad"):
             getattr(self.lib, name).argtypes = getattr(q.lib(), name).argtypes
-        self.lib.recorded_name.restype = ctypes.c_char_p
+        self.lib.recorded_name.restype = self.lib.registered_name.restype = ctypes.c_char_p
         for name in ("blocks", "threads", "rows", "x", "codes", "scale"):
             getattr(self.lib, "recorded_" + name).restype = ctypes.c_uint64
 
@@ -48,6 +48,10 @@ class Recorder:
     def available() -> bool:
         return bool(shutil.which(CLANG)) and all(
             os.path.exists(os.path.join(ROOT, "_build", o + ".o")) for o in OBJECTS)
+
+    def kernels(self):
+        """Every kernel of the objects."""
+        return {_kernel(self.lib.registered_name(i).decode()) for i in range(self.lib.registered())}
 
     def take(self):
         L = self.lib

@@ -7,6 +7,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <iterator>
 #include <map>
 #include <string>
 #include <vector>
@@ -82,6 +83,8 @@ hipError_t hipGetLastError() {
   return e;
 }
 
+int registered() { return (int)names().size(); }
+const char* registered_name(int i) { return std::next(names().begin(), i)->second.c_str(); }
 int recorded() { return (int)launches.size(); }
 void forget() { launches.clear(); }
 const char* recorded_name(int i) { return launches[i].name.c_str(); }

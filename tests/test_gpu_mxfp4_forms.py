@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import product_forms
 import quantized_moe_02_amd as q
 from oracle import operators as ref
 from test_gpu_mxfp4 import Problem, _close, _quantize
@@ -92,3 +93,81 @@ def test_product_of_more_than_one_launch():
     for lo in (0, (1 << 18) - 16, (1 << 18), R - 16):
         a = x[lo:lo + 16]
         _close(o[lo:lo + 16], a @ w.T, np.abs(a) @ np.abs(w).T, k, True)
+
+
+@pytest.mark.parametrize("kernel,kind,counts,n,k,extra,gather", product_forms.PRODUCTS, ids=product_forms.NAMES)
+def test_every_kernel(kernel, kind, counts, n, k, extra, gather):
+    """Values, and NaN in place: a NaN at the end of a row's inputs, NaN scales
+    in an expert's first and last blocks, indices outside.  Outputs at whole
+    lines and at an odd pitch."""
+    far = gather == product_forms.FAR
+    P = Problem(counts, n, k, seed=n + k, extra=extra, gather=1 if far else gather)
+    live = int(P.off[-1])
+    used = [e for e, c in enumerate(counts) if c]
+    first, last = used[0], used[-1]
+    off = P.offsets() if P.E > 1 else None
+    if kind == "dx":
+        P.dy[live - 1, n - 1] = float("nan")
+        P.ws[first, n - 1, 0] = P.ws[last, 0, k // 32 - 1] = 255
+        src = P.dy.double().numpy()
+    else:
+        P.ws[first, 7, k // 32 - 1] = P.ws[last, n - 1, 0] = 255
+        if far:
+            P.index = torch.randint(0, gather, (P.R,), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+            a = torch.empty(gather, k, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(2))
+        else:
+            a = P.a.cuda()
+        if P.index is not None and live > 4:
+            P.index[1], P.index[live - 2] = -1, a.shape[0]
+        a[live - 1 if P.index is None else int(P.index[live - 1]), k - 1] = float("nan")
+        src, args = a, {}
+        if kind == "mxfp4":
+            codes, scales = _quantize(a)
+            src = ref.mx_values(codes.cpu().numpy(), scales.cpu().numpy())
+            a, args = codes, {"a_scale": scales}
+        elif far:
+            at = P.index.long().clamp(0, gather - 1)
+            src = a[at.cuda()].double().cpu().numpy()
+            src[((P.index < 0) | (P.index >= gather)).numpy()] = 0
+        else:
+            src = a.double().cpu().numpy()
+    w64 = ref.mx_values(P.wq.numpy(), P.ws.numpy())
+    index = None if P.index is None or far or kind == "dx" else P.index.numpy()
+    want, mag = ref.grouped_matmul(src, w64, P.off, index, P.R, transpose=kind == "dx")
+    want, mag = want[:live], mag[:live]
+    nan = np.isnan(want)
+    assert 0 < nan.sum() and (not nan.all() or live < 3)
+    cols, terms = (k, n) if kind == "dx" else (n, k)
+    wq, ws = P.wq.cuda(), P.ws.cuda()
+    for out, pitch in (("f32", -(-cols // 64) * 64), ("bf16", -(-cols // 64) * 64), ("bf16", cols + 3)):
+        full = torch.full((P.R, pitch), 77.0, dtype=DT[out], device="cuda")
+        if kind == "dx":
+            q.moe_mxfp4_matmul_dx(P.dy.cuda(), wq, ws, full[:, :cols], expert_offsets=off)
+        else:
+            q.moe_mxfp4_matmul(a, wq, ws, full[:, :cols], expert_offsets=off, row_index=P.dev(P.index), **args)
+        got = full[:live, :cols]
+        assert np.array_equal(torch.isnan(got).cpu().numpy(), nan), (out, pitch)
+        _close(got[torch.from_numpy(~nan).cuda()], want[~nan], mag[~nan], terms, out == "bf16")
+        assert (full[live:] == 77.0).all() and (full[:, cols:] == 77.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,cols,pitch", [(4099, 4097, 4097), (4099, 4097, 4102), (20000, 4097, 4097)])
+def test_conversions_of_every_kernel(rows, cols, pitch, dtype):
+    """One and four chunks per lane: rows of an odd length that repeat with a
+    period that no workgroup's share has."""
+    period = 37
+    g = torch.Generator().manual_seed(cols)
+    x = torch.randn(period, cols, generator=g) * torch.exp2(torch.randint(-9, 9, (period, cols), generator=g).float())
+    x = x.to(DT[dtype])
+    wide = torch.full((rows, pitch), float("nan"), dtype=DT[dtype], device="cuda")
+    src = wide[:, :cols]
+    src.copy_(x.cuda().repeat(rows // period + 1, 1)[:rows])
+    codes, scales = _quantize(src)
+    rc, rs = ref.mx_quantize(x.double().numpy())
+    back = torch.full((rows, pitch), 7.0, dtype=DT[dtype], device="cuda")
+    q.moe_mxfp4_dequantize(codes, scales, back[:, :cols])
+    held = torch.from_numpy(ref.mx_values(rc, rs)[:, :cols]).to(DT[dtype])
+    for got, want in ((codes, torch.from_numpy(rc)), (scales, torch.from_numpy(rs)), (back[:, :cols], held)):
+        assert torch.equal(got, want.cuda().repeat(rows // period + 1, 1)[:rows])
+    assert (back[:, cols:] == 7.0).all()

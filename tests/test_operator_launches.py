@@ -4,6 +4,7 @@ import ctypes
 import pytest
 
 import launches as rec
+import product_forms
 import quantized_moe_02_amd as q
 
 X, CODES, SCALE = 1 << 60, 1 << 50, 1 << 40          # never dereferenced
@@ -100,3 +101,24 @@ def test_product_launches_cover_every_unit(record, R, n, k, E, a_rows, act, inde
         assert l.kernel == ls[0].kernel and l.first == at and l.blocks % per == 0
         at += l.blocks // per
     assert at >= R // 16 + (min(E, R) if E > 1 else 1)
+
+
+@pytest.mark.parametrize("kernel,kind,counts,n,k,extra,gather", product_forms.PRODUCTS, ids=product_forms.NAMES)
+def test_forms_reach_their_kernels(record, kernel, kind, counts, n, k, extra, gather):
+    R = sum(counts) + extra
+    ls = _product(record, R, n, k, len(counts), gather or None, kind, bool(gather), dx=kind == "dx")
+    assert [l.kernel for l in ls] == [kernel]
+
+
+def test_forms_name_every_kernel(record):
+    """Every product's kernel that the objects hold is reached by some form."""
+    assert {kernel for kernel, *_ in product_forms.PRODUCTS} == {k for k in record.kernels() if "matmul" in k}
+
+
+@pytest.mark.parametrize("rows,cols,dtype,chunks", [
+    (4099, 4097, q.MOE_DT_BF16, 4), (4099, 4097, q.MOE_DT_F16, 4), (4099, 4097, q.MOE_DT_F32, 1), (4099, 2057, q.MOE_DT_F16, 1),
+    (20000, 4097, q.MOE_DT_BF16, 1)])
+def test_conversions_reach_their_kernels(record, rows, cols, dtype, chunks):
+    record.lib.moe_mxfp4_quantize(X, dtype, rows, cols, cols, CODES, SCALE, None)
+    record.lib.moe_mxfp4_dequantize(CODES, SCALE, rows, cols, X, dtype, cols, None)
+    assert [l.kernel for l in record.take()] == [f"mx_quantize<{dtype}, {chunks}>", f"mx_dequantize<{dtype}, {chunks}>"]
