@@ -470,7 +470,8 @@ moe_status moe_mxfp4_quantize(const void* src, int32_t dtype, int64_t rows, int6
 
 /* MXFP4 rows to dst [rows][cols] of dtype MOE_DT_F32, _BF16 or _F16 (rounded
  * to nearest even where the type cannot hold the value), row stride ld.
- * Exact in F32 and BF16. */
+ * Exact in F32 and BF16 below 2^128; values from there on, which scales 253 and
+ * 254 alone reach (moe_mxfp4_quantize writes neither), become infinities. */
 moe_status moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scale, int64_t rows,
                                 int64_t cols, void* dst, int32_t dtype, int64_t ld,
                                 hipStream_t stream);
@@ -505,7 +506,10 @@ typedef struct {
  *   row_index  int32 [R] (moe_permute's sorted_token), or NULL; a row whose
  *            index lies outside [0, a_rows) reads as zeros
  *   out      [R][n] of out_dtype, row stride ldo >= n, 16-byte aligned
- * Products are exact, sums are held in fp32; one rounding at the store.
+ * Products are exact, sums are held in fp32; one rounding at the store.  Beside
+ * bf16 rows the weights are bf16 values, exact below 2^128: one from there on
+ * (scales 253 and 254 alone reach it) is an infinity, so NaN against a zero.
+ * Beside MXFP4 rows every weight is exact.
  * R == 0 enqueues nothing. */
 moe_status moe_mxfp4_matmul(const moe_matmul_config* cfg, const void* a, const uint8_t* a_scale,
                             const uint8_t* w_codes, const uint8_t* w_scale,
@@ -520,7 +524,7 @@ moe_status moe_mxfp4_matmul(const moe_matmul_config* cfg, const void* a, const u
  *   dy  [R][n] bf16, row stride lda >= n, lda a multiple of 8, 16-byte aligned
  *   dx  [R][k] of out_dtype, row stride ldo >= k, 16-byte aligned
  * cfg as for moe_mxfp4_matmul with a_dtype MOE_DT_BF16, a_rows == rows, and n
- * a multiple of 32 (else MOE_ERR_INVALID_ARG). */
+ * a multiple of 32 (else MOE_ERR_INVALID_ARG).  Weights as beside bf16 rows there. */
 moe_status moe_mxfp4_matmul_dx(const moe_matmul_config* cfg, const void* dy,
                                const uint8_t* w_codes, const uint8_t* w_scale,
                                const int32_t* expert_offsets, void* dx, hipStream_t stream);

@@ -171,3 +171,44 @@ def test_conversions_of_every_kernel(rows, cols, pitch, dtype):
     for got, want in ((codes, torch.from_numpy(rc)), (scales, torch.from_numpy(rs)), (back[:, :cols], held)):
         assert torch.equal(got, want.cuda().repeat(rows // period + 1, 1)[:rows])
     assert (back[:, cols:] == 7.0).all()
+
+
+@pytest.mark.parametrize("ends", ["low", "high", "top"])
+@pytest.mark.parametrize("kernel", sorted({p[0] for p in product_forms.PRODUCTS}))
+def test_ends_of_the_scale_range(kernel, ends):
+    """Weights of the smallest scales (bf16 has them as subnormals) and the
+    largest, with inputs that keep the sums finite: exact products throughout.
+    Weights of 2^128 and more (scales 253 and 254) are infinities beside bf16
+    rows and in the gradient, and exact beside MXFP4 rows."""
+    _, kind, counts, n, k, extra, gather = next(p for p in product_forms.PRODUCTS if p[0] == kernel)
+    P = Problem(counts, n, k, seed=n + k, extra=extra, gather=gather)
+    lo, hi = {"low": (0, 4), "high": (250, 253), "top": (240, 250)}[ends]
+    P.ws = torch.randint(lo, hi, P.ws.shape, generator=torch.Generator().manual_seed(7), dtype=torch.uint8)
+    if ends == "top":
+        P.ws[:, 5], P.ws[:, 6, 0] = 253, 254
+    if ends != "low":
+        P.a, P.dy = ((t.float() * 2.0 ** -30).to(torch.bfloat16) for t in (P.a, P.dy))
+    w64 = ref.mx_values(P.wq.numpy(), P.ws.numpy())
+    wq, ws, off = P.wq.cuda(), P.ws.cuda(), P.offsets()
+    got = torch.full((P.R, k if kind == "dx" else n), 77.0, device="cuda")
+    if kind == "dx":
+        src = P.dy.double().numpy()
+        q.moe_mxfp4_matmul_dx(P.dy.cuda(), wq, ws, got, expert_offsets=off)
+    elif kind == "bf16":
+        src = P.a.double().numpy()
+        q.moe_mxfp4_matmul(P.a.cuda(), wq, ws, got, expert_offsets=off, row_index=P.dev(P.index))
+    else:
+        codes, scales = _quantize(P.a.cuda())
+        src = ref.mx_values(codes.cpu().numpy(), scales.cpu().numpy())
+        q.moe_mxfp4_matmul(codes, wq, ws, got, a_scale=scales, expert_offsets=off, row_index=P.dev(P.index))
+    if kind != "mxfp4":
+        w64[np.abs(w64) >= 2.0 ** 128] *= np.inf
+    with np.errstate(invalid="ignore"):
+        want, mag = ref.grouped_matmul(src, w64, P.off, None if P.index is None or kind == "dx" else P.index.numpy(), P.R,
+                                       transpose=kind == "dx")
+    live = int(P.off[-1])
+    got, want, mag = got[:live], want[:live], mag[:live]
+    fin = np.isfinite(want)
+    assert fin.any() and (fin.all() or (ends == "top" and kind != "mxfp4"))
+    assert np.array_equal(got.cpu().numpy()[~fin], want[~fin].astype(np.float32), equal_nan=True)
+    _close(got[torch.from_numpy(fin).cuda()], want[fin], mag[fin], n if kind == "dx" else k, False)
