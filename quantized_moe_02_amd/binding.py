@@ -87,7 +87,7 @@ _lib = None
 
 def lib() -> ctypes.CDLL:
     """Load libqmoe.so (once).  Raises if it has not been built."""
-    global _lib
+    global _lib, _several
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -131,6 +131,7 @@ def lib() -> ctypes.CDLL:
             fn.restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_status_string.restype = ctypes.c_char_p
+        _several = torch.cuda.device_count() > 1
         _lib = L
     return _lib
 
@@ -312,6 +313,7 @@ def moe_cache_slot_of(cache, expert: int) -> int:
 # (whose kernels would read another device's memory), raises QmoeError
 # (MOE_ERR_INVALID_ARG).
 _current_device = torch._C._cuda_getDevice
+_several = True     # more than one device; known once the library is loaded
 _DT = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
 _SCORE = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}
 
@@ -319,14 +321,6 @@ _SCORE = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}
 def _require(ok: bool, where: str):
     if not ok:
         raise QmoeError(MOE_ERR_INVALID_ARG, where)
-
-
-def _device(where: str, t: torch.Tensor) -> int:
-    """The current device, which `t` has to lie on."""
-    dev = t.get_device()
-    if dev < 0 or dev != _current_device():
-        raise QmoeError(MOE_ERR_INVALID_ARG, where)
-    return dev
 
 
 def _fits(where: str, dev: int, t: torch.Tensor, dtype, shape: tuple):
@@ -349,8 +343,11 @@ def _matrix(where: str, dev: int, t: torch.Tensor, dtypes):
     return rows, cols, ld if rows > 1 else max(cols, 1)
 
 
-def _queue(stream, dev: int):
-    """The stream's handle; by default the device's current stream."""
+def _queue(where: str, stream, dev: int):
+    """The stream's handle, by default the device's current stream.  `dev` has
+    to be the current device."""
+    if dev < 0 or ((dev > 0 or _several) and dev != _current_device()):
+        raise QmoeError(MOE_ERR_INVALID_ARG, where)
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -368,7 +365,7 @@ def mxfp4_empty(rows: int, cols: int, device="cuda"):
 
 
 def _mxfp4_rows(where, x, codes, scales):
-    dev = _device(where, x)
+    dev = x.get_device()
     rows, cols, ld = _matrix(where, dev, x, _DT)
     nb = (cols + 31) // 32
     _fits(where, dev, codes, torch.uint8, (rows, 16 * nb))
@@ -378,16 +375,20 @@ def _mxfp4_rows(where, x, codes, scales):
 
 def moe_mxfp4_quantize(src, codes, scales, stream=None):
     """Rows of `src` (fp32, bf16 or fp16) to MXFP4 codes and scales."""
-    rows, cols, ld, dev = _mxfp4_rows("moe_mxfp4_quantize", src, codes, scales)
+    where = "moe_mxfp4_quantize"
+    rows, cols, ld, dev = _mxfp4_rows(where, src, codes, scales)
+    queue = _queue(where, stream, dev)
     _check(lib().moe_mxfp4_quantize(src.data_ptr(), _DT[src.dtype], rows, cols, ld, codes.data_ptr(),
-                                    scales.data_ptr(), _queue(stream, dev)), "moe_mxfp4_quantize")
+                                    scales.data_ptr(), queue), where)
 
 
 def moe_mxfp4_dequantize(codes, scales, dst, stream=None):
     """The values of MXFP4 rows, into `dst` (fp32, bf16 or fp16)."""
-    rows, cols, ld, dev = _mxfp4_rows("moe_mxfp4_dequantize", dst, codes, scales)
+    where = "moe_mxfp4_dequantize"
+    rows, cols, ld, dev = _mxfp4_rows(where, dst, codes, scales)
+    queue = _queue(where, stream, dev)
     _check(lib().moe_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, dst.data_ptr(),
-                                      _DT[dst.dtype], ld, _queue(stream, dev)), "moe_mxfp4_dequantize")
+                                      _DT[dst.dtype], ld, queue), where)
 
 
 def _grouped_weights(where, dev, w_codes, w_scales, expert_offsets):
@@ -410,7 +411,7 @@ def moe_mxfp4_matmul(a, w_codes, w_scales, out, a_scale=None, expert_offsets=Non
     """out[r] = a[row_index[r]] @ W[expert of r].T over MXFP4 weights [E][n][k/2];
     `a` is bf16 [rows][k], or MXFP4 codes uint8 [rows][k/2] with `a_scale`."""
     where = "moe_mxfp4_matmul"
-    dev = _device(where, out)
+    dev = out.get_device()
     E, N, K = _grouped_weights(where, dev, w_codes, w_scales, expert_offsets)
     R, cols, ldo = _matrix(where, dev, out, _OUT_DT)
     _require(cols == N, where)
@@ -425,24 +426,26 @@ def moe_mxfp4_matmul(a, w_codes, w_scales, out, a_scale=None, expert_offsets=Non
         lda, dt = K, MOE_DT_MXFP4
     if row_index is not None:
         _fits(where, dev, row_index, torch.int32, (R,))
+    queue = _queue(where, stream, dev)
     cfg = MoeMatmulConfig(R, N, K, E, a_rows, dt, _DT[out.dtype], lda, ldo)
     _check(lib().moe_mxfp4_matmul(ctypes.byref(cfg), a.data_ptr(), _at(a_scale), w_codes.data_ptr(),
                                   w_scales.data_ptr(), _at(expert_offsets), _at(row_index),
-                                  out.data_ptr(), _queue(stream, dev)), where)
+                                  out.data_ptr(), queue), where)
 
 
 def moe_mxfp4_matmul_dx(dy, w_codes, w_scales, dx, expert_offsets=None, stream=None):
     """dx[r] = dy[r] @ W[expert of r]: the gradient of moe_mxfp4_matmul's rows."""
     where = "moe_mxfp4_matmul_dx"
-    dev = _device(where, dx)
+    dev = dx.get_device()
     E, N, K = _grouped_weights(where, dev, w_codes, w_scales, expert_offsets)
     rows, cols, lda = _matrix(where, dev, dy, _BF16)
     R, dx_cols, ldo = _matrix(where, dev, dx, _OUT_DT)
     _require(rows == R and cols == N and dx_cols == K, where)
+    queue = _queue(where, stream, dev)
     cfg = MoeMatmulConfig(R, N, K, E, R, MOE_DT_BF16, _DT[dx.dtype], lda, ldo)
     _check(lib().moe_mxfp4_matmul_dx(ctypes.byref(cfg), dy.data_ptr(), w_codes.data_ptr(),
-                                     w_scales.data_ptr(), _at(expert_offsets), dx.data_ptr(),
-                                     _queue(stream, dev)), where)
+                                     w_scales.data_ptr(), _at(expert_offsets), dx.data_ptr(), queue),
+           where)
 
 
 def make_balance_config(tokens: int, n_experts: int, top_k: int = 1, n_seq: int = 1,
@@ -464,9 +467,10 @@ def balance_workspace(tokens: int, n_experts: int, n_seq: int = 1, device="cuda"
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets):
+def _balance(where, stream, logits, topk_ids, counts, tokens, coef, score, seq_offsets):
     _require(logits.dim() == 2 and topk_ids.dim() == 2 and counts.dim() == 2 and score in _SCORE, where)
-    dev = _device(where, counts)
+    dev = counts.get_device()
+    queue = _queue(where, stream, dev)
     T, E = shape = logits.shape
     S, K = counts.shape[0], topk_ids.shape[1]
     _require(logits.dtype in _OUT_DT, where)
@@ -476,7 +480,7 @@ def _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets):
     _fits(where, dev, tokens, torch.int32, (S,))
     if seq_offsets is not None:
         _fits(where, dev, seq_offsets, torch.int32, (S + 1,))
-    return MoeBalanceConfig(T, E, K, S, _SCORE[score], _DT[logits.dtype], coef), dev
+    return MoeBalanceConfig(T, E, K, S, _SCORE[score], _DT[logits.dtype], coef), dev, queue
 
 
 def moe_balance_loss(logits, topk_ids, counts, tokens, loss, coef, score="sigmoid", seq_offsets=None,
@@ -485,18 +489,17 @@ def moe_balance_loss(logits, topk_ids, counts, tokens, loss, coef, score="sigmoi
     (counts [S][E]) and routed tokens per sequence (tokens [S]).  Without `ws`
     the call takes a workspace from torch's allocator, on its stream."""
     where = "moe_balance_loss"
-    cfg, dev = _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets)
+    cfg, dev, queue = _balance(where, stream, logits, topk_ids, counts, tokens, coef, score, seq_offsets)
     _fits(where, dev, loss, torch.float32, (1,))
     if ws is None:
         # of the memory that belongs to the call's stream, whose order keeps it until the call has run
-        queue = _queue(stream, dev)
         with torch.cuda.stream(torch.cuda.ExternalStream(queue) if queue else torch.cuda.default_stream()):
             ws = torch.empty(moe_balance_workspace_size(cfg), dtype=torch.uint8, device=counts.device)
     else:
-        _fits(where, dev, ws, torch.uint8, ws.shape)
+        _require(ws.get_device() == dev and ws.dtype is torch.uint8 and ws.is_contiguous(), where)
     _check(lib().moe_balance_loss(ctypes.byref(cfg), logits.data_ptr(), topk_ids.data_ptr(),
                                   _at(seq_offsets), counts.data_ptr(), tokens.data_ptr(),
-                                  loss.data_ptr(), ws.data_ptr(), ws.numel(), _queue(stream, dev)), where)
+                                  loss.data_ptr(), ws.data_ptr(), ws.numel(), queue), where)
 
 
 def moe_balance_loss_grad(logits, topk_ids, counts, tokens, dlogits, coef, score="sigmoid",
@@ -504,10 +507,10 @@ def moe_balance_loss_grad(logits, topk_ids, counts, tokens, dlogits, coef, score
     """dlogits [T][E]: dloss (1 if None) times the loss's gradient, from the
     counts and tokens that moe_balance_loss wrote."""
     where = "moe_balance_loss_grad"
-    cfg, dev = _balance(where, logits, topk_ids, counts, tokens, coef, score, seq_offsets)
+    cfg, dev, queue = _balance(where, stream, logits, topk_ids, counts, tokens, coef, score, seq_offsets)
     _fits(where, dev, dlogits, logits.dtype, logits.shape)
     if dloss is not None:
         _fits(where, dev, dloss, torch.float32, (1,))
     _check(lib().moe_balance_loss_grad(ctypes.byref(cfg), logits.data_ptr(), topk_ids.data_ptr(),
                                        _at(seq_offsets), counts.data_ptr(), tokens.data_ptr(),
-                                       _at(dloss), dlogits.data_ptr(), _queue(stream, dev)), where)
+                                       _at(dloss), dlogits.data_ptr(), queue), where)

@@ -56,11 +56,12 @@ def no_library(monkeypatch):
         def __getattr__(self, name):
             raise Reached
     monkeypatch.setattr(binding, "lib", Library)
-    monkeypatch.setattr(binding, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0)
 
 
 @pytest.mark.parametrize("name", _calls())
-def test_tensors_lie_on_the_current_device(name, no_library):
+def test_tensors_lie_on_the_current_device(name, no_library, monkeypatch):
     call, tensors = _calls()[name]
     with pytest.raises(Reached):                     # all on it: nothing is refused
         call([On.of(t) for t in tensors])
@@ -68,6 +69,10 @@ def test_tensors_lie_on_the_current_device(name, no_library):
         with pytest.raises(q.QmoeError) as ei:
             call([On.of(t, int(i in far)) for i, t in enumerate(tensors)])
         assert ei.value.status == q.MOE_ERR_INVALID_ARG, far
+    monkeypatch.setattr(binding, "_several", True)
+    monkeypatch.setattr(binding, "_current_device", lambda: 1)      # all on device 0, which is not the current one
+    with pytest.raises(q.QmoeError):
+        call([On.of(t) for t in tensors])
     for host in range(len(tensors)):
         with pytest.raises(q.QmoeError):
             call([t if i == host else On.of(t) for i, t in enumerate(tensors)])
