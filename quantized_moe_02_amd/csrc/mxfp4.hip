@@ -9,7 +9,7 @@
 // they round to nearest even and saturate at 6.
 //
 // Both directions move bytes and are bound by HBM (small calls: by the
-// launch: a row of 6144 takes 1.5 us each way).  A lane takes a chunk of eight inputs, four lanes a block, so a
+// launch: a row of 6144 takes 1.8 us each way).  A lane takes a chunk of eight inputs, four lanes a block, so a
 // wave reads (16-bit types) and writes whole lines; the four meet in two
 // cross-lane maxima.  Magnitudes compare as integers, two 16-bit ones per
 // instruction.  Rows may start at any element: the loads are declared

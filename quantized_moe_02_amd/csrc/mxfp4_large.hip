@@ -9,9 +9,9 @@
 // rows of `a` go through LDS by direct loads.  128 inputs per stage, two
 // stages: a K block's MFMAs take longer than the next block's loads.
 //
-// 4096 tokens, 8 of 256 experts, 4096 x 6144: 1.50 ms, 1.10 PFLOP/s (a library
-// product of 16384^3 in bf16: 1.36), MFMAs busy in 57 % of the cycles; what is left
-// is mostly an item's start and end.  32x32x16 MFMAs with half the LDS reads took
+// 4096 tokens, 8 of 256 experts, 4096 x 6144: 1.45 to 1.56 ms on average from card to
+// card, 1.06 to 1.14 PFLOP/s (a library product of 16384^3 in bf16: 1.36), MFMAs busy
+// in 57 % of the cycles; what is left is mostly an item's start and end.  32x32x16 MFMAs with half the LDS reads took
 // 1.60 to 1.72 ms.
 //
 // The next block's requests are spread over the first half of a block: issued

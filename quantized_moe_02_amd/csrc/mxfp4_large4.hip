@@ -15,8 +15,9 @@
 // block kb + 2 is requested, once every wave has block kb's last step in
 // registers; the requests are spread over the following steps.
 //
-// 16384 tokens, 8 of 256 experts, 4096 x 6144: 2.03 ms beside 0.05 for quantising
-// the tokens, 3.2 PFLOP/s, MFMAs busy in 43 % of the cycles.
+// 16384 tokens, 8 of 256 experts, 4096 x 6144: 1.97 to 2.13 ms on average from card
+// to card, beside 0.05 for quantising the tokens, 3.1 to 3.3 PFLOP/s, MFMAs busy in 43
+// % of the cycles.
 //
 // Scales: 16 blocks of a row at a time.  Where a row's bytes may start
 // anywhere, a thread loads the five aligned words around them, shifts them into

@@ -5,8 +5,9 @@
 // or the call is a few microseconds of latency.  So the rows come into LDS, the
 // weights straight from global memory into the matrix units' operands, whole
 // lines per row, and the four waves of a workgroup split the sum and add their
-// parts up in LDS, in a fixed order.  One token, 8 of 256 experts, 4096 x 6144: 23.5
-// us, 107 MB at 4.5 TB/s; 64 tokens, 76 experts, 6144 x 2048: 146 us.
+// parts up in LDS, in a fixed order.  One token, 8 of 256 experts, 4096 x 6144: 24.1
+// us (107 MB at 4.4 TB/s; shortest of 60 runs 23.4); 64 tokens, 76 experts, 6144 x
+// 2048: 156 us (145).
 #include <algorithm>
 #include <cmath>
 
@@ -41,7 +42,9 @@ hipError_t by_units(long units, long per, int threads, F&& launch) {
 // outputs.  A step is 256 inputs, a line of a row's codes: lane (lr, lq) takes
 // blocks 2 lq and 2 lq + 1 of row lr.  Wave w takes steps w, w + 4, ... of a
 // slab, the steps whose rows fit LDS (most calls have one slab, whose rows then
-// stay for every tile).  Two of a wave's steps are in flight: with three or
+// stay for every tile; of 9 to 16 rows it holds four steps, one of each wave, and
+// nothing is in flight from slab to slab: 76 of 256 experts, 6144 x 2048, 8 rows each
+// 131 us, 9 rows 154; 6144 x 1024, one slab either way, 74 and 75).  Two of a wave's steps are in flight: with three or
 // four, one token's gate and up (8 experts) took 24.3 and 27.6 us instead of
 // 23.4, the registers costing more waves than the loads gain.
 // ---------------------------------------------------------------------------
@@ -336,7 +339,9 @@ bool mid_is_faster(const MatmulArgs& g, int outputs) {
 }  // namespace
 
 hipError_t launch_mx_matmul(const MatmulArgs& g, bool a_mxfp4, hipStream_t s) {
-  // sources past 32-bit offsets: the few-row kernel, which has 64-bit addresses
+  // sources past 32-bit offsets: the few-row kernel, which has 64-bit addresses (32768
+  // rows of 256 experts, 4096 x 8192, gathered from 262144 rows: 11.5 ms, from 261000
+  // 1.9)
   const int64_t ldb = a_mxfp4 ? g.K / 2 : g.lda * 2;
   const int64_t span = (g.index ? (int64_t)g.a_rows : kFatRows) * ldb;
   const bool near = span < (int64_t)kOutside;
