@@ -452,7 +452,8 @@ typedef enum {
   MOE_DT_F32 = 0,   /* = MOE_OUT_F32 */
   MOE_DT_BF16 = 1,  /* = MOE_OUT_BF16 */
   MOE_DT_F16 = 2,
-  MOE_DT_MXFP4 = 3  /* codes and scales, rows packed without gaps */
+  MOE_DT_MXFP4 = 3, /* codes and scales, rows packed without gaps */
+  MOE_DT_E4M3 = 4   /* codes and scales, see the row operators */
 } moe_dtype;
 
 /* Rows to MXFP4.  Per block of 32: with e = floor(log2(largest magnitude)),
@@ -578,6 +579,160 @@ moe_status moe_balance_loss_grad(const moe_balance_config* cfg, const void* logi
                                  const int32_t* topk_ids, const int32_t* seq_offsets,
                                  const int32_t* counts, const int32_t* tokens, const float* dloss,
                                  void* dlogits, hipStream_t stream);
+
+/* Row operators
+ * -------------
+ * What lies between the products of an MoE layer, forward and backward: the
+ * norm before it, tokens' rows into expert order and back, SwiGLU.  The
+ * conventions above hold (device pointers, caller-owned buffers, checks before
+ * any HIP call, no floating-point atomics).  Matrices of MOE_DT_F32 and
+ * MOE_DT_BF16 have contiguous rows at a stride of their own (in elements, at
+ * least the columns) and any element alignment.  Arithmetic is fp32, sums are
+ * held in fp32 or more, and every result is rounded once, to nearest even, to
+ * the type it is stored in.  Outputs overlap nothing else of the call unless
+ * stated.  Columns: 1..65536 (more: MOE_ERR_UNSUPPORTED).
+ *
+ * MOE_DT_E4M3 rows hold one byte a value (E4M3 "fn": bias 7, no infinities,
+ * largest 448) and one fp32 scale a row, value = code * scale:
+ *   codes  uint8 [rows][cols] without gaps, 8-byte aligned; scale float32 [rows]
+ * A row is brought to it with scale = max(amax / 448, 2^-126), amax its largest
+ * magnitude, each code the nearest E4M3 value of x / scale (ties to even).  A
+ * row that holds an infinity or a NaN gets scale NaN and codes 0.
+ *
+ * Root-mean-square norm with the residual's addition.  Per row of cols values:
+ *   h = x + residual            (rounded to h's type; without a residual h = x)
+ *   y = h * m * w,  m = 1 / sqrt(mean(h^2) + eps)
+ * The norm goes by the rounded h, so that the gradient, which reads it, is the
+ * gradient of this very function.  mean(h^2) is held in float64: no row of
+ * finite h overflows it.  A NaN makes its row NaN, an infinity itself and the
+ * rest of its row 0. */
+typedef struct {
+  int32_t rows, cols;      /* rows <= 16 * MOE_MAX_TOKENS, else MOE_ERR_UNSUPPORTED */
+  int32_t x_dtype;         /* MOE_DT_F32 or MOE_DT_BF16, as every dtype but q_dtype */
+  int32_t residual_dtype;  /* of residual and h; ignored without a residual */
+  int32_t weight_dtype;
+  int32_t y_dtype;         /* ignored without y */
+  int32_t q_dtype;         /* MOE_DT_E4M3 or MOE_DT_MXFP4; ignored without q */
+  float eps;               /* finite and > 0 */
+  int64_t ldx, ldr, ldh, ldy;  /* row strides of x, residual, h, y */
+} moe_rmsnorm_config;
+
+/*   x         [rows][cols]
+ *   residual  [rows][cols], or NULL
+ *   weight    [cols]
+ *   h         [rows][cols] out, NULL if not wanted or without a residual; may be
+ *             `residual` itself (at the same stride), or x where the types agree
+ *   y         [rows][cols] out, or NULL
+ *   q, q_scale  out, or both NULL: y before its rounding, in q_dtype (E4M3 rows,
+ *             or MXFP4 as moe_mxfp4_quantize makes them, codes 16-byte aligned)
+ * At least one of h, y and q.  rows == 0 enqueues nothing. */
+moe_status moe_rmsnorm(const moe_rmsnorm_config* cfg, const void* x, const void* residual,
+                       const void* weight, void* h, void* y, uint8_t* q, void* q_scale,
+                       hipStream_t stream);
+
+/* Gradient of the norm, from the h that it wrote (x without a residual):
+ *   g = dy * w,  dx = dh + m * (g - h * m^2 * mean(g * h)),  dweight = sum over
+ * rows of dy * h * m.  dx is the gradient of x and of the residual alike; dh is
+ * the gradient that reaches h on the residual's own way.  The sums over a row are
+ * float64; dweight's are fp32 over the rows that one workgroup takes and float64
+ * over the workgroups.  Fields as in moe_rmsnorm_config. */
+typedef struct {
+  int32_t rows, cols;
+  int32_t h_dtype, weight_dtype, dy_dtype;
+  int32_t dx_dtype;        /* of dx and dh */
+  float eps;
+  int64_t ldh, lddy, lddh, lddx;  /* row strides of h, dy, dh, dx */
+} moe_rmsnorm_grad_config;
+
+/* Bytes of workspace moe_rmsnorm_grad needs for dweight (host output).  Enough
+ * for every call of no more rows and columns. */
+moe_status moe_rmsnorm_workspace_size(int32_t rows, int32_t cols, size_t* bytes);
+
+/*   dy, h     [rows][cols]; weight [cols]
+ *   dh        [rows][cols], or NULL for none
+ *   dx        [rows][cols] out; may be dh or dy itself (same type and stride)
+ *   dweight   float32 [cols] out, or NULL; then no workspace is needed
+ *   ws        256-byte aligned, of moe_rmsnorm_workspace_size bytes
+ * rows == 0 writes zeros to dweight. */
+moe_status moe_rmsnorm_grad(const moe_rmsnorm_grad_config* cfg, const void* dy, const void* h,
+                            const void* weight, const void* dh, void* dx, float* dweight,
+                            void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Tokens' rows into expert order and back.  `inv_perm` [tokens][top_k] holds the
+ * slot of each pick as moe_permute writes it: a row in [0, slots), each at most
+ * once.  Picks with another value (-1: dropped) take part in nothing.
+ * Limits: tokens >= 0, slots >= 0, top_k >= 1, else MOE_ERR_INVALID_ARG; tokens
+ * <= MOE_MAX_TOKENS, slots <= 16 * MOE_MAX_TOKENS, top_k <= 16, else
+ * MOE_ERR_UNSUPPORTED. */
+typedef struct {
+  int32_t tokens, cols, top_k, slots;
+  int32_t token_dtype;   /* of the token-major matrix */
+  int32_t row_dtype;     /* of the matrix in expert order */
+  int32_t addend_dtype;  /* moe_collect's addend; ignored without it */
+  int64_t ldt;           /* row stride of the token-major matrix */
+  int64_t ldr;           /* row stride of the matrix in expert order */
+  int64_t lda;           /* row stride of moe_collect's addend */
+} moe_rows_config;
+
+/* rows[inv_perm[t][i]] = x[t].  Rows of no pick are left as they are.
+ *   x [tokens][cols] of token_dtype, rows [slots][cols] out of row_dtype: both
+ * MOE_DT_F32 or MOE_DT_BF16 (rounded where they differ), or both MOE_DT_E4M3 or
+ * both MOE_DT_MXFP4 (codes and scales as they are; x_scale and row_scale as these
+ * formats have them, else NULL; ldt and ldr are cols).  Its gradient is
+ * moe_collect without weights. */
+moe_status moe_dispatch(const moe_rows_config* cfg, const void* x, const void* x_scale,
+                        const int32_t* inv_perm, void* rows, void* row_scale, hipStream_t stream);
+
+/* y[t] = addend[t] + sum_i weights[t][i] * rows[inv_perm[t][i]].
+ *   rows     [slots][cols] of row_dtype (F32 or BF16)
+ *   weights  float32 [tokens][top_k], or NULL for 1
+ *   addend   [tokens][cols] of addend_dtype (F32 or BF16), or NULL for 0; may be y
+ *            itself (same type and stride)
+ *   y        [tokens][cols] out of token_dtype (F32 or BF16) */
+moe_status moe_collect(const moe_rows_config* cfg, const void* rows, const int32_t* inv_perm,
+                       const float* weights, const void* addend, void* y, hipStream_t stream);
+
+/* Gradient of moe_collect:
+ *   drows[inv_perm[t][i]] = weights[t][i] * dy[t]
+ *   dweights[t][i] = sum over the columns of dy[t] * rows[inv_perm[t][i]]
+ *   dy        [tokens][cols] of token_dtype (F32 or BF16)
+ *   rows      [slots][cols] of row_dtype, stride ldr; needed for dweights alone
+ *   drows     [slots][cols] out of row_dtype, stride ldr, or NULL; rows of no pick
+ *             are left as they are; may be `rows` itself
+ *   dweights  float32 [tokens][top_k] out, or NULL; 0 for picks without a slot
+ * At least one of drows and dweights.  The addend's gradient is dy. */
+moe_status moe_collect_grad(const moe_rows_config* cfg, const void* dy, const void* rows,
+                            const int32_t* inv_perm, const float* weights, void* drows,
+                            float* dweights, hipStream_t stream);
+
+/* SwiGLU over rows [gate | up] in expert order:
+ *   out[r][j] = silu(gu[r][j]) * gu[r][cols + j],  silu(g) = g / (1 + e^-g).
+ * Rows from expert_offsets[n_experts] on belong to no expert: they are not read,
+ * and what belongs to them is left as it is.  An infinite gate gives what the
+ * formula gives: itself for +inf, NaN for -inf (and NaN in the gate's gradient). */
+typedef struct {
+  int32_t rows, cols;   /* rows <= 16 * MOE_MAX_TOKENS, else MOE_ERR_UNSUPPORTED */
+  int32_t n_experts;    /* places of expert_offsets' last entry; >= 1 */
+  int32_t gu_dtype;     /* MOE_DT_F32 or MOE_DT_BF16; of gu and dgu */
+  int32_t out_dtype;    /* of out: F32, BF16, E4M3 or MXFP4; of dh: F32 or BF16 */
+  int64_t ldg;          /* row stride of gu and dgu, >= 2 cols */
+  int64_t ldo;          /* row stride of out or dh; E4M3 and MXFP4: cols */
+} moe_swiglu_config;
+
+/*   gu        [rows][2 cols]
+ *   expert_offsets  int32 [n_experts + 1], or NULL: every row counts
+ *   out       [rows][cols] out; MXFP4 as moe_mxfp4_quantize makes it of the fp32
+ *             values (codes 16-byte aligned)
+ *   out_scale E4M3: float32 [rows]; MXFP4: uint8 [rows][ceil(cols / 32)]; else NULL */
+moe_status moe_swiglu(const moe_swiglu_config* cfg, const void* gu, const int32_t* expert_offsets,
+                      void* out, void* out_scale, hipStream_t stream);
+
+/* Its gradient, s = 1 / (1 + e^-g):
+ *   dgate = dh * up * s * (1 + g * (1 - s)),  dup = dh * g * s
+ *   dh   [rows][cols] of out_dtype, stride ldo
+ *   dgu  [rows][2 cols] out, stride ldg; may be gu itself */
+moe_status moe_swiglu_grad(const moe_swiglu_config* cfg, const void* gu, const void* dh,
+                           const int32_t* expert_offsets, void* dgu, hipStream_t stream);
 
 #ifdef __cplusplus
 }

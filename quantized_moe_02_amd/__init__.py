@@ -15,4 +15,7 @@ from .binding import (  # noqa: F401
     MoeMatmulConfig, MoeBalanceConfig, mxfp4_empty, moe_mxfp4_quantize, moe_mxfp4_dequantize,
     moe_mxfp4_matmul, moe_mxfp4_matmul_dx, make_balance_config, moe_balance_workspace_size,
     balance_workspace, moe_balance_loss, moe_balance_loss_grad,
+    MOE_DT_E4M3, MoeRmsnormConfig, MoeRmsnormGradConfig, MoeRowsConfig, MoeSwigluConfig,
+    moe_rmsnorm, moe_rmsnorm_workspace_size, rmsnorm_workspace, moe_rmsnorm_grad,
+    moe_dispatch, moe_collect, moe_collect_grad, moe_swiglu, moe_swiglu_grad,
 )

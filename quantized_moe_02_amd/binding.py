@@ -24,7 +24,7 @@ MOE_WFMT_INT4_ROW_F32, MOE_WFMT_INT8_ROW_F32, MOE_WFMT_INT2_ROW_F32 = 2, 3, 4
 MOE_OUT_F32, MOE_OUT_BF16 = 0, 1
 MOE_OPT_NO_GRID_WAIT, MOE_OPT_GRID_WAIT_NONE, MOE_OPT_INT8_ACTIVATIONS = 1, 2, 4
 MOE_FLAG_GRID_WAIT_TIMEOUT = 1
-MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16, MOE_DT_MXFP4 = 0, 1, 2, 3
+MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16, MOE_DT_MXFP4, MOE_DT_E4M3 = 0, 1, 2, 3, 4
 MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
 MOE_MAX_TOKENS = 262144
 MOE_NOALLOC_WS_BYTES = 32 << 20
@@ -82,6 +82,34 @@ class MoeBalanceConfig(ctypes.Structure):
                 ("logits_dtype", ctypes.c_int32), ("coef", ctypes.c_float)]
 
 
+class MoeRmsnormConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("residual_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("q_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldh", ctypes.c_int64),
+                ("ldy", ctypes.c_int64)]
+
+
+class MoeRmsnormGradConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("h_dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("dy_dtype", ctypes.c_int32),
+                ("dx_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("ldh", ctypes.c_int64),
+                ("lddy", ctypes.c_int64), ("lddh", ctypes.c_int64), ("lddx", ctypes.c_int64)]
+
+
+class MoeRowsConfig(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("cols", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("slots", ctypes.c_int32), ("token_dtype", ctypes.c_int32),
+                ("row_dtype", ctypes.c_int32), ("addend_dtype", ctypes.c_int32),
+                ("ldt", ctypes.c_int64), ("ldr", ctypes.c_int64), ("lda", ctypes.c_int64)]
+
+
+class MoeSwigluConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("n_experts", ctypes.c_int32),
+                ("gu_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("ldg", ctypes.c_int64), ("ldo", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -98,6 +126,7 @@ def lib() -> ctypes.CDLL:
         exp = ctypes.POINTER(MoeQExperts)
         i64 = ctypes.c_int64
         mmp, balp = ctypes.POINTER(MoeMatmulConfig), ctypes.POINTER(MoeBalanceConfig)
+        rowp, swip = ctypes.POINTER(MoeRowsConfig), ctypes.POINTER(MoeSwigluConfig)
         sig = {
             "moe_workspace_size": [cfgp, i32, ctypes.POINTER(sz)],
             "moe_route": [cfgp, i32, vp, vp, vp, vp, vp, vp, sz, vp],
@@ -124,6 +153,14 @@ def lib() -> ctypes.CDLL:
             "moe_balance_workspace_size": [balp, ctypes.POINTER(sz)],
             "moe_balance_loss": [balp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
             "moe_balance_loss_grad": [balp, vp, vp, vp, vp, vp, vp, vp, vp],
+            "moe_rmsnorm": [ctypes.POINTER(MoeRmsnormConfig), vp, vp, vp, vp, vp, vp, vp, vp],
+            "moe_rmsnorm_workspace_size": [i32, i32, ctypes.POINTER(sz)],
+            "moe_rmsnorm_grad": [ctypes.POINTER(MoeRmsnormGradConfig), vp, vp, vp, vp, vp, vp, vp, sz, vp],
+            "moe_dispatch": [rowp, vp, vp, vp, vp, vp, vp],
+            "moe_collect": [rowp, vp, vp, vp, vp, vp, vp],
+            "moe_collect_grad": [rowp, vp, vp, vp, vp, vp, vp, vp],
+            "moe_swiglu": [swip, vp, vp, vp, vp, vp],
+            "moe_swiglu_grad": [swip, vp, vp, vp, vp, vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -514,3 +551,218 @@ def moe_balance_loss_grad(logits, topk_ids, counts, tokens, dlogits, coef, score
     _check(lib().moe_balance_loss_grad(ctypes.byref(cfg), logits.data_ptr(), topk_ids.data_ptr(),
                                        _at(seq_offsets), counts.data_ptr(), tokens.data_ptr(),
                                        _at(dloss), dlogits.data_ptr(), queue), where)
+
+
+# ---- row operators -------------------------------------------------------------
+# Matrices in 8 bits are torch.float8_e4m3fn with fp32 scales [rows], in MXFP4
+# uint8 codes with uint8 scales (mxfp4_empty).  Arguments as above.
+_E4M3 = torch.float8_e4m3fn
+
+
+def _coded(where, dev, codes, scale, rows, cols):
+    """dtype of a matrix in 8 or 4 bits of this size, with its scales."""
+    _require(scale is not None, where)
+    if codes.dtype is _E4M3:
+        _fits(where, dev, codes, _E4M3, (rows, cols))
+        _fits(where, dev, scale, torch.float32, (rows,))
+        return MOE_DT_E4M3
+    nb = (cols + 31) // 32
+    _fits(where, dev, codes, torch.uint8, (rows, 16 * nb))
+    _fits(where, dev, scale, torch.uint8, (rows, nb))
+    return MOE_DT_MXFP4
+
+
+def _sized(where, dev, t, dtypes, rows, cols):
+    """dtype and row stride of a matrix of this size."""
+    r, c, ld = _matrix(where, dev, t, dtypes)
+    _require(r == rows and c == cols, where)
+    return _DT[t.dtype], ld
+
+
+def moe_rmsnorm(x, weight, eps, y=None, residual=None, h=None, q=None, q_scale=None, stream=None):
+    """h = x + residual (h = x without one) and y = h / sqrt(mean(h^2) + eps) * weight
+    over the rows of `x`; `q` with `q_scale` takes y in E4M3 or MXFP4.  h may be
+    `residual` itself."""
+    where = "moe_rmsnorm"
+    dev = x.get_device()
+    queue = _queue(where, stream, dev)
+    rows, cols, ldx = _matrix(where, dev, x, _OUT_DT)
+    _require(weight.dtype in _OUT_DT, where)
+    _fits(where, dev, weight, weight.dtype, (cols,))
+    rt = yt = qt = ldr = ldh = ldy = 0
+    if residual is not None:
+        rt, ldr = _sized(where, dev, residual, _OUT_DT, rows, cols)
+        if h is not None:
+            _, ldh = _sized(where, dev, h, (residual.dtype,), rows, cols)
+    if y is not None:
+        yt, ldy = _sized(where, dev, y, _OUT_DT, rows, cols)
+    if q is not None:
+        qt = _coded(where, dev, q, q_scale, rows, cols)
+    cfg = MoeRmsnormConfig(rows, cols, _DT[x.dtype], rt, _DT[weight.dtype], yt, qt, eps, ldx, ldr, ldh, ldy)
+    _check(lib().moe_rmsnorm(ctypes.byref(cfg), x.data_ptr(), _at(residual), weight.data_ptr(), _at(h), _at(y),
+                             _at(q), _at(q_scale), queue), where)
+
+
+def moe_rmsnorm_workspace_size(rows: int, cols: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_rmsnorm_workspace_size(rows, cols, ctypes.byref(n)), "moe_rmsnorm_workspace_size")
+    return n.value
+
+
+def rmsnorm_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor:
+    """A torch-allocated workspace for moe_rmsnorm_grad of this size."""
+    return torch.empty(moe_rmsnorm_workspace_size(rows, cols), dtype=torch.uint8, device=device)
+
+
+def moe_rmsnorm_grad(dy, h, weight, eps, dx, dh=None, dweight=None, ws=None, stream=None):
+    """dx: the gradient of moe_rmsnorm's x and residual, from the h that it wrote
+    (x without a residual), plus `dh`; dweight fp32 [cols].  Without `ws` a call
+    with dweight takes a workspace from torch's allocator, on its stream."""
+    where = "moe_rmsnorm_grad"
+    dev = dx.get_device()
+    queue = _queue(where, stream, dev)
+    rows, cols, lddx = _matrix(where, dev, dx, _OUT_DT)
+    ht, ldh = _sized(where, dev, h, _OUT_DT, rows, cols)
+    yt, lddy = _sized(where, dev, dy, _OUT_DT, rows, cols)
+    _require(weight.dtype in _OUT_DT, where)
+    _fits(where, dev, weight, weight.dtype, (cols,))
+    lddh = 0
+    if dh is not None:
+        _, lddh = _sized(where, dev, dh, (dx.dtype,), rows, cols)
+    n = 0
+    if dweight is not None:
+        _fits(where, dev, dweight, torch.float32, (cols,))
+        if ws is None:
+            # of the memory that belongs to the call's stream, whose order keeps it until the call has run
+            with torch.cuda.stream(torch.cuda.ExternalStream(queue) if queue else torch.cuda.default_stream()):
+                ws = torch.empty(moe_rmsnorm_workspace_size(rows, cols), dtype=torch.uint8, device=dx.device)
+    if ws is not None:
+        _require(ws.get_device() == dev and ws.dtype is torch.uint8 and ws.is_contiguous(), where)
+        n = ws.numel()
+    cfg = MoeRmsnormGradConfig(rows, cols, ht, _DT[weight.dtype], yt, _DT[dx.dtype], eps, ldh, lddy, lddh, lddx)
+    _check(lib().moe_rmsnorm_grad(ctypes.byref(cfg), dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _at(dh),
+                                  dx.data_ptr(), _at(dweight), _at(ws), n, queue), where)
+
+
+def _picks(where, dev, inv_perm, tokens):
+    shape = inv_perm.shape
+    _require(len(shape) == 2 and shape[0] == tokens, where)
+    _fits(where, dev, inv_perm, torch.int32, shape)
+    return shape[1]
+
+
+def moe_dispatch(x, inv_perm, rows, x_scale=None, row_scale=None, stream=None):
+    """rows[inv_perm[t, i]] = x[t]; picks outside [0, rows) take no row.  `x` and
+    `rows` are fp32 or bf16, or both in E4M3 or MXFP4 with their scales."""
+    where = "moe_dispatch"
+    dev = rows.get_device()
+    queue = _queue(where, stream, dev)
+    if x.dtype in _DT:
+        T, cols, ldt = _matrix(where, dev, x, _OUT_DT)
+        slots, rcols, ldr = _matrix(where, dev, rows, _OUT_DT)
+        _require(cols == rcols and x_scale is None and row_scale is None, where)
+        tt, rt = _DT[x.dtype], _DT[rows.dtype]
+    else:
+        _require(x.dim() == 2 and rows.dim() == 2 and rows.dtype is x.dtype, where)
+        T, slots = x.shape[0], rows.shape[0]
+        # of MXFP4 rows the last block counts whole: columns only say how many blocks there are
+        cols = ldt = ldr = x.shape[1] * (1 if x.dtype is _E4M3 else 2)
+        tt = _coded(where, dev, x, x_scale, T, cols)
+        rt = _coded(where, dev, rows, row_scale, slots, cols)
+    K = _picks(where, dev, inv_perm, T)
+    cfg = MoeRowsConfig(T, cols, K, slots, tt, rt, 0, ldt, ldr, 0)
+    _check(lib().moe_dispatch(ctypes.byref(cfg), x.data_ptr(), _at(x_scale), inv_perm.data_ptr(), rows.data_ptr(),
+                              _at(row_scale), queue), where)
+
+
+def moe_collect(rows, inv_perm, y, weights=None, addend=None, stream=None):
+    """y[t] = addend[t] + sum_i weights[t, i] * rows[inv_perm[t, i]]; picks outside
+    [0, rows) count for nothing.  The gradient of moe_dispatch is this call without
+    weights.  `addend` may be y itself."""
+    where = "moe_collect"
+    dev = y.get_device()
+    queue = _queue(where, stream, dev)
+    T, cols, ldt = _matrix(where, dev, y, _OUT_DT)
+    slots, rcols, ldr = _matrix(where, dev, rows, _OUT_DT)
+    _require(cols == rcols, where)
+    K = _picks(where, dev, inv_perm, T)
+    at = lda = 0
+    if addend is not None:
+        at, lda = _sized(where, dev, addend, _OUT_DT, T, cols)
+    if weights is not None:
+        _fits(where, dev, weights, torch.float32, (T, K))
+    cfg = MoeRowsConfig(T, cols, K, slots, _DT[y.dtype], _DT[rows.dtype], at, ldt, ldr, lda)
+    _check(lib().moe_collect(ctypes.byref(cfg), rows.data_ptr(), inv_perm.data_ptr(), _at(weights), _at(addend),
+                             y.data_ptr(), queue), where)
+
+
+def moe_collect_grad(dy, inv_perm, drows=None, weights=None, rows=None, dweights=None, stream=None):
+    """Gradient of moe_collect by its rows (drows[inv_perm[t, i]] = weights[t, i] *
+    dy[t]; rows of no pick are left as they are) and by its weights (dweights[t, i] =
+    dy[t] . rows[inv_perm[t, i]], 0 for picks without a row).  drows may be `rows`
+    itself."""
+    where = "moe_collect_grad"
+    dev = dy.get_device()
+    queue = _queue(where, stream, dev)
+    T, cols, ldt = _matrix(where, dev, dy, _OUT_DT)
+    _require(drows is not None or rows is not None, where)
+    like = drows if rows is None else rows
+    slots, rcols, ldr = _matrix(where, dev, like, _OUT_DT)
+    _require(cols == rcols, where)
+    if drows is not None and rows is not None:
+        _, ld = _sized(where, dev, drows, (rows.dtype,), slots, cols)
+        _require(ld == ldr or slots <= 1, where)
+    K = _picks(where, dev, inv_perm, T)
+    if weights is not None:
+        _fits(where, dev, weights, torch.float32, (T, K))
+    if dweights is not None:
+        _require(rows is not None, where)
+        _fits(where, dev, dweights, torch.float32, (T, K))
+    cfg = MoeRowsConfig(T, cols, K, slots, _DT[dy.dtype], _DT[like.dtype], 0, ldt, ldr, 0)
+    _check(lib().moe_collect_grad(ctypes.byref(cfg), dy.data_ptr(), _at(rows), inv_perm.data_ptr(), _at(weights),
+                                  _at(drows), _at(dweights), queue), where)
+
+
+def _gate_up(where, dev, gu, expert_offsets, rows, cols):
+    R, twice, ldg = _matrix(where, dev, gu, _OUT_DT)
+    _require(R == rows and twice == 2 * cols, where)
+    if expert_offsets is None:
+        return 1, ldg
+    shape = expert_offsets.shape
+    _require(len(shape) == 1 and shape[0] >= 2, where)
+    _fits(where, dev, expert_offsets, torch.int32, shape)
+    return shape[0] - 1, ldg
+
+
+def moe_swiglu(gu, out, out_scale=None, expert_offsets=None, stream=None):
+    """out = silu(gate) * up over rows [gate | up]; `out` fp32, bf16, or E4M3 or
+    MXFP4 with `out_scale`.  Rows from expert_offsets[-1] on are left as they are."""
+    where = "moe_swiglu"
+    dev = gu.get_device()
+    queue = _queue(where, stream, dev)
+    _require(gu.dim() == 2 and gu.shape[1] % 2 == 0, where)
+    rows, cols = gu.shape[0], gu.shape[1] // 2
+    if out.dtype in _DT:
+        _require(out_scale is None, where)
+        ot, ldo = _sized(where, dev, out, _OUT_DT, rows, cols)
+    else:
+        ot, ldo = _coded(where, dev, out, out_scale, rows, cols), cols
+    E, ldg = _gate_up(where, dev, gu, expert_offsets, rows, cols)
+    cfg = MoeSwigluConfig(rows, cols, E, _DT[gu.dtype], ot, ldg, ldo)
+    _check(lib().moe_swiglu(ctypes.byref(cfg), gu.data_ptr(), _at(expert_offsets), out.data_ptr(), _at(out_scale), queue),
+           where)
+
+
+def moe_swiglu_grad(gu, dh, dgu, expert_offsets=None, stream=None):
+    """dgu: the gradient of moe_swiglu's gate and up from that of its output.  dgu may
+    be `gu` itself."""
+    where = "moe_swiglu_grad"
+    dev = gu.get_device()
+    queue = _queue(where, stream, dev)
+    rows, cols, ldo = _matrix(where, dev, dh, _OUT_DT)
+    E, ldg = _gate_up(where, dev, gu, expert_offsets, rows, cols)
+    _, ld = _sized(where, dev, dgu, (gu.dtype,), rows, 2 * cols)
+    _require(ld == ldg or rows <= 1, where)
+    cfg = MoeSwigluConfig(rows, cols, E, _DT[gu.dtype], _DT[dh.dtype], ldg, ldo)
+    _check(lib().moe_swiglu_grad(ctypes.byref(cfg), gu.data_ptr(), dh.data_ptr(), _at(expert_offsets), dgu.data_ptr(),
+                                 queue), where)

@@ -1,0 +1,82 @@
+// Internal interfaces of the row operators (norm, dispatch and collect,
+// SwiGLU), between their C-ABI layer (rows_api.cpp) and the kernel launchers.
+#pragma once
+
+#include "operators_internal.h"
+
+namespace qmoe {
+
+constexpr int kRowMaxCols = 65536;
+constexpr int kRowMaxRows = 16 * MOE_MAX_TOKENS;
+
+// A matrix in device memory; ld in elements.
+struct RowMat {
+  void* p;
+  int64_t ld;
+  int dtype;
+};
+
+struct NormArgs {
+  RowMat x, res, h, y;     // res.p, h.p, y.p nullable
+  const void* w;
+  int w_dtype;
+  void* q;                 // nullable: E4M3 codes or MXFP4 codes
+  void* q_scale;
+  int q_dtype;
+  int rows, cols;
+  float eps;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s);
+
+struct NormGradArgs {
+  RowMat h, dy, dh, dx;    // dh.p nullable
+  const void* w;
+  int w_dtype;
+  float* dw;               // nullable
+  float* part;             // [workgroups][cols]: the workgroups' sums for dw
+  int rows, cols;
+  float eps;
+};
+// The most workgroups, a row of `part` each, that the gradient of no more rows
+// takes, whatever its columns.
+int norm_grad_most_blocks(int rows);
+hipError_t launch_rmsnorm_grad(const NormGradArgs& a, hipStream_t s);
+
+struct DispatchArgs {
+  RowMat x, rows;
+  const uint8_t* x_scale;  // E4M3, MXFP4: scale_bytes of them a row
+  uint8_t* row_scale;
+  int scale_bytes;
+  const int32_t* inv;
+  int T, K, slots, cols;
+};
+hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s);
+
+struct CollectArgs {
+  RowMat rows, add, y;     // add.p nullable
+  const int32_t* inv;
+  const float* w;          // nullable
+  int T, K, slots, cols;
+};
+hipError_t launch_collect(const CollectArgs& a, hipStream_t s);
+
+struct CollectGradArgs {
+  RowMat dy, rows, drows;  // rows.p, drows.p nullable
+  const int32_t* inv;
+  const float* w;          // nullable
+  float* dw;               // nullable
+  int T, K, slots, cols;
+};
+hipError_t launch_collect_grad(const CollectGradArgs& a, hipStream_t s);
+
+struct SwigluArgs {
+  RowMat gu, out;          // out: of the gradient, dh
+  RowMat dgu;              // of the gradient
+  void* out_scale;
+  const int32_t* end;      // nullable: the row behind the last that counts
+  int rows, cols;
+};
+hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s);
+hipError_t launch_swiglu_grad(const SwigluArgs& a, hipStream_t s);
+
+}  // namespace qmoe
