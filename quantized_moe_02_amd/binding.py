@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -126,7 +127,6 @@ def lib() -> ctypes.CDLL:
         exp = ctypes.POINTER(MoeQExperts)
         i64 = ctypes.c_int64
         mmp, balp = ctypes.POINTER(MoeMatmulConfig), ctypes.POINTER(MoeBalanceConfig)
-        rowp, swip = ctypes.POINTER(MoeRowsConfig), ctypes.POINTER(MoeSwigluConfig)
         sig = {
             "moe_workspace_size": [cfgp, i32, ctypes.POINTER(sz)],
             "moe_route": [cfgp, i32, vp, vp, vp, vp, vp, vp, sz, vp],
@@ -153,14 +153,15 @@ def lib() -> ctypes.CDLL:
             "moe_balance_workspace_size": [balp, ctypes.POINTER(sz)],
             "moe_balance_loss": [balp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
             "moe_balance_loss_grad": [balp, vp, vp, vp, vp, vp, vp, vp, vp],
-            "moe_rmsnorm": [ctypes.POINTER(MoeRmsnormConfig), vp, vp, vp, vp, vp, vp, vp, vp],
+            # the row operators' structs come as packed bytes or by reference
+            "moe_rmsnorm": [vp, vp, vp, vp, vp, vp, vp, vp, vp],
             "moe_rmsnorm_workspace_size": [i32, i32, ctypes.POINTER(sz)],
-            "moe_rmsnorm_grad": [ctypes.POINTER(MoeRmsnormGradConfig), vp, vp, vp, vp, vp, vp, vp, sz, vp],
-            "moe_dispatch": [rowp, vp, vp, vp, vp, vp, vp],
-            "moe_collect": [rowp, vp, vp, vp, vp, vp, vp],
-            "moe_collect_grad": [rowp, vp, vp, vp, vp, vp, vp, vp],
-            "moe_swiglu": [swip, vp, vp, vp, vp, vp],
-            "moe_swiglu_grad": [swip, vp, vp, vp, vp, vp],
+            "moe_rmsnorm_grad": [vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+            "moe_dispatch": [vp, vp, vp, vp, vp, vp, vp],
+            "moe_collect": [vp, vp, vp, vp, vp, vp, vp],
+            "moe_collect_grad": [vp, vp, vp, vp, vp, vp, vp, vp],
+            "moe_swiglu": [vp, vp, vp, vp, vp, vp],
+            "moe_swiglu_grad": [vp, vp, vp, vp, vp, vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -555,8 +556,45 @@ def moe_balance_loss_grad(logits, topk_ids, counts, tokens, dlogits, coef, score
 
 # ---- row operators -------------------------------------------------------------
 # Matrices in 8 bits are torch.float8_e4m3fn with fp32 scales [rows], in MXFP4
-# uint8 codes with uint8 scales (mxfp4_empty).  Arguments as above.
-_E4M3 = torch.float8_e4m3fn
+# uint8 codes with uint8 scales (mxfp4_empty).  Arguments as above.  A call of a
+# few rows costs what its checks cost, so each reads a tensor's properties once
+# and the C structs are packed.
+_E4M3, _U8, _I32, _F32 = torch.float8_e4m3fn, torch.uint8, torch.int32, torch.float32
+_PLAIN = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16}
+
+
+def _packer(config):
+    """bytes of a ctypes struct of int32, float and int64 fields from their values."""
+    code = {ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_int64: "q"}
+    s = struct.Struct("@" + "".join(code[t] for _, t in config._fields_))
+    assert s.size == ctypes.sizeof(config)
+    return s.pack
+
+
+_norm_config, _norm_grad_config = _packer(MoeRmsnormConfig), _packer(MoeRmsnormGradConfig)
+_rows_config, _swiglu_config = _packer(MoeRowsConfig), _packer(MoeSwigluConfig)
+
+
+def _plain(where: str, dev: int, t: torch.Tensor):
+    """dtype, rows, columns and row stride of an fp32 or bf16 matrix on this device
+    whose rows are contiguous."""
+    dt, shape = _PLAIN.get(t.dtype), t.shape
+    if dt is None or len(shape) != 2 or t.get_device() != dev:
+        raise QmoeError(MOE_ERR_INVALID_ARG, where)
+    rows, cols = shape
+    if t.is_contiguous():
+        return dt, rows, cols, cols or 1
+    ld, step = t.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
+        raise QmoeError(MOE_ERR_INVALID_ARG, where)
+    return dt, rows, cols, ld if rows > 1 else cols or 1
+
+
+def _weight(where, dev, w, cols):
+    dt = _PLAIN.get(w.dtype)
+    if dt is None or w.shape != (cols,) or w.get_device() != dev or not w.is_contiguous():
+        raise QmoeError(MOE_ERR_INVALID_ARG, where)
+    return dt
 
 
 def _coded(where, dev, codes, scale, rows, cols):
@@ -564,19 +602,12 @@ def _coded(where, dev, codes, scale, rows, cols):
     _require(scale is not None, where)
     if codes.dtype is _E4M3:
         _fits(where, dev, codes, _E4M3, (rows, cols))
-        _fits(where, dev, scale, torch.float32, (rows,))
+        _fits(where, dev, scale, _F32, (rows,))
         return MOE_DT_E4M3
     nb = (cols + 31) // 32
-    _fits(where, dev, codes, torch.uint8, (rows, 16 * nb))
-    _fits(where, dev, scale, torch.uint8, (rows, nb))
+    _fits(where, dev, codes, _U8, (rows, 16 * nb))
+    _fits(where, dev, scale, _U8, (rows, nb))
     return MOE_DT_MXFP4
-
-
-def _sized(where, dev, t, dtypes, rows, cols):
-    """dtype and row stride of a matrix of this size."""
-    r, c, ld = _matrix(where, dev, t, dtypes)
-    _require(r == rows and c == cols, where)
-    return _DT[t.dtype], ld
 
 
 def moe_rmsnorm(x, weight, eps, y=None, residual=None, h=None, q=None, q_scale=None, stream=None):
@@ -586,21 +617,32 @@ def moe_rmsnorm(x, weight, eps, y=None, residual=None, h=None, q=None, q_scale=N
     where = "moe_rmsnorm"
     dev = x.get_device()
     queue = _queue(where, stream, dev)
-    rows, cols, ldx = _matrix(where, dev, x, _OUT_DT)
-    _require(weight.dtype in _OUT_DT, where)
-    _fits(where, dev, weight, weight.dtype, (cols,))
+    xt, rows, cols, ldx = _plain(where, dev, x)
+    wt = _weight(where, dev, weight, cols)
+    size = rows, cols
     rt = yt = qt = ldr = ldh = ldy = 0
+    rp = hp = yp = qp = sp = None
     if residual is not None:
-        rt, ldr = _sized(where, dev, residual, _OUT_DT, rows, cols)
-        if h is not None:
-            _, ldh = _sized(where, dev, h, (residual.dtype,), rows, cols)
+        rt, r, c, ldr = _plain(where, dev, residual)
+        _require((r, c) == size, where)
+        rp = residual.data_ptr()
+    if h is not None:
+        ht, r, c, ldh = _plain(where, dev, h)
+        _require((r, c) == size and rp is not None and ht == rt, where)
+        hp = h.data_ptr()
     if y is not None:
-        yt, ldy = _sized(where, dev, y, _OUT_DT, rows, cols)
+        yt, r, c, ldy = _plain(where, dev, y)
+        _require((r, c) == size, where)
+        yp = y.data_ptr()
     if q is not None:
         qt = _coded(where, dev, q, q_scale, rows, cols)
-    cfg = MoeRmsnormConfig(rows, cols, _DT[x.dtype], rt, _DT[weight.dtype], yt, qt, eps, ldx, ldr, ldh, ldy)
-    _check(lib().moe_rmsnorm(ctypes.byref(cfg), x.data_ptr(), _at(residual), weight.data_ptr(), _at(h), _at(y),
-                             _at(q), _at(q_scale), queue), where)
+        qp = q.data_ptr()
+    if q_scale is not None:
+        sp = q_scale.data_ptr()
+    status = lib().moe_rmsnorm(_norm_config(rows, cols, xt, rt, wt, yt, qt, eps, ldx, ldr, ldh, ldy), x.data_ptr(), rp,
+                               weight.data_ptr(), hp, yp, qp, sp, queue)
+    if status:
+        raise QmoeError(status, where)
 
 
 def moe_rmsnorm_workspace_size(rows: int, cols: int) -> int:
@@ -621,33 +663,41 @@ def moe_rmsnorm_grad(dy, h, weight, eps, dx, dh=None, dweight=None, ws=None, str
     where = "moe_rmsnorm_grad"
     dev = dx.get_device()
     queue = _queue(where, stream, dev)
-    rows, cols, lddx = _matrix(where, dev, dx, _OUT_DT)
-    ht, ldh = _sized(where, dev, h, _OUT_DT, rows, cols)
-    yt, lddy = _sized(where, dev, dy, _OUT_DT, rows, cols)
-    _require(weight.dtype in _OUT_DT, where)
-    _fits(where, dev, weight, weight.dtype, (cols,))
-    lddh = 0
+    xt, rows, cols, lddx = _plain(where, dev, dx)
+    ht, r, c, ldh = _plain(where, dev, h)
+    yt, r2, c2, lddy = _plain(where, dev, dy)
+    _require(r == r2 == rows and c == c2 == cols, where)
+    wt = _weight(where, dev, weight, cols)
+    lddh = n = 0
+    dp = wp = sp = None
     if dh is not None:
-        _, lddh = _sized(where, dev, dh, (dx.dtype,), rows, cols)
-    n = 0
+        dt, r, c, lddh = _plain(where, dev, dh)
+        _require(dt == xt and r == rows and c == cols, where)
+        dp = dh.data_ptr()
     if dweight is not None:
-        _fits(where, dev, dweight, torch.float32, (cols,))
+        _fits(where, dev, dweight, _F32, (cols,))
+        wp = dweight.data_ptr()
         if ws is None:
             # of the memory that belongs to the call's stream, whose order keeps it until the call has run
             with torch.cuda.stream(torch.cuda.ExternalStream(queue) if queue else torch.cuda.default_stream()):
                 ws = torch.empty(moe_rmsnorm_workspace_size(rows, cols), dtype=torch.uint8, device=dx.device)
     if ws is not None:
-        _require(ws.get_device() == dev and ws.dtype is torch.uint8 and ws.is_contiguous(), where)
-        n = ws.numel()
-    cfg = MoeRmsnormGradConfig(rows, cols, ht, _DT[weight.dtype], yt, _DT[dx.dtype], eps, ldh, lddy, lddh, lddx)
-    _check(lib().moe_rmsnorm_grad(ctypes.byref(cfg), dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _at(dh),
-                                  dx.data_ptr(), _at(dweight), _at(ws), n, queue), where)
+        _require(ws.get_device() == dev and ws.dtype is _U8 and ws.is_contiguous(), where)
+        n, sp = ws.numel(), ws.data_ptr()
+    status = lib().moe_rmsnorm_grad(_norm_grad_config(rows, cols, ht, wt, yt, xt, eps, ldh, lddy, lddh, lddx), dy.data_ptr(),
+                                    h.data_ptr(), weight.data_ptr(), dp, dx.data_ptr(), wp, sp, n, queue)
+    if status:
+        raise QmoeError(status, where)
 
 
-def _picks(where, dev, inv_perm, tokens):
+def _picks(where, dev, inv_perm, tokens, weights=None):
+    """Picks a token; `weights` (if any) fit them."""
     shape = inv_perm.shape
-    _require(len(shape) == 2 and shape[0] == tokens, where)
-    _fits(where, dev, inv_perm, torch.int32, shape)
+    if len(shape) != 2 or shape[0] != tokens:
+        raise QmoeError(MOE_ERR_INVALID_ARG, where)
+    _fits(where, dev, inv_perm, _I32, shape)
+    if weights is not None:
+        _fits(where, dev, weights, _F32, shape)
     return shape[1]
 
 
@@ -657,11 +707,11 @@ def moe_dispatch(x, inv_perm, rows, x_scale=None, row_scale=None, stream=None):
     where = "moe_dispatch"
     dev = rows.get_device()
     queue = _queue(where, stream, dev)
-    if x.dtype in _DT:
-        T, cols, ldt = _matrix(where, dev, x, _OUT_DT)
-        slots, rcols, ldr = _matrix(where, dev, rows, _OUT_DT)
+    xs = rs = None
+    if x.dtype in _PLAIN:
+        tt, T, cols, ldt = _plain(where, dev, x)
+        rt, slots, rcols, ldr = _plain(where, dev, rows)
         _require(cols == rcols and x_scale is None and row_scale is None, where)
-        tt, rt = _DT[x.dtype], _DT[rows.dtype]
     else:
         _require(x.dim() == 2 and rows.dim() == 2 and rows.dtype is x.dtype, where)
         T, slots = x.shape[0], rows.shape[0]
@@ -669,10 +719,12 @@ def moe_dispatch(x, inv_perm, rows, x_scale=None, row_scale=None, stream=None):
         cols = ldt = ldr = x.shape[1] * (1 if x.dtype is _E4M3 else 2)
         tt = _coded(where, dev, x, x_scale, T, cols)
         rt = _coded(where, dev, rows, row_scale, slots, cols)
+        xs, rs = x_scale.data_ptr(), row_scale.data_ptr()
     K = _picks(where, dev, inv_perm, T)
-    cfg = MoeRowsConfig(T, cols, K, slots, tt, rt, 0, ldt, ldr, 0)
-    _check(lib().moe_dispatch(ctypes.byref(cfg), x.data_ptr(), _at(x_scale), inv_perm.data_ptr(), rows.data_ptr(),
-                              _at(row_scale), queue), where)
+    status = lib().moe_dispatch(_rows_config(T, cols, K, slots, tt, rt, 0, ldt, ldr, 0), x.data_ptr(), xs, inv_perm.data_ptr(),
+                                rows.data_ptr(), rs, queue)
+    if status:
+        raise QmoeError(status, where)
 
 
 def moe_collect(rows, inv_perm, y, weights=None, addend=None, stream=None):
@@ -682,18 +734,20 @@ def moe_collect(rows, inv_perm, y, weights=None, addend=None, stream=None):
     where = "moe_collect"
     dev = y.get_device()
     queue = _queue(where, stream, dev)
-    T, cols, ldt = _matrix(where, dev, y, _OUT_DT)
-    slots, rcols, ldr = _matrix(where, dev, rows, _OUT_DT)
-    _require(cols == rcols, where)
-    K = _picks(where, dev, inv_perm, T)
+    yt, T, cols, ldt = _plain(where, dev, y)
+    rt, slots, rcols, ldr = _plain(where, dev, rows)
+    K = _picks(where, dev, inv_perm, T, weights)
     at = lda = 0
+    ap = None
     if addend is not None:
-        at, lda = _sized(where, dev, addend, _OUT_DT, T, cols)
-    if weights is not None:
-        _fits(where, dev, weights, torch.float32, (T, K))
-    cfg = MoeRowsConfig(T, cols, K, slots, _DT[y.dtype], _DT[rows.dtype], at, ldt, ldr, lda)
-    _check(lib().moe_collect(ctypes.byref(cfg), rows.data_ptr(), inv_perm.data_ptr(), _at(weights), _at(addend),
-                             y.data_ptr(), queue), where)
+        at, r, c, lda = _plain(where, dev, addend)
+        _require(r == T and c == cols, where)
+        ap = addend.data_ptr()
+    _require(cols == rcols, where)
+    status = lib().moe_collect(_rows_config(T, cols, K, slots, yt, rt, at, ldt, ldr, lda), rows.data_ptr(), inv_perm.data_ptr(),
+                               None if weights is None else weights.data_ptr(), ap, y.data_ptr(), queue)
+    if status:
+        raise QmoeError(status, where)
 
 
 def moe_collect_grad(dy, inv_perm, drows=None, weights=None, rows=None, dweights=None, stream=None):
@@ -704,34 +758,37 @@ def moe_collect_grad(dy, inv_perm, drows=None, weights=None, rows=None, dweights
     where = "moe_collect_grad"
     dev = dy.get_device()
     queue = _queue(where, stream, dev)
-    T, cols, ldt = _matrix(where, dev, dy, _OUT_DT)
-    _require(drows is not None or rows is not None, where)
+    yt, T, cols, ldt = _plain(where, dev, dy)
+    K = _picks(where, dev, inv_perm, T, weights)
     like = drows if rows is None else rows
-    slots, rcols, ldr = _matrix(where, dev, like, _OUT_DT)
+    _require(like is not None, where)
+    rt, slots, rcols, ldr = _plain(where, dev, like)
     _require(cols == rcols, where)
-    if drows is not None and rows is not None:
-        _, ld = _sized(where, dev, drows, (rows.dtype,), slots, cols)
-        _require(ld == ldr or slots <= 1, where)
-    K = _picks(where, dev, inv_perm, T)
-    if weights is not None:
-        _fits(where, dev, weights, torch.float32, (T, K))
+    rp = wp = None
+    if rows is not None:
+        rp = rows.data_ptr()
+        if drows is not None:
+            dt, r, c, ld = _plain(where, dev, drows)
+            _require(dt == rt and r == slots and c == cols and ld == ldr, where)
     if dweights is not None:
-        _require(rows is not None, where)
-        _fits(where, dev, dweights, torch.float32, (T, K))
-    cfg = MoeRowsConfig(T, cols, K, slots, _DT[dy.dtype], _DT[like.dtype], 0, ldt, ldr, 0)
-    _check(lib().moe_collect_grad(ctypes.byref(cfg), dy.data_ptr(), _at(rows), inv_perm.data_ptr(), _at(weights),
-                                  _at(drows), _at(dweights), queue), where)
+        _require(rp is not None, where)
+        _fits(where, dev, dweights, _F32, (T, K))
+        wp = dweights.data_ptr()
+    status = lib().moe_collect_grad(_rows_config(T, cols, K, slots, yt, rt, 0, ldt, ldr, 0), dy.data_ptr(), rp,
+                                    inv_perm.data_ptr(), None if weights is None else weights.data_ptr(),
+                                    None if drows is None else drows.data_ptr(), wp, queue)
+    if status:
+        raise QmoeError(status, where)
 
 
-def _gate_up(where, dev, gu, expert_offsets, rows, cols):
-    R, twice, ldg = _matrix(where, dev, gu, _OUT_DT)
-    _require(R == rows and twice == 2 * cols, where)
+def _experts(where, dev, expert_offsets):
+    """Experts of a table of offsets; without one every row counts."""
     if expert_offsets is None:
-        return 1, ldg
+        return 1
     shape = expert_offsets.shape
     _require(len(shape) == 1 and shape[0] >= 2, where)
-    _fits(where, dev, expert_offsets, torch.int32, shape)
-    return shape[0] - 1, ldg
+    _fits(where, dev, expert_offsets, _I32, shape)
+    return shape[0] - 1
 
 
 def moe_swiglu(gu, out, out_scale=None, expert_offsets=None, stream=None):
@@ -740,17 +797,21 @@ def moe_swiglu(gu, out, out_scale=None, expert_offsets=None, stream=None):
     where = "moe_swiglu"
     dev = gu.get_device()
     queue = _queue(where, stream, dev)
-    _require(gu.dim() == 2 and gu.shape[1] % 2 == 0, where)
-    rows, cols = gu.shape[0], gu.shape[1] // 2
-    if out.dtype in _DT:
-        _require(out_scale is None, where)
-        ot, ldo = _sized(where, dev, out, _OUT_DT, rows, cols)
+    gt, rows, twice, ldg = _plain(where, dev, gu)
+    cols = twice >> 1
+    sp = None
+    if out.dtype in _PLAIN:
+        ot, r, c, ldo = _plain(where, dev, out)
+        _require(r == rows and 2 * c == twice and out_scale is None, where)
     else:
+        _require(2 * cols == twice, where)
         ot, ldo = _coded(where, dev, out, out_scale, rows, cols), cols
-    E, ldg = _gate_up(where, dev, gu, expert_offsets, rows, cols)
-    cfg = MoeSwigluConfig(rows, cols, E, _DT[gu.dtype], ot, ldg, ldo)
-    _check(lib().moe_swiglu(ctypes.byref(cfg), gu.data_ptr(), _at(expert_offsets), out.data_ptr(), _at(out_scale), queue),
-           where)
+        sp = out_scale.data_ptr()
+    E = _experts(where, dev, expert_offsets)
+    status = lib().moe_swiglu(_swiglu_config(rows, cols, E, gt, ot, ldg, ldo), gu.data_ptr(),
+                              None if expert_offsets is None else expert_offsets.data_ptr(), out.data_ptr(), sp, queue)
+    if status:
+        raise QmoeError(status, where)
 
 
 def moe_swiglu_grad(gu, dh, dgu, expert_offsets=None, stream=None):
@@ -759,10 +820,12 @@ def moe_swiglu_grad(gu, dh, dgu, expert_offsets=None, stream=None):
     where = "moe_swiglu_grad"
     dev = gu.get_device()
     queue = _queue(where, stream, dev)
-    rows, cols, ldo = _matrix(where, dev, dh, _OUT_DT)
-    E, ldg = _gate_up(where, dev, gu, expert_offsets, rows, cols)
-    _, ld = _sized(where, dev, dgu, (gu.dtype,), rows, 2 * cols)
-    _require(ld == ldg or rows <= 1, where)
-    cfg = MoeSwigluConfig(rows, cols, E, _DT[gu.dtype], _DT[dh.dtype], ldg, ldo)
-    _check(lib().moe_swiglu_grad(ctypes.byref(cfg), gu.data_ptr(), dh.data_ptr(), _at(expert_offsets), dgu.data_ptr(),
-                                 queue), where)
+    gt, rows, twice, ldg = _plain(where, dev, gu)
+    ht, r, cols, ldo = _plain(where, dev, dh)
+    dt, r2, c2, ld = _plain(where, dev, dgu)
+    _require(r == r2 == rows and twice == c2 == 2 * cols and dt == gt and ld == ldg, where)
+    E = _experts(where, dev, expert_offsets)
+    status = lib().moe_swiglu_grad(_swiglu_config(rows, cols, E, gt, ht, ldg, ldo), gu.data_ptr(), dh.data_ptr(),
+                                   None if expert_offsets is None else expert_offsets.data_ptr(), dgu.data_ptr(), queue)
+    if status:
+        raise QmoeError(status, where)

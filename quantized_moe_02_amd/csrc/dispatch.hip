@@ -12,77 +12,16 @@ namespace qmoe {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kMaxK = 16;
+constexpr int64_t kGradFill = 1 << 17;   // lanes that fill the chip
 
-// How tokens and the chunks of their rows lie over workgroups: rows of 64 chunks
-// and more in `parts` workgroups of `threads` lanes, shorter ones 2^bits lanes a
-// token.
-struct TokenMap {
-  int parts, threads, bits;
-  int first;                // token of the launch's first workgroup
-};
-
-TokenMap token_map(int chunks) {
-  if (chunks > 32) {
-    const int parts = (chunks + kBlock - 1) / kBlock;
-    const int each = (chunks + parts - 1) / parts;
-    return {parts, (each + kWave - 1) / kWave * kWave, -1, 0};
-  }
-  int bits = 0;
-  while ((1 << bits) < chunks) ++bits;
-  return {1, kBlock, bits, 0};
-}
-
-// Calls f(workgroups, map) for runs of tokens of at most 2^31 work items: a launch
-// has to stay below 2^32.
-template <class F>
-hipError_t by_tokens(TokenMap m, int T, F&& f) {
-  const int most = m.bits < 0 ? (int)((1u << 31) / ((unsigned)m.parts * kBlock)) : 1 << 20;
-  for (; m.first < T; m.first += most) {
-    const unsigned n = (unsigned)std::min(most, T - m.first);
-    f(m.bits < 0 ? n * m.parts : ((n << m.bits) + kBlock - 1) / kBlock, m);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
-}
-
-// Token and chunk of a lane; the token is uniform where rows are long.
-template <bool LONG>
-__device__ __forceinline__ void locate(const TokenMap& m, int& t, int& c) {
-  if constexpr (LONG) {
-    const unsigned row = blockIdx.x / (unsigned)m.parts;
-    c = (blockIdx.x - row * m.parts) * blockDim.x + threadIdx.x;
-    t = m.first + row;
-  } else {
-    const unsigned at = blockIdx.x * kBlock + threadIdx.x;
-    t = m.first + (at >> m.bits);
-    c = at & ((1u << m.bits) - 1);
-  }
-}
-
-// Bytes [at, at + n) of a row of bytes, n <= 16.
-__device__ __forceinline__ uint4 load_bytes16(const uint8_t* p, int n) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (n >= 16) {
-    __builtin_memcpy(&v, p, 16);
-  } else {
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 15; ++i)
-      if (i < n) w[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
-    v = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  return v;
-}
-__device__ __forceinline__ void store_bytes16(uint8_t* p, int n, const uint4& v) {
-  if (n >= 16) {
-    __builtin_memcpy(p, &v, 16);
-  } else {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 15; ++i)
-      if (i < n) p[i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
+// The first n (0 < n < 16) of 16 bytes, as runs of eight, four, two and one.
+__device__ __forceinline__ void copy_bytes(uint8_t* to, const uint8_t* from, int n) {
+  for (int at = 0; at < n;) {
+    const int rest = n - at;
+    if (rest >= 8) __builtin_memcpy(to + at, from + at, 8), at += 8;
+    else if (rest >= 4) __builtin_memcpy(to + at, from + at, 4), at += 4;
+    else if (rest >= 2) __builtin_memcpy(to + at, from + at, 2), at += 2;
+    else to[at] = from[at], at += 1;
   }
 }
 
@@ -96,139 +35,192 @@ struct CopyArgs {
   int T, K, slots;
 };
 
-// Rows as they are, then their scales: chunk `chunks` and the following ones.
+// Rows as they are, then their scales: chunk `chunks` and the following ones.  A row's
+// last chunk ends where the row ends (Span); of less than 16 bytes it goes in pieces.
 template <bool LONG>
-__global__ void __launch_bounds__(kBlock) dispatch_copy_kernel(CopyArgs a, TokenMap m) {
+__global__ void __launch_bounds__(kBlock) dispatch_copy_kernel(CopyArgs a, RowMap m) {
   int t, c;
   locate<LONG>(m, t, c);
   if (t >= a.T) return;
+  const int64_t pick = (int64_t)t * a.K;
+  if (c < a.chunks && a.row_bytes >= 16) {
+    const int at = min(c * 16, a.row_bytes - 16);
+    uint4 v;
+    __builtin_memcpy(&v, a.x + t * a.x_pitch + at, 16);
+    for (int i = 0; i < a.K; ++i) {
+      const int slot = a.inv[pick + i];
+      if ((unsigned)slot < (unsigned)a.slots) __builtin_memcpy(a.rows + slot * a.row_pitch + at, &v, 16);
+    }
+    return;
+  }
   const bool scale = c >= a.chunks;
-  const int at = (scale ? c - a.chunks : c) * 16;
-  const int bytes = scale ? a.scale_bytes : a.row_bytes;
+  const int at = (scale ? c - a.chunks : c) * 16, bytes = scale ? a.scale_bytes : a.row_bytes;
   if (at >= bytes) return;
-  const uint8_t* src = scale ? a.x_scale + (int64_t)t * bytes : a.x + t * a.x_pitch;
-  const uint4 v = load_bytes16(src + at, bytes - at);
+  const int64_t x_pitch = scale ? bytes : a.x_pitch, pitch = scale ? bytes : a.row_pitch;
+  const uint8_t* from = (scale ? a.x_scale : a.x) + t * x_pitch + at;
+  uint8_t* to = (scale ? a.row_scale : a.rows) + at;
   for (int i = 0; i < a.K; ++i) {
-    const int slot = a.inv[(int64_t)t * a.K + i];
+    const int slot = a.inv[pick + i];
     if ((unsigned)slot >= (unsigned)a.slots) continue;
-    uint8_t* dst = scale ? a.row_scale + (int64_t)slot * bytes : a.rows + slot * a.row_pitch;
-    store_bytes16(dst + at, bytes - at, v);
+    if (bytes - at >= 16) __builtin_memcpy(to + slot * pitch, from, 16);
+    else if (bytes - at == 4) __builtin_memcpy(to + slot * pitch, from, 4);
+    else copy_bytes(to + slot * pitch, from, bytes - at);
   }
 }
 
 // Rows from fp32 to bf16 or back.
-template <int DT, bool LONG>
-__global__ void __launch_bounds__(kBlock) dispatch_cast_kernel(DispatchArgs a, TokenMap m) {
-  int t, c;
-  locate<LONG>(m, t, c);
-  c *= kUnit;
-  const int n = a.cols - c;
-  if (t >= a.T || n <= 0) return;
+template <int DT, bool LONG, bool TAIL>
+__global__ void __launch_bounds__(kBlock) dispatch_cast_kernel(DispatchArgs a, RowMap m) {
+  int t, unit;
+  locate<LONG>(m, t, unit);
+  const Span<TAIL> p(unit, a.cols);
+  if (t >= a.T || p.n <= 0) return;
   Unit<DT> u;
   float v[kUnit];
-  load_unit(u, a.x.p, DT, (int64_t)t * a.x.ld + c, n);
+  load_unit<TAIL>(u, a.x.p, DT, (int64_t)t * a.x.ld + p.c, p.n);
   unit_floats(u, DT, v);
   for (int i = 0; i < a.K; ++i) {
     const int slot = a.inv[(int64_t)t * a.K + i];
     if ((unsigned)slot >= (unsigned)a.slots) continue;
-    store_unit(a.rows.p, DT == MOE_DT_BF16 ? MOE_DT_F32 : MOE_DT_BF16, (int64_t)slot * a.rows.ld + c, n, v);
+    store_unit<TAIL>(a.rows.p, DT == MOE_DT_BF16 ? MOE_DT_F32 : MOE_DT_BF16, (int64_t)slot * a.rows.ld + p.c, p.n, v);
   }
 }
 
-template <int DT, bool LONG>
-__global__ void __launch_bounds__(kBlock) collect_kernel(CollectArgs a, TokenMap m) {
-  int t, c;
-  locate<LONG>(m, t, c);
-  c *= kUnit;
-  const int n = a.cols - c;
-  if (t >= a.T || n <= 0) return;
-  float y[kUnit] = {};
-  for (int i = 0; i < a.K; ++i) {
-    const int slot = a.inv[(int64_t)t * a.K + i];
-    if ((unsigned)slot >= (unsigned)a.slots) continue;
-    const float w = a.w ? a.w[(int64_t)t * a.K + i] : 1.0f;
-    Unit<DT> u;
-    float v[kUnit];
-    load_unit(u, a.rows.p, DT, (int64_t)slot * a.rows.ld + c, n);
-    unit_floats(u, DT, v);
+// Slots of picks [i, i + N) of a token, -1 for those that take no part.
+template <int N>
+__device__ __forceinline__ void slots_of(const int32_t* inv, int64_t pick, int n, int slots, int (&s)[N]) {
 #pragma unroll
-    for (int j = 0; j < kUnit; ++j) y[j] = fmaf(w, v[j], y[j]);
+  for (int j = 0; j < N; ++j) s[j] = j < n ? inv[pick + j] : -1;
+#pragma unroll
+  for (int j = 0; j < N; ++j) s[j] = (unsigned)s[j] < (unsigned)slots ? s[j] : -1;
+}
+
+template <int DT, bool LONG, bool TAIL>
+__global__ void __launch_bounds__(kBlock) collect_kernel(CollectArgs a, RowMap m) {
+  constexpr int N = 8;          // rows in flight
+  int t, unit;
+  locate<LONG>(m, t, unit);
+  const Span<TAIL> p(unit, a.cols);
+  if (t >= a.T || p.n <= 0) return;
+  float y[kUnit] = {};
+  for (int i = 0; i < a.K; i += N) {
+    const int64_t pick = (int64_t)t * a.K + i;
+    int slot[N];
+    slots_of(a.inv, pick, a.K - i, a.slots, slot);
+    Unit<DT> u[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (slot[j] >= 0) load_unit<TAIL>(u[j], a.rows.p, DT, (int64_t)slot[j] * a.rows.ld + p.c, p.n);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (slot[j] < 0) continue;
+      const float w = a.w ? a.w[pick + j] : 1.0f;
+      float v[kUnit];
+      unit_floats(u[j], DT, v);
+#pragma unroll
+      for (int l = 0; l < kUnit; ++l) y[l] = fmaf(w, v[l], y[l]);
+    }
   }
   if (a.add.p) {
     Unit<kAnyDtype> u;
     float v[kUnit];
-    load_unit(u, a.add.p, a.add.dtype, (int64_t)t * a.add.ld + c, n);
+    load_unit<TAIL>(u, a.add.p, a.add.dtype, (int64_t)t * a.add.ld + p.c, p.n);
     unit_floats(u, a.add.dtype, v);
 #pragma unroll
     for (int j = 0; j < kUnit; ++j) y[j] += v[j];
   }
-  store_unit(a.y.p, a.y.dtype, (int64_t)t * a.y.ld + c, n, y);
+  store_unit<TAIL>(a.y.p, a.y.dtype, (int64_t)t * a.y.ld + p.c, p.n, y);
 }
 
-// One token a workgroup (G == 256) or a wave: its rows one after the other.
-template <int DT, int G>
-__global__ void __launch_bounds__(kBlock) collect_grad_kernel(CollectGradArgs a) {
-  __shared__ float lds[kMaxK][kBlock / kWave];
-  const int lane = threadIdx.x % G;
-  const int t = blockIdx.x * (kBlock / G) + __builtin_amdgcn_readfirstlane(threadIdx.x / G);
+// A token's picks [i, i + span) by G lanes that walk along its row (G == 0: by the
+// whole workgroup), four picks at a time.
+constexpr int kPicks = 4;
+template <int DT, int G, bool TAIL>
+__global__ void __launch_bounds__(kBlock) collect_grad_kernel(CollectGradArgs a, int span) {
+  __shared__ float lds[G ? 1 : kBlock / kWave][kPicks];
+  const int lanes = G ? G : blockDim.x;
+  const int lane = G ? threadIdx.x % (G ? G : 1) : threadIdx.x;
+  const int spans = (a.K + span - 1) / span;
+  unsigned at = block_number(a.in_order);
+  if constexpr (G == kWave) at = at * (kBlock / G) + __builtin_amdgcn_readfirstlane(threadIdx.x / G);
+  else if constexpr (G != 0) at = at * (kBlock / G) + threadIdx.x / G;
+  const int t = (int)(at / (unsigned)spans), begin = (int)(at - (unsigned)t * spans) * span;
   if (t >= a.T) return;
-  for (int i = 0; i < a.K; ++i) {
-    const int slot = a.inv[(int64_t)t * a.K + i];
-    const bool on = (unsigned)slot < (unsigned)a.slots;
-    const float w = a.w ? a.w[(int64_t)t * a.K + i] : 1.0f;
-    float dot = 0.0f;
-    if (on) {
-      for (int c = lane * kUnit; c < a.cols; c += G * kUnit) {
-        const int n = a.cols - c;
-        Unit<kAnyDtype> d;
-        Unit<DT> r;
-        float dy[kUnit], v[kUnit];
-        load_unit(d, a.dy.p, a.dy.dtype, (int64_t)t * a.dy.ld + c, n);
-        unit_floats(d, a.dy.dtype, dy);
-        if (a.dw) {
-          load_unit(r, a.rows.p, DT, (int64_t)slot * a.rows.ld + c, n);
-          unit_floats(r, DT, v);
+  const int end = min(begin + span, a.K), units = (a.cols + kUnit - 1) / kUnit;
+  for (int i = begin; i < end; i += kPicks) {
+    const int64_t pick = (int64_t)t * a.K + i;
+    int slot[kPicks];
+    float w[kPicks], dot[kPicks];
+    slots_of(a.inv, pick, end - i, a.slots, slot);
 #pragma unroll
-          for (int j = 0; j < kUnit; ++j) dot = fmaf(dy[j], v[j], dot);
+    for (int j = 0; j < kPicks; ++j) {
+      w[j] = a.w && i + j < end ? a.w[pick + j] : 1.0f;
+      dot[j] = 0.0f;
+    }
+    for (int unit = lane; unit < units; unit += lanes) {
+      const Span<TAIL> p(unit, a.cols);
+      Unit<kAnyDtype> d;
+      Unit<DT> r[kPicks];
+      load_unit<TAIL>(d, a.dy.p, a.dy.dtype, (int64_t)t * a.dy.ld + p.c, p.n);
+      if (a.dw) {
+#pragma unroll
+        for (int j = 0; j < kPicks; ++j)
+          if (slot[j] >= 0) load_unit<TAIL>(r[j], a.rows.p, DT, (int64_t)slot[j] * a.rows.ld + p.c, p.n);
+      }
+      float dy[kUnit], v[kUnit];
+      unit_floats(d, a.dy.dtype, dy);
+#pragma unroll
+      for (int j = 0; j < kPicks; ++j) {
+        __builtin_amdgcn_sched_barrier(0);   // one pick after the other, for fewer registers
+        if (slot[j] < 0) continue;
+        if (a.dw) {
+          unit_floats(r[j], DT, v);
+          if (p.skip == 0) {
+#pragma unroll
+            for (int l = 0; l < kUnit; ++l) dot[j] = fmaf(dy[l], v[l], dot[j]);
+          } else {
+#pragma unroll
+            for (int l = 0; l < kUnit; ++l) dot[j] = l >= p.skip ? fmaf(dy[l], v[l], dot[j]) : dot[j];
+          }
         }
         if (a.drows.p) {
 #pragma unroll
-          for (int j = 0; j < kUnit; ++j) v[j] = w * dy[j];
-          store_unit(a.drows.p, DT, (int64_t)slot * a.drows.ld + c, n, v);
+          for (int l = 0; l < kUnit; ++l) v[l] = w[j] * dy[l];
+          store_unit<TAIL>(a.drows.p, DT, (int64_t)slot[j] * a.drows.ld + p.c, p.n, v);
         }
       }
     }
-    if (a.dw) {
-      dot = wave_sum(dot);
-      if (G == kWave) {
-        if (lane == 0) a.dw[(int64_t)t * a.K + i] = dot;
+    if (!a.dw) continue;
+#pragma unroll
+    for (int j = 0; j < kPicks; ++j) {
+      dot[j] = lanes_reduce<(G ? G : kWave)>(dot[j], [](float x, float y) { return x + y; });
+      if constexpr (G != 0) {
+        if (lane == 0 && i + j < end) a.dw[pick + j] = dot[j];
       } else if ((threadIdx.x & 63) == 0) {
-        lds[i][threadIdx.x >> 6] = dot;
+        lds[threadIdx.x >> 6][j] = dot[j];
       }
     }
+    if constexpr (G == 0) {
+      __syncthreads();
+      if (lane < kPicks && i + lane < end) {
+        float sum = lds[0][lane];
+        for (int v = 1; v < lanes / kWave; ++v) sum += lds[v][lane];
+        a.dw[pick + lane] = sum;
+      }
+      __syncthreads();
+    }
   }
-  if (G > kWave && a.dw) {
-    __syncthreads();
-    if (lane < a.K) a.dw[(int64_t)t * a.K + lane] = (lds[lane][0] + lds[lane][1]) + (lds[lane][2] + lds[lane][3]);
-  }
-}
-
-template <class F>
-hipError_t by_length(const TokenMap& map, int T, F&& f) {
-  return by_tokens(map, T, [&](unsigned blocks, const TokenMap& m) {
-    if (m.bits < 0) f(std::true_type{}, dim3(blocks), dim3(m.threads), m);
-    else f(std::false_type{}, dim3(blocks), dim3(m.threads), m);
-  });
 }
 
 }  // namespace
 
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
   if (a.x.dtype != a.rows.dtype) {
-    return by_length(token_map((a.cols + kUnit - 1) / kUnit), a.T, [&](auto L, dim3 grid, dim3 block, const TokenMap& m) {
-      constexpr bool l = decltype(L)::value;
-      if (a.x.dtype == MOE_DT_F32) hipLaunchKernelGGL((dispatch_cast_kernel<MOE_DT_F32, l>), grid, block, 0, s, a, m);
-      else hipLaunchKernelGGL((dispatch_cast_kernel<MOE_DT_BF16, l>), grid, block, 0, s, a, m);
+    return by_rows(row_map((a.cols + kUnit - 1) / kUnit, ragged_lines(a.rows.p, a.rows.ld * element(a.rows.dtype))), a.T,
+                   a.cols < kUnit, [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
+      constexpr bool l = decltype(L)::value, t = decltype(T)::value;
+      if (a.x.dtype == MOE_DT_F32) hipLaunchKernelGGL((dispatch_cast_kernel<MOE_DT_F32, l, t>), grid, block, 0, s, a, m);
+      else hipLaunchKernelGGL((dispatch_cast_kernel<MOE_DT_BF16, l, t>), grid, block, 0, s, a, m);
     });
   }
   CopyArgs c{};
@@ -251,29 +243,51 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
   c.T = a.T;
   c.K = a.K;
   c.slots = a.slots;
-  return by_length(token_map(c.chunks + (c.scale_bytes + 15) / 16), a.T, [&](auto L, dim3 grid, dim3 block, const TokenMap& m) {
+  return by_rows(row_map(c.chunks + (c.scale_bytes + 15) / 16, ragged_lines(c.rows, c.row_pitch)), a.T, false,
+                 [&](auto L, auto, dim3 grid, dim3 block, const RowMap& m) {
     hipLaunchKernelGGL((dispatch_copy_kernel<decltype(L)::value>), grid, block, 0, s, c, m);
   });
 }
 
 hipError_t launch_collect(const CollectArgs& a, hipStream_t s) {
-  return by_length(token_map((a.cols + kUnit - 1) / kUnit), a.T, [&](auto L, dim3 grid, dim3 block, const TokenMap& m) {
-    constexpr bool l = decltype(L)::value;
-    if (a.rows.dtype == MOE_DT_F32) hipLaunchKernelGGL((collect_kernel<MOE_DT_F32, l>), grid, block, 0, s, a, m);
-    else hipLaunchKernelGGL((collect_kernel<MOE_DT_BF16, l>), grid, block, 0, s, a, m);
+  const bool tail = a.cols < kUnit || (a.y.p == a.add.p && a.cols % kUnit != 0);
+  return by_rows(row_map((a.cols + kUnit - 1) / kUnit, ragged_lines(a.y.p, a.y.ld * element(a.y.dtype))), a.T, tail,
+                 [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
+    constexpr bool l = decltype(L)::value, t = decltype(T)::value;
+    if (a.rows.dtype == MOE_DT_F32) hipLaunchKernelGGL((collect_kernel<MOE_DT_F32, l, t>), grid, block, 0, s, a, m);
+    else hipLaunchKernelGGL((collect_kernel<MOE_DT_BF16, l, t>), grid, block, 0, s, a, m);
   });
 }
 
-hipError_t launch_collect_grad(const CollectGradArgs& a, hipStream_t s) {
-  auto launch = [&](auto D) {
-    constexpr int d = decltype(D)::value;
-    if (a.cols <= 1024)
-      hipLaunchKernelGGL((collect_grad_kernel<d, kWave>), dim3((a.T + 3) / 4), dim3(kBlock), 0, s, a);
-    else
-      hipLaunchKernelGGL((collect_grad_kernel<d, kBlock>), dim3(a.T), dim3(kBlock), 0, s, a);
+hipError_t launch_collect_grad(const CollectGradArgs& args, hipStream_t s) {
+  CollectGradArgs a = args;
+  a.in_order = a.drows.p && ragged_lines(a.drows.p, a.drows.ld * element(a.drows.dtype));
+  using std::integral_constant;
+  const int chunks = (a.cols + kUnit - 1) / kUnit;
+  auto launch = [&](auto D, auto G, auto T) {
+    constexpr int g = decltype(G)::value;
+    int threads = kBlock, per = g ? kBlock / (g ? g : 1) : 1;
+    if constexpr (g == 0) threads = row_map(chunks, false).threads;
+    // few tokens: a workgroup for each pick
+    const int span = (int64_t)a.T * (g ? g : threads) >= kGradFill ? a.K : 1;
+    const int64_t groups = (int64_t)a.T * ((a.K + span - 1) / span);
+    hipLaunchKernelGGL((collect_grad_kernel<decltype(D)::value, g, decltype(T)::value>), dim3((unsigned)((groups + per - 1) / per)),
+                       dim3(threads), 0, s, a, span);
   };
-  if (a.rows.dtype == MOE_DT_F32) launch(std::integral_constant<int, MOE_DT_F32>{});
-  else launch(std::integral_constant<int, MOE_DT_BF16>{});
+  auto by_lanes = [&](auto D) {
+    // over the rows themselves a row's last lane must not read what the lane before it wrote
+    const bool tail = a.cols < kUnit || (a.rows.p == a.drows.p && a.cols % kUnit != 0);
+    auto lanes = [&](auto T) {
+      if (chunks <= 8) launch(D, integral_constant<int, 8>{}, T);
+      else if (chunks <= 16) launch(D, integral_constant<int, 16>{}, T);
+      else if (chunks <= 64) launch(D, integral_constant<int, 64>{}, T);
+      else launch(D, integral_constant<int, 0>{}, T);
+    };
+    if (tail) lanes(std::true_type{});
+    else lanes(std::false_type{});
+  };
+  if (a.rows.dtype == MOE_DT_F32) by_lanes(integral_constant<int, MOE_DT_F32>{});
+  else by_lanes(integral_constant<int, MOE_DT_BF16>{});
   return hipGetLastError();
 }
 

@@ -11,28 +11,43 @@
 namespace qmoe {
 namespace {
 
-constexpr int kBlock = 256;
-constexpr int kWide = 1024;      // lanes for rows past kBlock * 4 units
+// Lanes of a workgroup whose rows take G lanes each, and its rows.
+constexpr int block_of(int g) { return g > 256 ? g : 256; }
+// Lanes for rows that are read again; the gradient holds dweight's sums in up to 128
+// registers of each.
+constexpr int kWide = 1024, kGradWide = 512;
 
-// What is done with eight values of y.
-template <int G>
-__device__ __forceinline__ void put_y(const NormArgs& a, int row, int c, const float (&v)[kUnit]) {
-  const int n = a.cols - c;
-  if (a.y.p && n > 0) store_unit(a.y.p, a.y.dtype, (int64_t)row * a.y.ld + c, n, v);
-}
-
-// MXFP4 of a unit; all lanes of a quad take part, also those past the row's end.
-__device__ __forceinline__ void put_mxfp4(const NormArgs& a, int row, int c, const float (&v)[kUnit]) {
+// MXFP4 of a unit's own values; all lanes of a quad take part, also those past the
+// row's end.
+__device__ __forceinline__ void put_mxfp4(const NormArgs& a, int64_t row, int unit, int skip, float (&v)[kUnit]) {
   uint32_t byte;
+  own_first(v, skip);
   const uint32_t q = mxfp4_codes(v, byte);
   const int nb = (a.cols + kMxBlock - 1) / kMxBlock;
-  if (c < nb * kMxBlock) {
-    static_cast<uint32_t*>(a.q)[(int64_t)row * nb * 4 + c / kUnit] = q;
-    if (c % kMxBlock == 0) static_cast<uint8_t*>(a.q_scale)[(int64_t)row * nb + c / kMxBlock] = (uint8_t)byte;
+  if (unit < nb * 4) {
+    static_cast<uint32_t*>(a.q)[row * nb * 4 + unit] = q;
+    if (unit % 4 == 0) static_cast<uint8_t*>(a.q_scale)[row * nb + unit / 4] = (uint8_t)byte;
   }
 }
 
-// h of a unit (rounded to the stream's type), 0 past the row's end.
+__device__ __forceinline__ float inverse_rms(double sum, int cols, float eps) {
+  return (float)(1.0 / sqrt(sum / cols + (double)eps));
+}
+
+// Sum of squares of a unit's own values.
+__device__ __forceinline__ double squares(const float (&h)[kUnit], int skip) {
+  double sum = 0;
+  if (skip == 0) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) sum += (double)h[i] * h[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) sum += i >= skip ? (double)h[i] * h[i] : 0.0;
+  }
+  return sum;
+}
+
+// h of a unit, rounded to the stream's type, from x and the residual.
 template <int DT>
 __device__ __forceinline__ void add_residual(const NormArgs& a, const Unit<DT>& x, const Unit<DT>& r, float (&h)[kUnit]) {
   unit_floats(x, a.x.dtype, h);
@@ -45,112 +60,131 @@ __device__ __forceinline__ void add_residual(const NormArgs& a, const Unit<DT>& 
   }
 }
 
-__device__ __forceinline__ float inverse_rms(double sum, int cols, float eps) {
-  return (float)(1.0 / sqrt(sum / cols + (double)eps));
+// h of a unit between the sum and its use: bf16 where it is that, else fp32.
+template <int DT>
+__device__ __forceinline__ void hold(Unit<DT>& u, const float (&h)[kUnit]) {
+  if constexpr (DT == MOE_DT_BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u.w[i] = pack_bf16(h[2 * i], h[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) u.w[i] = __float_as_uint(h[i]);
+  }
 }
 
-template <int DT, int G, int U>
-__global__ void __launch_bounds__(kBlock) rmsnorm_kernel(NormArgs a) {
-  __shared__ double sums[kBlock / kWave];
-  __shared__ uint32_t tops[kBlock / kWave];
+// The kernels of bf16 matrices have bf16 weights too.
+template <int DT>
+constexpr int weight_dtype() { return DT == MOE_DT_BF16 ? MOE_DT_BF16 : kAnyDtype; }
+
+// Nothing is stored before the whole row is read: h may be the residual itself, and
+// the last lanes of a row read values of the ones before them.
+template <int DT, int G, int U, bool TAIL>
+__global__ void __launch_bounds__(block_of(G)) rmsnorm_kernel(NormArgs a) {
+  constexpr int kRows = block_of(G) / G, kHeld = DT == MOE_DT_BF16 ? MOE_DT_BF16 : MOE_DT_F32;
+  __shared__ double sums[block_of(G) / kWave];
+  __shared__ uint32_t tops[block_of(G) / kWave];
   const int lane = threadIdx.x % G;
-  const int row = blockIdx.x * (kBlock / G) + __builtin_amdgcn_readfirstlane(threadIdx.x / G);
+  int64_t row = block_number(a.in_order) * kRows;
+  if constexpr (G < kWave) row += threadIdx.x / G;
+  else if constexpr (G == kWave) row += __builtin_amdgcn_readfirstlane(threadIdx.x / G);
   if (row >= a.rows) return;
   Unit<DT> x[U], r[U];
+  Unit<weight_dtype<DT>()> w[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int c = (u * G + lane) * kUnit;
-    load_unit(x[u], a.x.p, a.x.dtype, (int64_t)row * a.x.ld + c, a.cols - c);
-    if (a.res.p) load_unit(r[u], a.res.p, a.res.dtype, (int64_t)row * a.res.ld + c, a.cols - c);
+    const Span<TAIL> p(u * G + lane, a.cols);
+    load_unit<TAIL>(x[u], a.x.p, a.x.dtype, row * a.x.ld + p.c, p.n);
+    if (a.res.p) load_unit<TAIL>(r[u], a.res.p, a.res.dtype, row * a.res.ld + p.c, p.n);
+    load_unit<TAIL>(w[u], a.w, a.w_dtype, p.c, p.n);
   }
-  float h[U][kUnit];
   double sum = 0;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int c = (u * G + lane) * kUnit, n = a.cols - c;
-    add_residual(a, x[u], r[u], h[u]);
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) sum += (double)h[u][i] * h[u][i];
-    if (a.h.p && n > 0) store_unit(a.h.p, a.h.dtype, (int64_t)row * a.h.ld + c, n, h[u]);
+    float h[kUnit];
+    add_residual(a, x[u], r[u], h);
+    sum += squares(h, Span<TAIL>(u * G + lane, a.cols).skip);
+    hold(x[u], h);
   }
-  if (!a.y.p && !a.q) return;
   const float m = inverse_rms(group_sum<G>(sum, sums), a.cols, a.eps);
   uint32_t top = 0;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int c = (u * G + lane) * kUnit;
-    Unit<kAnyDtype> w;
-    float wv[kUnit];
-    load_unit(w, a.w, a.w_dtype, c, a.cols - c);
-    unit_floats(w, a.w_dtype, wv);
+    const Span<TAIL> p(u * G + lane, a.cols);
+    float h[kUnit], v[kUnit];
+    forget_values(x[u]);       // else the fp32 values stay in registers all along
+    unit_floats(x[u], kHeld, h);
+    if (a.h.p && p.n > 0) store_unit<TAIL>(a.h.p, a.h.dtype, row * a.h.ld + p.c, p.n, h);
+    unit_floats(w[u], a.w_dtype, v);
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) h[u][i] = c + i < a.cols ? h[u][i] * m * wv[i] : 0.0f;
-    put_y<G>(a, row, c, h[u]);
-    if (a.q && a.q_dtype == MOE_DT_MXFP4) put_mxfp4(a, row, c, h[u]);
-    top = max(top, top_bits(h[u]));
+    for (int i = 0; i < kUnit; ++i) v[i] = h[i] * m * v[i];
+    if (a.y.p && p.n > 0) store_unit<TAIL>(a.y.p, a.y.dtype, row * a.y.ld + p.c, p.n, v);
+    if (a.q && a.q_dtype == MOE_DT_MXFP4) put_mxfp4(a, row, u * G + lane, p.skip, v);
+    if (a.q && a.q_dtype == MOE_DT_E4M3) top = max(top, top_bits(v));
   }
   if (a.q && a.q_dtype == MOE_DT_E4M3) {
     const float scale = e4m3_scale(group_max<G>(top, tops));
-    const float inv = scale == scale ? 1.0f / scale : 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = (u * G + lane) * kUnit, n = a.cols - c;
-      if (n > 0) store_bytes(static_cast<uint8_t*>(a.q) + (int64_t)row * a.cols + c, n, e4m3_codes(h[u], inv));
+      const Span<TAIL> p(u * G + lane, a.cols);
+      float h[kUnit], v[kUnit];
+      unit_floats(x[u], kHeld, h);
+      unit_floats(w[u], a.w_dtype, v);
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) v[i] = h[i] * m * v[i];
+      if (p.n > 0) store_bytes<TAIL>(static_cast<uint8_t*>(a.q) + row * a.cols + p.c, p.n, e4m3_codes(v, scale));
     }
     if (lane == 0) static_cast<float*>(a.q_scale)[row] = scale;
   }
 }
 
-// Rows of any length, a workgroup each, read again for each pass over them.  h,
+// Rows past the registers of a workgroup, read again for each pass over them.  h,
 // which may be the residual itself, is written with the last reading.
 __global__ void __launch_bounds__(kWide) rmsnorm_wide_kernel(NormArgs a) {
   __shared__ double sums[kWide / kWave];
   __shared__ uint32_t tops[kWide / kWave];
-  const int row = blockIdx.x;
-  const int span = (a.cols + kMxBlock - 1) / kMxBlock * kMxBlock;     // whole quads of lanes
+  const int64_t row = block_number(a.in_order);
+  const int units = (a.cols + kMxBlock - 1) / kMxBlock * 4;     // whole quads of lanes
   auto read = [&](int c, float (&h)[kUnit]) {
     Unit<kAnyDtype> x, r;
-    load_unit(x, a.x.p, a.x.dtype, (int64_t)row * a.x.ld + c, a.cols - c);
-    if (a.res.p) load_unit(r, a.res.p, a.res.dtype, (int64_t)row * a.res.ld + c, a.cols - c);
+    load_unit<true>(x, a.x.p, a.x.dtype, row * a.x.ld + c, a.cols - c);
+    if (a.res.p) load_unit<true>(r, a.res.p, a.res.dtype, row * a.res.ld + c, a.cols - c);
     add_residual(a, x, r, h);
   };
   auto normed = [&](int c, float m, float (&h)[kUnit]) {
     Unit<kAnyDtype> w;
     float wv[kUnit];
-    load_unit(w, a.w, a.w_dtype, c, a.cols - c);
+    load_unit<true>(w, a.w, a.w_dtype, c, a.cols - c);
     unit_floats(w, a.w_dtype, wv);
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) h[i] = c + i < a.cols ? h[i] * m * wv[i] : 0.0f;
+    for (int i = 0; i < kUnit; ++i) h[i] = h[i] * m * wv[i];
   };
   double sum = 0;
   float h[kUnit];
-  for (int c = threadIdx.x * kUnit; c < span; c += kWide * kUnit) {
-    read(c, h);
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) sum += (double)h[i] * h[i];
+  for (int u = threadIdx.x; u < units; u += kWide) {
+    read(u * kUnit, h);
+    sum += squares(h, 0);
   }
   const float m = inverse_rms(group_sum<kWide>(sum, sums), a.cols, a.eps);
-  float scale = 0.0f, inv = 0.0f;
+  float scale = 0.0f;
   if (a.q && a.q_dtype == MOE_DT_E4M3) {
     uint32_t top = 0;
-    for (int c = threadIdx.x * kUnit; c < span; c += kWide * kUnit) {
-      read(c, h);
-      normed(c, m, h);
+    for (int u = threadIdx.x; u < units; u += kWide) {
+      read(u * kUnit, h);
+      normed(u * kUnit, m, h);
       top = max(top, top_bits(h));
     }
     scale = e4m3_scale(group_max<kWide>(top, tops));
-    inv = scale == scale ? 1.0f / scale : 0.0f;
     if (threadIdx.x == 0) static_cast<float*>(a.q_scale)[row] = scale;
   }
-  for (int c = threadIdx.x * kUnit; c < span; c += kWide * kUnit) {
-    const int n = a.cols - c;
+  for (int u = threadIdx.x; u < units; u += kWide) {
+    const int c = u * kUnit, n = a.cols - c;
     read(c, h);
-    if (a.h.p && n > 0) store_unit(a.h.p, a.h.dtype, (int64_t)row * a.h.ld + c, n, h);
+    if (a.h.p && n > 0) store_unit<true>(a.h.p, a.h.dtype, row * a.h.ld + c, n, h);
     normed(c, m, h);
-    put_y<kWide>(a, row, c, h);
+    if (a.y.p && n > 0) store_unit<true>(a.y.p, a.y.dtype, row * a.y.ld + c, n, h);
     if (!a.q) continue;
-    if (a.q_dtype == MOE_DT_MXFP4) put_mxfp4(a, row, c, h);
-    else if (n > 0) store_bytes(static_cast<uint8_t*>(a.q) + (int64_t)row * a.cols + c, n, e4m3_codes(h, inv));
+    if (a.q_dtype == MOE_DT_MXFP4) put_mxfp4(a, row, u, 0, h);
+    else if (n > 0) store_bytes<true>(static_cast<uint8_t*>(a.q) + row * a.cols + c, n, e4m3_codes(h, scale));
   }
 }
 
@@ -166,38 +200,56 @@ __device__ __forceinline__ void row_factors(RowSums s, int cols, float eps, floa
   k = (float)(s.product / cols * r * r);
 }
 
-template <int DT, int G, int U>
-__global__ void __launch_bounds__(kBlock) rmsnorm_grad_kernel(NormGradArgs a) {
-  constexpr int kRows = kBlock / G;
+// Sum of dy * w * h over a unit's own values.
+__device__ __forceinline__ double product(const float (&dy)[kUnit], const float (&w)[kUnit], const float (&h)[kUnit], int skip) {
+  double sum = 0;
+  if (skip == 0) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) sum += (double)(dy[i] * w[i]) * h[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) sum += i >= skip ? (double)(dy[i] * w[i]) * h[i] : 0.0;
+  }
+  return sum;
+}
+
+// Workgroups take rows in turn and hold dw's sums over theirs.  As in the norm,
+// nothing of a row is stored before all of it is read.
+template <int DT, int G, int U, bool TAIL>
+__global__ void __launch_bounds__(block_of(G)) rmsnorm_grad_kernel(NormGradArgs a) {
+  constexpr int kBlock = block_of(G), kRows = kBlock / G;
   __shared__ double lds[2][2][kBlock / kWave];
   const int lane = threadIdx.x % G;
-  const int first = blockIdx.x * kRows + __builtin_amdgcn_readfirstlane(threadIdx.x / G);
+  int64_t row = block_number(a.in_order) * kRows;
+  if constexpr (G < kWave) row += threadIdx.x / G;
+  else if constexpr (G == kWave) row += __builtin_amdgcn_readfirstlane(threadIdx.x / G);
+  Unit<weight_dtype<DT>()> wr[U];
   float acc[U][kUnit] = {};
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Span<TAIL> p(u * G + lane, a.cols);
+    load_unit<TAIL>(wr[u], a.w, a.w_dtype, p.c, p.n);
+  }
   int turn = 0;
-  for (int row = first; row < a.rows; row += gridDim.x * kRows, turn ^= 1) {
+  for (; row < a.rows; row += (int64_t)gridDim.x * kRows, turn ^= 1) {
     Unit<DT> hr[U], yr[U], dr[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = (u * G + lane) * kUnit, n = a.cols - c;
-      load_unit(hr[u], a.h.p, a.h.dtype, (int64_t)row * a.h.ld + c, n);
-      load_unit(yr[u], a.dy.p, a.dy.dtype, (int64_t)row * a.dy.ld + c, n);
-      if (a.dh.p) load_unit(dr[u], a.dh.p, a.dh.dtype, (int64_t)row * a.dh.ld + c, n);
+      const Span<TAIL> p(u * G + lane, a.cols);
+      load_unit<TAIL>(hr[u], a.h.p, a.h.dtype, row * a.h.ld + p.c, p.n);
+      load_unit<TAIL>(yr[u], a.dy.p, a.dy.dtype, row * a.dy.ld + p.c, p.n);
+      if (a.dh.p) load_unit<TAIL>(dr[u], a.dh.p, a.dh.dtype, row * a.dh.ld + p.c, p.n);
     }
     RowSums s{0, 0};
-    float h[U][kUnit], dy[U][kUnit], w[U][kUnit];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = (u * G + lane) * kUnit, n = a.cols - c;
-      Unit<kAnyDtype> wr;
-      load_unit(wr, a.w, a.w_dtype, c, n);
-      unit_floats(wr, a.w_dtype, w[u]);
-      unit_floats(hr[u], a.h.dtype, h[u]);
-      unit_floats(yr[u], a.dy.dtype, dy[u]);
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) {
-        s.squares += (double)h[u][i] * h[u][i];
-        s.product += (double)(dy[u][i] * w[u][i]) * h[u][i];
-      }
+      const int skip = Span<TAIL>(u * G + lane, a.cols).skip;
+      float w[kUnit], h[kUnit], dy[kUnit];
+      unit_floats(wr[u], a.w_dtype, w);
+      unit_floats(hr[u], a.h.dtype, h);
+      unit_floats(yr[u], a.dy.dtype, dy);
+      s.squares += squares(h, skip);
+      s.product += product(dy, w, h, skip);
     }
     s.squares = group_sum<G>(s.squares, lds[turn][0]);
     s.product = group_sum<G>(s.product, lds[turn][1]);
@@ -205,12 +257,18 @@ __global__ void __launch_bounds__(kBlock) rmsnorm_grad_kernel(NormGradArgs a) {
     row_factors(s, a.cols, a.eps, m, k);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = (u * G + lane) * kUnit, n = a.cols - c;
-      float dx[kUnit];
+      const Span<TAIL> p(u * G + lane, a.cols);
+      float dx[kUnit], w[kUnit], h[kUnit], dy[kUnit];
+      forget_values(wr[u]);      // else the fp32 values stay in registers all along
+      forget_values(hr[u]);
+      forget_values(yr[u]);
+      unit_floats(wr[u], a.w_dtype, w);
+      unit_floats(hr[u], a.h.dtype, h);
+      unit_floats(yr[u], a.dy.dtype, dy);
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) {
-        dx[i] = m * (dy[u][i] * w[u][i] - h[u][i] * k);
-        acc[u][i] += dy[u][i] * (h[u][i] * m);
+        dx[i] = m * (dy[i] * w[i] - h[i] * k);
+        acc[u][i] += dy[i] * (h[i] * m);
       }
       if (a.dh.p) {
         float d[kUnit];
@@ -218,55 +276,58 @@ __global__ void __launch_bounds__(kBlock) rmsnorm_grad_kernel(NormGradArgs a) {
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) dx[i] += d[i];
       }
-      if (n > 0) store_unit(a.dx.p, a.dx.dtype, (int64_t)row * a.dx.ld + c, n, dx);
+      if (p.n > 0) store_unit<TAIL>(a.dx.p, a.dx.dtype, row * a.dx.ld + p.c, p.n, dx);
     }
   }
   if (!a.dw) return;
   float* part = gridDim.x == 1 ? a.dw : a.part + (int64_t)blockIdx.x * a.cols;
-  if constexpr (kRows > 1) {       // the waves' sums, in order
-    __shared__ float waves[kRows][G * U * kUnit];
+  if constexpr (kRows > 1) {       // the sums of the workgroup's rows, in order
+    __shared__ float all[kRows][G * U * kUnit];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      const Span<TAIL> p(u * G + lane, a.cols);
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) waves[threadIdx.x / G][(u * G + lane) * kUnit + i] = acc[u][i];
+      for (int i = 0; i < kUnit; ++i)
+        if (p.n > 0) all[threadIdx.x / G][p.c + i] = acc[u][i];
+    }
     __syncthreads();
     for (int c = threadIdx.x; c < a.cols; c += kBlock) {
-      float v = waves[0][c];
-#pragma unroll
-      for (int i = 1; i < kRows; ++i) v += waves[i][c];
+      float v = all[0][c];
+#pragma unroll 8
+      for (int i = 1; i < kRows; ++i) v += all[i][c];
       part[c] = v;
     }
   } else {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = (u * G + lane) * kUnit;
-      if (c < a.cols) store_unit(part, MOE_DT_F32, c, a.cols - c, acc[u]);
+      const Span<TAIL> p(u * G + lane, a.cols);
+      if (p.n > 0) store_unit<TAIL>(part, MOE_DT_F32, p.c, p.n, acc[u]);
     }
   }
 }
 
-// Rows past kBlock * 4 units: read twice, dweight's sums in registers.
+// Longer rows: read twice, dweight's sums in registers.
 template <int U>
-__global__ void __launch_bounds__(kWide) rmsnorm_grad_wide_kernel(NormGradArgs a) {
-  __shared__ double lds[2][2][kWide / kWave];
+__global__ void __launch_bounds__(kGradWide) rmsnorm_grad_wide_kernel(NormGradArgs a) {
+  __shared__ double lds[2][2][kGradWide / kWave];
   float acc[U][kUnit] = {};
   int turn = 0;
-  for (int row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+  for (int64_t row = block_number(a.in_order); row < a.rows; row += gridDim.x, turn ^= 1) {
     auto read = [&](int c, float (&h)[kUnit], float (&dy)[kUnit], float (&g)[kUnit]) {
       Unit<kAnyDtype> v;
       const int n = a.cols - c;
-      load_unit(v, a.h.p, a.h.dtype, (int64_t)row * a.h.ld + c, n);
+      load_unit<true>(v, a.h.p, a.h.dtype, (int64_t)row * a.h.ld + c, n);
       unit_floats(v, a.h.dtype, h);
-      load_unit(v, a.dy.p, a.dy.dtype, (int64_t)row * a.dy.ld + c, n);
+      load_unit<true>(v, a.dy.p, a.dy.dtype, (int64_t)row * a.dy.ld + c, n);
       unit_floats(v, a.dy.dtype, dy);
-      load_unit(v, a.w, a.w_dtype, c, n);
+      load_unit<true>(v, a.w, a.w_dtype, c, n);
       unit_floats(v, a.w_dtype, g);
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) g[i] *= dy[i];
     };
     RowSums s{0, 0};
     float h[kUnit], dy[kUnit], g[kUnit];
-    for (int c = threadIdx.x * kUnit; c < a.cols; c += kWide * kUnit) {
+    for (int c = threadIdx.x * kUnit; c < a.cols; c += kGradWide * kUnit) {
       read(c, h, dy, g);
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) {
@@ -274,13 +335,13 @@ __global__ void __launch_bounds__(kWide) rmsnorm_grad_wide_kernel(NormGradArgs a
         s.product += (double)g[i] * h[i];
       }
     }
-    s.squares = group_sum<kWide>(s.squares, lds[turn][0]);
-    s.product = group_sum<kWide>(s.product, lds[turn][1]);
+    s.squares = group_sum<kGradWide>(s.squares, lds[turn][0]);
+    s.product = group_sum<kGradWide>(s.product, lds[turn][1]);
     float m, k;
     row_factors(s, a.cols, a.eps, m, k);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = (u * kWide + threadIdx.x) * kUnit, n = a.cols - c;
+      const int c = (u * kGradWide + threadIdx.x) * kUnit, n = a.cols - c;
       if (n <= 0) continue;
       read(c, h, dy, g);
       float dx[kUnit];
@@ -291,63 +352,95 @@ __global__ void __launch_bounds__(kWide) rmsnorm_grad_wide_kernel(NormGradArgs a
       }
       if (a.dh.p) {
         Unit<kAnyDtype> v;
-        load_unit(v, a.dh.p, a.dh.dtype, (int64_t)row * a.dh.ld + c, n);
+        load_unit<true>(v, a.dh.p, a.dh.dtype, (int64_t)row * a.dh.ld + c, n);
         unit_floats(v, a.dh.dtype, h);
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) dx[i] += h[i];
       }
-      store_unit(a.dx.p, a.dx.dtype, (int64_t)row * a.dx.ld + c, n, dx);
+      store_unit<true>(a.dx.p, a.dx.dtype, (int64_t)row * a.dx.ld + c, n, dx);
     }
   }
   if (!a.dw) return;
   float* part = gridDim.x == 1 ? a.dw : a.part + (int64_t)blockIdx.x * a.cols;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int c = (u * kWide + threadIdx.x) * kUnit;
-    if (c < a.cols) store_unit(part, MOE_DT_F32, c, a.cols - c, acc[u]);
+    const int c = (u * kGradWide + threadIdx.x) * kUnit;
+    if (c < a.cols) store_unit<true>(part, MOE_DT_F32, c, a.cols - c, acc[u]);
   }
 }
 
-// dw[c] = sum of the workgroups' parts: 64 columns a workgroup, a share of the
-// parts each wave, joined in order.
-__global__ void __launch_bounds__(kWide) rmsnorm_dw_kernel(const float* part, int parts, int cols, float* dw) {
-  __shared__ double lds[kWide / kWave][kWave];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * kWave + lane;
-  double v = 0;
-  if (c < cols) {
+// dw[c] = sum of the workgroups' parts: 32 columns a workgroup, eight lanes to a part,
+// the shares of the parts joined in order.
+constexpr int kDwCols = 32;
+__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* part, int parts, int cols, float* dw) {
+  constexpr int kShares = 1024 / 8, kGroups = 1024 / kDwCols;
+  __shared__ double lds[kShares][kDwCols];
+  const int lane = threadIdx.x % 8, share = threadIdx.x / 8;
+  const int c = blockIdx.x * kDwCols + lane * 4;
+  double v[4] = {};
 #pragma unroll 8
-    for (int p = wave; p < parts; p += kWide / kWave) v += part[(int64_t)p * cols + c];
+  for (int p = share; p < parts; p += kShares) {
+    float x[4] = {};
+    const float* at = part + (int64_t)p * cols + c;
+    if (c + 4 <= cols) {
+      __builtin_memcpy(x, at, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (c + i < cols) x[i] = at[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += x[i];
   }
-  lds[wave][lane] = v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) lds[share][lane * 4 + i] = v[i];
   __syncthreads();
-  if (wave == 0 && c < cols) {
-    for (int i = 1; i < kWide / kWave; ++i) v += lds[i][lane];
-    dw[c] = (float)v;
+  const int col = threadIdx.x % kDwCols, group = threadIdx.x / kDwCols;
+  double sum = 0;
+#pragma unroll
+  for (int i = 0; i < kShares / kGroups; ++i) sum += lds[group * (kShares / kGroups) + i][col];
+  __syncthreads();
+  lds[group][col] = sum;
+  __syncthreads();
+  if (group == 0 && blockIdx.x * kDwCols + col < cols) {
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) sum += lds[i][col];
+    dw[blockIdx.x * kDwCols + col] = (float)sum;
   }
 }
 
-__global__ void __launch_bounds__(kBlock) fill_zero_kernel(float* p, int n) {
-  const int i = blockIdx.x * kBlock + threadIdx.x;
+__global__ void __launch_bounds__(256) fill_zero_kernel(float* p, int n) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
   if (i < n) p[i] = 0.0f;
 }
 
 constexpr int kGradBlocks = 1024;
 
-// Calls f(dtype, lanes, units) as integral constants for rows of up to 8192
+// Calls f(dtype, lanes, units, tail) as integral constants for rows of up to MOST
 // columns, g() for longer ones.
-template <class F, class G>
-void by_shape(bool all_bf16, bool all_f32, int cols, F&& f, G&& g) {
+template <int MOST, class F, class H>
+void by_shape(bool all_bf16, bool all_f32, int cols, F&& f, H&& g) {
   using std::integral_constant;
   const int units = (cols + kUnit - 1) / kUnit;
   auto shape = [&](auto D) {
-    if (units <= 64) f(D, integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    else if (units <= 256) f(D, integral_constant<int, 256>{}, integral_constant<int, 1>{});
-    else if (units <= 512) f(D, integral_constant<int, 256>{}, integral_constant<int, 2>{});
-    else if (units <= 768) f(D, integral_constant<int, 256>{}, integral_constant<int, 3>{});
-    else f(D, integral_constant<int, 256>{}, integral_constant<int, 4>{});
+    auto at = [&](auto G, auto U) { f(D, G, U, std::false_type{}); };
+    if (cols < kUnit) f(D, integral_constant<int, 4>{}, integral_constant<int, 1>{}, std::true_type{});
+    else if (units <= 4) at(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+    else if (units <= 8) at(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+    else if (units <= 16) at(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+    else if (units <= 32) at(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+    else if (units <= 64) at(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else if (units <= 128) at(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else if (units <= 192) at(integral_constant<int, 64>{}, integral_constant<int, 3>{});
+    else if (units <= 256) at(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    else if (units <= 512) at(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    else if (units <= 768) at(integral_constant<int, 256>{}, integral_constant<int, 3>{});
+    else if (units <= 1024) at(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+    else if constexpr (MOST <= 16384) at(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+    else if (units <= 2048) at(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    else at(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
   };
-  if (units > 1024) g();
+  if (cols > MOST) g();
   else if (all_bf16) shape(integral_constant<int, MOE_DT_BF16>{});
   else if (all_f32) shape(integral_constant<int, MOE_DT_F32>{});
   else shape(integral_constant<int, kAnyDtype>{});
@@ -359,38 +452,50 @@ bool all_of(int dtype, std::initializer_list<const RowMat*> all) {
 
 }  // namespace
 
-hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s) {
-  by_shape(all_of(MOE_DT_BF16, {&a.x, &a.res}), all_of(MOE_DT_F32, {&a.x, &a.res}), a.cols,
-           [&](auto D, auto G, auto U) {
-             constexpr int g = decltype(G)::value, rows = kBlock / g;
-             hipLaunchKernelGGL((rmsnorm_kernel<decltype(D)::value, g, decltype(U)::value>),
-                                dim3((a.rows + rows - 1) / rows), dim3(kBlock), 0, s, a);
-           },
-           [&] { hipLaunchKernelGGL(rmsnorm_wide_kernel, dim3(a.rows), dim3(kWide), 0, s, a); });
+hipError_t launch_rmsnorm(const NormArgs& args, hipStream_t s) {
+  NormArgs a = args;
+  const RowMat& out = a.y.p ? a.y : a.h;
+  a.in_order = out.p && ragged_lines(out.p, out.ld * element(out.dtype));
+  by_shape<32768>(
+      a.w_dtype == MOE_DT_BF16 && all_of(MOE_DT_BF16, {&a.x, &a.res}), all_of(MOE_DT_F32, {&a.x, &a.res}), a.cols,
+      [&](auto D, auto G, auto U, auto T) {
+        constexpr int g = decltype(G)::value, rows = block_of(g) / g;
+        hipLaunchKernelGGL((rmsnorm_kernel<decltype(D)::value, g, decltype(U)::value, decltype(T)::value>),
+                           dim3((a.rows + rows - 1) / rows), dim3(block_of(g)), 0, s, a);
+      },
+      [&] { hipLaunchKernelGGL(rmsnorm_wide_kernel, dim3(a.rows), dim3(kWide), 0, s, a); });
   return hipGetLastError();
 }
 
 int norm_grad_most_blocks(int rows) { return std::min(std::max(rows, 1), kGradBlocks); }
 
-hipError_t launch_rmsnorm_grad(const NormGradArgs& a, hipStream_t s) {
+hipError_t launch_rmsnorm_grad(const NormGradArgs& args, hipStream_t s) {
+  NormGradArgs a = args;
+  a.in_order = ragged_lines(a.dx.p, a.dx.ld * element(a.dx.dtype));
   if (a.rows == 0) {
-    hipLaunchKernelGGL(fill_zero_kernel, dim3((a.cols + kBlock - 1) / kBlock), dim3(kBlock), 0, s, a.dw, a.cols);
+    hipLaunchKernelGGL(fill_zero_kernel, dim3((a.cols + 255) / 256), dim3(256), 0, s, a.dw, a.cols);
     return hipGetLastError();
   }
-  const int per = a.cols <= 64 * kUnit ? kBlock / 64 : 1;     // rows a workgroup takes at a time
-  const int blocks = std::min((a.rows + per - 1) / per, kGradBlocks);
-  by_shape(all_of(MOE_DT_BF16, {&a.h, &a.dy, &a.dh}), all_of(MOE_DT_F32, {&a.h, &a.dy, &a.dh}), a.cols,
-           [&](auto D, auto G, auto U) {
-             hipLaunchKernelGGL((rmsnorm_grad_kernel<decltype(D)::value, decltype(G)::value, decltype(U)::value>),
-                                dim3(blocks), dim3(kBlock), 0, s, a);
-           },
-           [&] {
-             if (a.cols <= 2 * kWide * kUnit) hipLaunchKernelGGL((rmsnorm_grad_wide_kernel<2>), dim3(blocks), dim3(kWide), 0, s, a);
-             else if (a.cols <= 4 * kWide * kUnit) hipLaunchKernelGGL((rmsnorm_grad_wide_kernel<4>), dim3(blocks), dim3(kWide), 0, s, a);
-             else hipLaunchKernelGGL((rmsnorm_grad_wide_kernel<8>), dim3(blocks), dim3(kWide), 0, s, a);
-           });
+  // workgroups of `per` rows at a time, each as many times as the others
+  int blocks = 0;
+  auto grid = [&](int per) {
+    const int steps = (a.rows + per - 1) / per;
+    const int turns = (steps + kGradBlocks - 1) / kGradBlocks;
+    return dim3(blocks = (steps + turns - 1) / turns);
+  };
+  by_shape<16384>(
+      a.w_dtype == MOE_DT_BF16 && all_of(MOE_DT_BF16, {&a.h, &a.dy, &a.dh}), all_of(MOE_DT_F32, {&a.h, &a.dy, &a.dh}), a.cols,
+      [&](auto D, auto G, auto U, auto T) {
+        constexpr int g = decltype(G)::value;
+        hipLaunchKernelGGL((rmsnorm_grad_kernel<decltype(D)::value, g, decltype(U)::value, decltype(T)::value>), grid(block_of(g) / g),
+                           dim3(block_of(g)), 0, s, a);
+      },
+      [&] {
+        if (a.cols <= 8 * kGradWide * kUnit) hipLaunchKernelGGL((rmsnorm_grad_wide_kernel<8>), grid(1), dim3(kGradWide), 0, s, a);
+        else hipLaunchKernelGGL((rmsnorm_grad_wide_kernel<16>), grid(1), dim3(kGradWide), 0, s, a);
+      });
   if (a.dw && blocks > 1)
-    hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((a.cols + kWave - 1) / kWave), dim3(kWide), 0, s, a.part, blocks, a.cols, a.dw);
+    hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((a.cols + kDwCols - 1) / kDwCols), dim3(1024), 0, s, a.part, blocks, a.cols, a.dw);
   return hipGetLastError();
 }
 

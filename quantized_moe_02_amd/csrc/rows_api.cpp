@@ -12,7 +12,6 @@ constexpr size_t kAlign = 256;
 
 bool plain_dtype(int32_t d) { return d == MOE_DT_F32 || d == MOE_DT_BF16; }
 bool coded_dtype(int32_t d) { return d == MOE_DT_E4M3 || d == MOE_DT_MXFP4; }
-size_t element(int32_t d) { return d == MOE_DT_F32 ? 4 : 2; }
 bool element_aligned(const void* p, int32_t d) { return aligned(p, element(d)); }
 
 // Limits of a matrix's size; columns before rows.

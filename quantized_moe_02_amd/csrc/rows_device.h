@@ -11,6 +11,26 @@ constexpr int kUnit = 8;
 // dtype of a matrix known at compile time, or only at run time
 constexpr int kAnyDtype = -1;
 
+// Where a lane's unit lies in its row.  A row's last values come with those before
+// them, as whole units that end where the row ends: `skip` of the eight are another
+// lane's too, who comes to the same results and may store the same values.  Loads and
+// stores then need no path for parts of a unit, whose waits would end the flow of the
+// loads behind it (SwiGLU, norm and sums of 1502 columns: within 5 % of 1504).  Sums
+// leave the skipped values out.  TAIL: units start where they would and end early, for
+// rows of less than eight values and for results that overwrite what other lanes read.
+template <bool TAIL>
+struct Span {
+  int c;       // column of the first value
+  int n;       // own values of the unit; 0 and less: none
+  int skip;    // values before the own ones (8 and more: no own ones)
+  __device__ __forceinline__ Span(int unit, int cols) {
+    const int begin = unit * kUnit;
+    n = cols - begin;
+    c = TAIL ? begin : min(begin, cols - kUnit);
+    skip = begin - c;
+  }
+};
+
 template <int DT>
 struct Unit {
   uint32_t w[DT == MOE_DT_BF16 ? 4 : 8];
@@ -22,31 +42,67 @@ __device__ __forceinline__ bool is_bf16(int dtype) {
   return DT == MOE_DT_BF16;
 }
 
-// Values [at, at + 8) of a matrix in memory, those past the first n as zeros
+// The first n < 8 values of a row's last unit come and go as a run of four, one of
+// two and one of one (those that n has), so in three accesses at most.  WORDS of
+// dwords hold eight values.
+template <int WORDS>
+__device__ __forceinline__ void load_tail(uint32_t (&w)[WORDS], const uint8_t* p, int n) {
+  constexpr int kSize = WORDS / 2, kHalf = WORDS / 2, kQuarter = WORDS / 4;   // bytes a value; dwords of four, of two
+  const bool has4 = n & 4;
+  uint32_t four[kHalf] = {}, two[kQuarter] = {}, one = 0;
+  if (has4) __builtin_memcpy(four, p, 4 * kSize);
+  if (n & 2) __builtin_memcpy(two, p + (n & 4) * kSize, 2 * kSize);
+  if (n & 1) __builtin_memcpy(&one, p + (n & 6) * kSize, kSize);
+  uint32_t v[WORDS];
+#pragma unroll
+  for (int i = 0; i < kHalf; ++i) {
+    const uint32_t t = i < kQuarter ? two[i % kQuarter] : 0u;
+    v[i] = has4 ? four[i] : t;
+    v[kHalf + i] = has4 ? t : 0u;
+  }
+  // behind an even number of values
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i * kQuarter] = v[i * kQuarter] | ((n & 6) == 2 * i ? one : 0u);
+  if constexpr (kQuarter == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[2 * i + 1] = v[2 * i + 1];
+  }
+}
+
+template <int WORDS>
+__device__ __forceinline__ void store_tail(uint8_t* p, const uint32_t (&w)[WORDS], int n) {
+  constexpr int kSize = WORDS / 2, kHalf = WORDS / 2, kQuarter = WORDS / 4;
+  const uint32_t has4 = n & 4 ? ~0u : 0u;
+  uint32_t four[kHalf], two[kQuarter], one = 0;
+#pragma unroll
+  for (int i = 0; i < kHalf; ++i) four[i] = w[i];
+#pragma unroll
+  for (int i = 0; i < kQuarter; ++i) two[i] = (w[kHalf + i] & has4) | (w[i] & ~has4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) one |= (n & 6) == 2 * i ? w[i * kQuarter] : 0u;
+  if (n & 4) __builtin_memcpy(p, four, 4 * kSize);
+  if (n & 2) __builtin_memcpy(p + (n & 4) * kSize, two, 2 * kSize);
+  if (n & 1) __builtin_memcpy(p + (n & 6) * kSize, &one, kSize);
+}
+
+// Values [at, at + 8) of a matrix in memory; TAIL: those past the first n as zeros
 // (n <= 0: none is read).
-template <int DT>
+template <bool TAIL, int DT>
 __device__ __forceinline__ void load_unit(Unit<DT>& u, const void* base, int dtype, int64_t at, int n) {
   constexpr int kWords = DT == MOE_DT_BF16 ? 4 : 8;
 #pragma unroll
   for (int i = 0; i < kWords; ++i) u.w[i] = 0;
   if (is_bf16<DT>(dtype)) {
-    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-    if (n >= kUnit) {
-      __builtin_memcpy(u.w, p, 16);
-    } else {
+    const uint8_t* p = static_cast<const uint8_t*>(base) + at * 2;
+    uint32_t w[4] = {};
+    if (!TAIL || n >= kUnit) __builtin_memcpy(w, p, 16);
+    else if (n > 0) load_tail(w, p, n);
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i)
-        if (i < n) u.w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
-    }
+    for (int i = 0; i < 4; ++i) u.w[i] = w[i];
   } else if constexpr (kWords == 8) {
-    const uint32_t* p = static_cast<const uint32_t*>(base) + at;
-    if (n >= kUnit) {
-      __builtin_memcpy(u.w, p, 32);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i)
-        if (i < n) u.w[i] = p[i];
-    }
+    const uint8_t* p = static_cast<const uint8_t*>(base) + at * 4;
+    if (!TAIL || n >= kUnit) __builtin_memcpy(u.w, p, 32);
+    else if (n > 0) load_tail(u.w, p, n);
   }
 }
 
@@ -62,6 +118,14 @@ __device__ __forceinline__ void unit_floats(const Unit<DT>& u, int dtype, float 
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) v[i] = __uint_as_float(u.w[i]);
   }
+}
+
+// Hides a unit's values from the optimiser, so that what was made of them before is
+// made again instead of being kept.
+template <int DT>
+__device__ __forceinline__ void forget_values(Unit<DT>& u) {
+#pragma unroll
+  for (int i = 0; i < (DT == MOE_DT_BF16 ? 4 : 8); ++i) opaque(u.w[i]);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -80,29 +144,23 @@ __device__ __forceinline__ void round_to(int dtype, float (&v)[kUnit]) {
   }
 }
 
-// The first n of eight values to [at, at + n) of a matrix.
+// Eight values to [at, at + 8) of a matrix; TAIL: the first n > 0 of them.
+template <bool TAIL>
 __device__ __forceinline__ void store_unit(void* base, int dtype, int64_t at, int n, const float (&v)[kUnit]) {
   if (dtype == MOE_DT_BF16) {
-    uint16_t* p = static_cast<uint16_t*>(base) + at;
+    uint8_t* p = static_cast<uint8_t*>(base) + at * 2;
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    if (n >= kUnit) {
-      __builtin_memcpy(p, w, 16);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i)
-        if (i < n) p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-    }
+    if (!TAIL || n >= kUnit) __builtin_memcpy(p, w, 16);
+    else store_tail(p, w, n);
   } else {
-    float* p = static_cast<float*>(base) + at;
-    if (n >= kUnit) {
-      __builtin_memcpy(p, v, 32);
-    } else {
+    uint8_t* p = static_cast<uint8_t*>(base) + at * 4;
+    uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i)
-        if (i < n) p[i] = v[i];
-    }
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
+    if (!TAIL || n >= kUnit) __builtin_memcpy(p, w, 32);
+    else store_tail(p, w, n);
   }
 }
 
@@ -115,17 +173,6 @@ __device__ __forceinline__ uint32_t top_bits(const float (&v)[kUnit]) {
   return m;
 }
 
-__device__ __forceinline__ uint32_t wave_max(uint32_t m) {
-  m = max(m, dpp<kDppXor1>(m));
-  m = max(m, dpp<kDppXor2>(m));
-  m = max(m, dpp<kDppHalfMirror>(m));
-  m = max(m, dpp<kDppMirror>(m));
-  auto r = __builtin_amdgcn_permlane16_swap(m, m, false, false);
-  m = max(r[0], r[1]);
-  r = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-  return max(r[0], r[1]);
-}
-
 // Scale of an E4M3 row from its largest magnitude.  Below 2^-126 a scale would
 // lose bits, and its reciprocal could overflow.
 __device__ __forceinline__ float e4m3_scale(uint32_t top) {
@@ -133,29 +180,66 @@ __device__ __forceinline__ float e4m3_scale(uint32_t top) {
   return fmaxf(__uint_as_float(top) / 448.0f, 0x1p-126f);
 }
 
-// E4M3 codes of eight values times 1 / scale (0: all codes 0).  The product with
-// the rounded reciprocal may pass 448 by a unit in the last place of fp32; E4M3
-// rounds everything below 464 to 448.
-__device__ __forceinline__ uint2 e4m3_codes(const float (&v)[kUnit], float inv) {
-  if (inv == 0.0f) return make_uint2(0u, 0u);
+// x / scale from the rounded reciprocal, one correction: the product alone would
+// put about one code in 10^6 on the other side of a tie.
+__device__ __forceinline__ float quotient(float x, float scale, float inv) {
+  const float v = x * inv;
+  return fmaf(fmaf(-v, scale, x), inv, v);
+}
+
+// E4M3 codes of eight values of a row with this scale (NaN: all codes 0).  A
+// quotient may pass 448 by a unit in the last place of fp32; E4M3 rounds
+// everything below 464 to 448.
+__device__ __forceinline__ uint2 e4m3_codes(const float (&v)[kUnit], float scale) {
+  if (scale != scale) return make_uint2(0u, 0u);
+  const float inv = 1.0f / scale;
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    int q = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] * inv, v[4 * i + 1] * inv, 0, false);
-    q = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * inv, v[4 * i + 3] * inv, q, true);
+    float d[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[j] = quotient(v[4 * i + j], scale, inv);
+    int q = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
+    q = __builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], q, true);
     w[i] = (uint32_t)q;
   }
   return make_uint2(w[0], w[1]);
 }
 
-// The first n of eight code bytes.
+// Eight code bytes; TAIL: the first n > 0 of them.
+template <bool TAIL>
 __device__ __forceinline__ void store_bytes(uint8_t* p, int n, uint2 q) {
-  if (n >= kUnit) {
+  if (!TAIL || n >= kUnit) {
     __builtin_memcpy(p, &q, 8);
-  } else {
+    return;
+  }
+  if (n & 4) __builtin_memcpy(p, &q.x, 4);
+  const uint32_t rest = n & 4 ? q.y : q.x;
+  if (n & 2) {
+    const uint16_t two = (uint16_t)rest;
+    __builtin_memcpy(p + (n & 4), &two, 2);
+  }
+  if (n & 1) p[n & 6] = (uint8_t)(n & 2 ? rest >> 16 : rest);
+}
+
+// The own values of a unit first, then zeros.
+__device__ __forceinline__ void own_first(float (&v)[kUnit], int skip) {
+  if (skip == 0) return;
+  if (skip & 4) {
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i)
-      if (i < n) p[i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+    for (int i = 0; i < kUnit; ++i) v[i] = i < 4 ? v[(i + 4) % kUnit] : 0.0f;
+  }
+  if (skip & 2) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) v[i] = i < 6 ? v[(i + 2) % kUnit] : 0.0f;
+  }
+  if (skip & 1) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) v[i] = i < 7 ? v[(i + 1) % kUnit] : 0.0f;
+  }
+  if (skip >= kUnit) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) v[i] = 0.0f;
   }
 }
 
@@ -178,32 +262,126 @@ __device__ __forceinline__ uint32_t mxfp4_codes(const float (&v)[kUnit], uint32_
   return q;
 }
 
-// Sum (maximum) over the G lanes that share a row: a wave, or the whole
-// workgroup through `lds`, which holds one value a wave and is free again after
-// the next barrier.
-template <int G>
-__device__ __forceinline__ double group_sum(double v, double* lds) {
-  v = wave_sum(v);
-  if constexpr (G > kWave) {
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = lds[0];
+// Reductions over G = 4, 8 .. 64 neighbouring lanes, every lane with the result.
+template <int G, class T, class F>
+__device__ __forceinline__ T lanes_reduce(T v, F&& join) {
+  auto step = [&](auto ctrl) {
+    constexpr int c = decltype(ctrl)::value;
+    if constexpr (sizeof(T) == 8) v = join(v, dppd<c>(v));
+    else v = join(v, __builtin_bit_cast(T, dpp<c>(__builtin_bit_cast(uint32_t, v))));
+  };
+  step(std::integral_constant<int, kDppXor1>{});
+  step(std::integral_constant<int, kDppXor2>{});
+  if constexpr (G >= 8) step(std::integral_constant<int, kDppHalfMirror>{});
+  if constexpr (G >= 16) step(std::integral_constant<int, kDppMirror>{});
+  auto swap = [&](auto m) {
+    if constexpr (sizeof(T) == 8) {
+      T a, b;
+      swap_pair<decltype(m)::value>(v, a, b);
+      v = join(a, b);
+    } else {
+      int a, b;
+      swap_pair<decltype(m)::value>(__builtin_bit_cast(int, v), a, b);
+      v = join(__builtin_bit_cast(T, a), __builtin_bit_cast(T, b));
+    }
+  };
+  if constexpr (G >= 32) swap(std::integral_constant<int, 16>{});
+  if constexpr (G >= 64) swap(std::integral_constant<int, 32>{});
+  return v;
+}
+
+// Over the G lanes that share a row: up to a wave, or the whole workgroup through
+// `lds`, which holds one value a wave and is free again after the next barrier.
+template <int G, class T, class F>
+__device__ __forceinline__ T group_reduce(T v, T* lds, F&& join) {
+  if constexpr (G <= kWave) return lanes_reduce<G>(v, join);
+  v = lanes_reduce<kWave>(v, join);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = lds[0];
 #pragma unroll
-    for (int i = 1; i < G / kWave; ++i) v += lds[i];
-  }
+  for (int i = 1; i < G / kWave; ++i) v = join(v, lds[i]);
   return v;
 }
 template <int G>
+__device__ __forceinline__ double group_sum(double v, double* lds) {
+  return group_reduce<G>(v, lds, [](double a, double b) { return a + b; });
+}
+template <int G>
 __device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t* lds) {
-  v = wave_max(v);
-  if constexpr (G > kWave) {
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = lds[0];
-#pragma unroll
-    for (int i = 1; i < G / kWave; ++i) v = max(v, lds[i]);
+  return group_reduce<G>(v, lds, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+
+// Workgroups go to the eight XCDs in turn.  In order they are numbered so that
+// neighbours run on one XCD.  Where rows end inside a line, both writers of the line
+// then meet in one L2 instead of each sending a part of it to memory (bf16, dispatch
+// of 8000 tokens to 8 rows of 4104: 122 us against 136; SwiGLU and gradient of 32000
+// x 4104: 357 against 392); with rows of whole lines taking turns is better (dispatch
+// of 16384 to 8 x 6144: 340 us against 355).
+__device__ __forceinline__ unsigned block_number(bool in_order) {
+  if (!in_order) return blockIdx.x;
+  const unsigned n = gridDim.x, xcd = blockIdx.x & 7, each = n >> 3, more = n & 7;
+  return xcd * each + min(xcd, more) + (blockIdx.x >> 3);
+}
+// Whether the rows of a matrix that is written end inside lines.
+inline bool ragged_lines(const void* p, int64_t pitch_bytes) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch_bytes) & 127) != 0;
+}
+
+// How the rows of a matrix lie over workgroups where each lane takes one chunk of
+// a row: rows of over 32 chunks take `parts` workgroups of `threads` lanes, shorter
+// ones 2^bits lanes (bits = -1 for the former).
+struct RowMap {
+  int parts, threads, bits;
+  int first;                // row of the launch's first workgroup
+  bool in_order;            // block_number
+};
+
+constexpr int kMapBlock = 256;
+
+// Row and chunk of a lane; the row is uniform over the workgroup if LONG.
+template <bool LONG>
+__device__ __forceinline__ void locate(const RowMap& m, int& row, int& chunk) {
+  if constexpr (LONG) {
+    const unsigned b = block_number(m.in_order), r = b / (unsigned)m.parts;
+    chunk = (b - r * m.parts) * blockDim.x + threadIdx.x;
+    row = m.first + r;
+  } else {
+    const unsigned at = block_number(m.in_order) * kMapBlock + threadIdx.x;
+    row = m.first + (at >> m.bits);
+    chunk = at & ((1u << m.bits) - 1);
   }
-  return v;
+}
+
+inline RowMap row_map(int chunks, bool in_order) {
+  if (chunks > 32) {
+    const int parts = (chunks + kMapBlock - 1) / kMapBlock;
+    const int each = (chunks + parts - 1) / parts;
+    return {parts, (each + kWave - 1) / kWave * kWave, -1, 0, in_order};
+  }
+  int bits = 0;
+  while ((1 << bits) < chunks) ++bits;
+  return {1, kMapBlock, bits, 0, in_order};
+}
+
+// Calls f(LONG, TAIL, grid, block, map), the first two as integral constants, for runs
+// of rows of at most 2^31 work items: a launch has to stay below 2^32.
+template <class F>
+hipError_t by_rows(RowMap m, int rows, bool tail, F&& f) {
+  const int64_t most = m.bits < 0 ? (1ll << 31) / ((int64_t)m.parts * kMapBlock) : 1 << 26;
+  for (int64_t r = 0; r < rows; r += most) {
+    const unsigned n = (unsigned)(rows - r < most ? rows - r : most);
+    m.first = (int)r;
+    auto launch = [&](auto T) {
+      if (m.bits < 0) f(std::true_type{}, T, dim3(n * m.parts), dim3(m.threads), m);
+      else f(std::false_type{}, T, dim3((unsigned)((((int64_t)n << m.bits) + kMapBlock - 1) / kMapBlock)), dim3(kMapBlock), m);
+    };
+    if (tail) launch(std::true_type{});
+    else launch(std::false_type{});
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace qmoe

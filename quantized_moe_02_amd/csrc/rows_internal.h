@@ -9,6 +9,9 @@ namespace qmoe {
 constexpr int kRowMaxCols = 65536;
 constexpr int kRowMaxRows = 16 * MOE_MAX_TOKENS;
 
+// Bytes of a value of MOE_DT_F32 or MOE_DT_BF16.
+inline int element(int dtype) { return dtype == MOE_DT_F32 ? 4 : 2; }
+
 // A matrix in device memory; ld in elements.
 struct RowMat {
   void* p;
@@ -25,6 +28,7 @@ struct NormArgs {
   int q_dtype;
   int rows, cols;
   float eps;
+  bool in_order;           // set by the launcher: how workgroups are numbered
 };
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s);
 
@@ -36,6 +40,7 @@ struct NormGradArgs {
   float* part;             // [workgroups][cols]: the workgroups' sums for dw
   int rows, cols;
   float eps;
+  bool in_order;           // as above
 };
 // The most workgroups, a row of `part` each, that the gradient of no more rows
 // takes, whatever its columns.
@@ -66,6 +71,7 @@ struct CollectGradArgs {
   const float* w;          // nullable
   float* dw;               // nullable
   int T, K, slots, cols;
+  bool in_order;           // as above
 };
 hipError_t launch_collect_grad(const CollectGradArgs& a, hipStream_t s);
 
@@ -75,6 +81,7 @@ struct SwigluArgs {
   void* out_scale;
   const int32_t* end;      // nullable: the row behind the last that counts
   int rows, cols;
+  bool in_order;           // as above
 };
 hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s);
 hipError_t launch_swiglu_grad(const SwigluArgs& a, hipStream_t s);

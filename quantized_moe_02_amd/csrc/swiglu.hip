@@ -6,8 +6,6 @@
 namespace qmoe {
 namespace {
 
-constexpr int kBlock = 256;
-
 // s = 1 / (1 + e^-g) and 1 - s, without overflow and without cancellation.
 __device__ __forceinline__ void sigmoids(float g, float& s, float& t) {
   const float x = __expf(-fabsf(g));
@@ -21,12 +19,14 @@ __device__ __forceinline__ int rows_that_count(const SwigluArgs& a) {
   return a.end ? min(max(*a.end, 0), a.rows) : a.rows;
 }
 
+template <bool TAIL, int DT>
+__device__ __forceinline__ void load_gate_up(const SwigluArgs& a, int64_t row, const Span<TAIL>& p, Unit<DT>& g, Unit<DT>& u) {
+  load_unit<TAIL>(g, a.gu.p, DT, row * a.gu.ld + p.c, p.n);
+  load_unit<TAIL>(u, a.gu.p, DT, row * a.gu.ld + a.cols + p.c, p.n);
+}
+
 template <int DT>
-__device__ __forceinline__ void swiglu_unit(const SwigluArgs& a, int64_t row, int c, float (&v)[kUnit]) {
-  const int n = a.cols - c;
-  Unit<DT> gr, ur;
-  load_unit(gr, a.gu.p, DT, row * a.gu.ld + c, n);
-  load_unit(ur, a.gu.p, DT, row * a.gu.ld + a.cols + c, n);
+__device__ __forceinline__ void swiglu_unit(const Unit<DT>& gr, const Unit<DT>& ur, float (&v)[kUnit]) {
   float g[kUnit], up[kUnit];
   unit_floats(gr, DT, g);
   unit_floats(ur, DT, up);
@@ -38,89 +38,156 @@ __device__ __forceinline__ void swiglu_unit(const SwigluArgs& a, int64_t row, in
   }
 }
 
-// A wave a row, `lanes` of it for MXFP4 a multiple of four.
-template <int DT>
-__global__ void __launch_bounds__(kBlock) swiglu_kernel(SwigluArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int rows = rows_that_count(a);
-  for (int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); row < rows; row += (int64_t)gridDim.x * 4) {
-    const int nb = (a.cols + kMxBlock - 1) / kMxBlock;
-    if (a.out.dtype == MOE_DT_E4M3) {
-      uint32_t top = 0;
-      float v[kUnit];
-      for (int c = lane * kUnit; c < a.cols; c += kWave * kUnit) {
-        swiglu_unit<DT>(a, row, c, v);
-        top = max(top, top_bits(v));
-      }
-      const float scale = e4m3_scale(wave_max(top));
-      const float inv = scale == scale ? 1.0f / scale : 0.0f;
-      for (int c = lane * kUnit; c < a.cols; c += kWave * kUnit) {
-        swiglu_unit<DT>(a, row, c, v);
-        store_bytes(static_cast<uint8_t*>(a.out.p) + row * a.cols + c, a.cols - c, e4m3_codes(v, inv));
-      }
-      if (lane == 0) static_cast<float*>(a.out_scale)[row] = scale;
-    } else {
-      for (int c = lane * kUnit; c < nb * kMxBlock; c += kWave * kUnit) {
-        float v[kUnit];
-        swiglu_unit<DT>(a, row, c, v);
-        if (a.out.dtype == MOE_DT_MXFP4) {
-          uint32_t byte;
-          const uint32_t q = mxfp4_codes(v, byte);
-          static_cast<uint32_t*>(a.out.p)[row * nb * 4 + c / kUnit] = q;
-          if (c % kMxBlock == 0) static_cast<uint8_t*>(a.out_scale)[row * nb + c / kMxBlock] = (uint8_t)byte;
-        } else if (c < a.cols) {
-          store_unit(a.out.p, a.out.dtype, row * a.out.ld + c, a.cols - c, v);
-        }
-      }
-    }
+// fp32, bf16 and MXFP4: a unit a lane.  A row's units come in whole quads, which
+// share a block of MXFP4.
+template <int DT, bool LONG, bool TAIL>
+__global__ void __launch_bounds__(kMapBlock) swiglu_kernel(SwigluArgs a, RowMap m) {
+  int row, unit;
+  locate<LONG>(m, row, unit);
+  const int nb = (a.cols + kMxBlock - 1) / kMxBlock;
+  if (row >= rows_that_count(a) || unit >= nb * 4) return;
+  const Span<TAIL> p(unit, a.cols);
+  Unit<DT> g, u;
+  float v[kUnit];
+  load_gate_up(a, row, p, g, u);
+  swiglu_unit(g, u, v);
+  if (a.out.dtype == MOE_DT_MXFP4) {
+    uint32_t byte;
+    own_first(v, p.skip);
+    const uint32_t q = mxfp4_codes(v, byte);
+    static_cast<uint32_t*>(a.out.p)[(int64_t)row * nb * 4 + unit] = q;
+    if (unit % 4 == 0) static_cast<uint8_t*>(a.out_scale)[(int64_t)row * nb + unit / 4] = (uint8_t)byte;
+  } else if (p.n > 0) {
+    store_unit<TAIL>(a.out.p, a.out.dtype, row * a.out.ld + p.c, p.n, v);
   }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kBlock) swiglu_grad_kernel(SwigluArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int rows = rows_that_count(a);
-  for (int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); row < rows; row += (int64_t)gridDim.x * 4) {
-    for (int c = lane * kUnit; c < a.cols; c += kWave * kUnit) {
-      const int n = a.cols - c;
-      Unit<DT> gr, ur;
-      Unit<kAnyDtype> dr;
-      load_unit(gr, a.gu.p, DT, row * a.gu.ld + c, n);
-      load_unit(ur, a.gu.p, DT, row * a.gu.ld + a.cols + c, n);
-      load_unit(dr, a.out.p, a.out.dtype, row * a.out.ld + c, n);
-      float g[kUnit], up[kUnit], dh[kUnit];
-      unit_floats(gr, DT, g);
-      unit_floats(ur, DT, up);
-      unit_floats(dr, a.out.dtype, dh);
+// E4M3: G lanes a row, which lies in their registers until its scale is known.
+template <int DT, int G, int U, bool TAIL>
+__global__ void __launch_bounds__(G > 256 ? G : 256) swiglu_e4m3_kernel(SwigluArgs a) {
+  constexpr int kBlock = G > 256 ? G : 256;
+  __shared__ uint32_t tops[kBlock / kWave];
+  const int lane = threadIdx.x % G;
+  int64_t row = block_number(a.in_order) * (kBlock / G);
+  if constexpr (G < kWave) row += threadIdx.x / G;
+  else if constexpr (G == kWave) row += __builtin_amdgcn_readfirstlane(threadIdx.x / G);
+  if (row >= rows_that_count(a)) return;
+  Unit<DT> g[U], u[U];
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) {
-        float s, t;
-        sigmoids(g[i], s, t);
-        const float d = dh[i] * s;
-        const float dg = d * up[i] * fmaf(g[i], t, 1.0f);
-        up[i] = d * g[i];
-        g[i] = dg;
-      }
-      store_unit(a.dgu.p, DT, row * a.dgu.ld + c, n, g);
-      store_unit(a.dgu.p, DT, row * a.dgu.ld + a.cols + c, n, up);
-    }
+  for (int i = 0; i < U; ++i) load_gate_up(a, row, Span<TAIL>(i * G + lane, a.cols), g[i], u[i]);
+  float v[U][kUnit];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    swiglu_unit(g[i], u[i], v[i]);
+    top = max(top, top_bits(v[i]));
   }
+  const float scale = e4m3_scale(group_max<G>(top, tops));
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const Span<TAIL> p(i * G + lane, a.cols);
+    if (p.n > 0) store_bytes<TAIL>(static_cast<uint8_t*>(a.out.p) + row * a.cols + p.c, p.n, e4m3_codes(v[i], scale));
+  }
+  if (lane == 0) static_cast<float*>(a.out_scale)[row] = scale;
 }
 
-unsigned blocks_of(int rows) { return (unsigned)std::min((rows + 3) / 4, 1 << 16); }
+// Rows past 16384 columns, read again once their scale is known.
+template <int DT>
+__global__ void __launch_bounds__(1024) swiglu_e4m3_wide_kernel(SwigluArgs a) {
+  __shared__ uint32_t tops[16];
+  const int64_t row = block_number(a.in_order);
+  if (row >= rows_that_count(a)) return;
+  Unit<DT> g, u;
+  float v[kUnit];
+  uint32_t top = 0;
+  for (int i = threadIdx.x; i * kUnit < a.cols; i += 1024) {
+    load_gate_up(a, row, Span<false>(i, a.cols), g, u);
+    swiglu_unit(g, u, v);
+    top = max(top, top_bits(v));
+  }
+  const float scale = e4m3_scale(group_max<1024>(top, tops));
+  for (int i = threadIdx.x; i * kUnit < a.cols; i += 1024) {
+    const Span<false> p(i, a.cols);
+    load_gate_up(a, row, p, g, u);
+    swiglu_unit(g, u, v);
+    store_bytes<false>(static_cast<uint8_t*>(a.out.p) + row * a.cols + p.c, p.n, e4m3_codes(v, scale));
+  }
+  if (threadIdx.x == 0) static_cast<float*>(a.out_scale)[row] = scale;
+}
+
+template <int DT, bool LONG, bool TAIL>
+__global__ void __launch_bounds__(kMapBlock) swiglu_grad_kernel(SwigluArgs a, RowMap m) {
+  int row, unit;
+  locate<LONG>(m, row, unit);
+  const Span<TAIL> p(unit, a.cols);
+  if (row >= rows_that_count(a) || p.n <= 0) return;
+  Unit<DT> gr, ur;
+  Unit<kAnyDtype> dr;
+  load_gate_up(a, row, p, gr, ur);
+  load_unit<TAIL>(dr, a.out.p, a.out.dtype, row * a.out.ld + p.c, p.n);
+  float g[kUnit], up[kUnit], dh[kUnit];
+  unit_floats(gr, DT, g);
+  unit_floats(ur, DT, up);
+  unit_floats(dr, a.out.dtype, dh);
+#pragma unroll
+  for (int i = 0; i < kUnit; ++i) {
+    float s, t;
+    sigmoids(g[i], s, t);
+    const float d = dh[i] * s;
+    const float dg = d * up[i] * fmaf(g[i], t, 1.0f);
+    up[i] = d * g[i];
+    g[i] = dg;
+  }
+  store_unit<TAIL>(a.dgu.p, DT, row * a.dgu.ld + p.c, p.n, g);
+  store_unit<TAIL>(a.dgu.p, DT, row * a.dgu.ld + a.cols + p.c, p.n, up);
+}
+
+template <int DT>
+hipError_t launch_e4m3(const SwigluArgs& a, hipStream_t s) {
+  const int units = (a.cols + kUnit - 1) / kUnit;
+  auto at = [&](auto G, auto U) {
+    constexpr int g = decltype(G)::value, block = g > 256 ? g : 256, rows = block / g;
+    hipLaunchKernelGGL((swiglu_e4m3_kernel<DT, g, decltype(U)::value, false>), dim3((a.rows + rows - 1) / rows), dim3(block), 0, s, a);
+  };
+  using std::integral_constant;
+  if (a.cols < kUnit)
+    hipLaunchKernelGGL((swiglu_e4m3_kernel<DT, 8, 1, true>), dim3((a.rows + 31) / 32), dim3(256), 0, s, a);
+  else if (units <= 8) at(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  else if (units <= 16) at(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  else if (units <= 32) at(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  else if (units <= 64) at(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (units <= 128) at(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else if (units <= 256) at(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  else if (units <= 512) at(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  else if (units <= 1024) at(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  else if (units <= 2048) at(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+  else hipLaunchKernelGGL((swiglu_e4m3_wide_kernel<DT>), dim3(a.rows), dim3(1024), 0, s, a);
+  return hipGetLastError();
+}
 
 }  // namespace
 
-hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s) {
-  if (a.gu.dtype == MOE_DT_F32) hipLaunchKernelGGL((swiglu_kernel<MOE_DT_F32>), dim3(blocks_of(a.rows)), dim3(kBlock), 0, s, a);
-  else hipLaunchKernelGGL((swiglu_kernel<MOE_DT_BF16>), dim3(blocks_of(a.rows)), dim3(kBlock), 0, s, a);
-  return hipGetLastError();
+hipError_t launch_swiglu(const SwigluArgs& args, hipStream_t s) {
+  SwigluArgs a = args;
+  a.in_order = ragged_lines(a.out.p, a.out.dtype == MOE_DT_E4M3 ? a.cols : a.out.ld * element(a.out.dtype));
+  if (a.out.dtype == MOE_DT_E4M3) return a.gu.dtype == MOE_DT_F32 ? launch_e4m3<MOE_DT_F32>(a, s) : launch_e4m3<MOE_DT_BF16>(a, s);
+  const int nb = (a.cols + kMxBlock - 1) / kMxBlock;
+  return by_rows(row_map(nb * (kMxBlock / kUnit), a.in_order && a.out.dtype != MOE_DT_MXFP4), a.rows, a.cols < kUnit,
+                 [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
+    constexpr bool l = decltype(L)::value, t = decltype(T)::value;
+    if (a.gu.dtype == MOE_DT_F32) hipLaunchKernelGGL((swiglu_kernel<MOE_DT_F32, l, t>), grid, block, 0, s, a, m);
+    else hipLaunchKernelGGL((swiglu_kernel<MOE_DT_BF16, l, t>), grid, block, 0, s, a, m);
+  });
 }
 
 hipError_t launch_swiglu_grad(const SwigluArgs& a, hipStream_t s) {
-  if (a.gu.dtype == MOE_DT_F32) hipLaunchKernelGGL((swiglu_grad_kernel<MOE_DT_F32>), dim3(blocks_of(a.rows)), dim3(kBlock), 0, s, a);
-  else hipLaunchKernelGGL((swiglu_grad_kernel<MOE_DT_BF16>), dim3(blocks_of(a.rows)), dim3(kBlock), 0, s, a);
-  return hipGetLastError();
+  const bool tail = a.cols < kUnit || (a.dgu.p == a.gu.p && a.cols % kUnit != 0);
+  return by_rows(row_map((a.cols + kUnit - 1) / kUnit, ragged_lines(a.dgu.p, a.dgu.ld * element(a.dgu.dtype))), a.rows, tail,
+                 [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
+    constexpr bool l = decltype(L)::value, t = decltype(T)::value;
+    if (a.gu.dtype == MOE_DT_F32) hipLaunchKernelGGL((swiglu_grad_kernel<MOE_DT_F32, l, t>), grid, block, 0, s, a, m);
+    else hipLaunchKernelGGL((swiglu_grad_kernel<MOE_DT_BF16, l, t>), grid, block, 0, s, a, m);
+  });
 }
 
 }  // namespace qmoe

@@ -325,9 +325,10 @@ def test_collect(T, K, cols, E, rt, yt, at, drop, pad):
     close(y, want, (K + 2) * U * mag, yt)
 
 
-def test_collect_onto_its_addend():
-    gen = _gen(8)
-    inv, rows, y = picks(9, 3, 5, gen), torch.randn(27, 70, generator=gen).cuda(), torch.randn(9, 70, generator=gen).cuda()
+@pytest.mark.parametrize("cols", [5, 70, 513, 1030, 2049, 6145])       # a row's last lane in a wave of its own, too
+def test_collect_onto_its_addend(cols):
+    gen = _gen(8, cols)
+    inv, rows, y = picks(9, 3, 5, gen), torch.randn(27, cols, generator=gen).cuda(), torch.randn(9, cols, generator=gen).cuda()
     want, mag = ref.collect(f64(rows), inv.numpy(), None, f64(y))
     q.moe_collect(rows, inv.cuda(), y, addend=y)
     close(y, want, 5 * U * mag, F)
