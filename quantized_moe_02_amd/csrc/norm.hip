@@ -48,15 +48,15 @@ __device__ __forceinline__ double squares(const float (&h)[kUnit], int skip) {
 }
 
 // h of a unit, rounded to the stream's type, from x and the residual.
-template <int DT>
-__device__ __forceinline__ void add_residual(const NormArgs& a, const Unit<DT>& x, const Unit<DT>& r, float (&h)[kUnit]) {
+template <int XT, int RT>
+__device__ __forceinline__ void add_residual(const NormArgs& a, const Unit<XT>& x, const Unit<RT>& r, float (&h)[kUnit]) {
   unit_floats(x, a.x.dtype, h);
   if (a.res.p) {
     float v[kUnit];
     unit_floats(r, a.res.dtype, v);
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) h[i] += v[i];
-    round_to(a.res.dtype, h);
+    round_to(RT == kAnyDtype ? a.res.dtype : RT, h);
   }
 }
 
@@ -72,15 +72,11 @@ __device__ __forceinline__ void hold(Unit<DT>& u, const float (&h)[kUnit]) {
   }
 }
 
-// The kernels of bf16 matrices have bf16 weights too.
-template <int DT>
-constexpr int weight_dtype() { return DT == MOE_DT_BF16 ? MOE_DT_BF16 : kAnyDtype; }
-
-// Nothing is stored before the whole row is read: h may be the residual itself, and
+// RT is h's type, with or without a residual.  Nothing is stored before the whole row is read: h may be the residual itself, and
 // the last lanes of a row read values of the ones before them.
-template <int DT, int G, int U, bool TAIL>
+template <int XT, int RT, int G, int U, bool TAIL>
 __global__ void __launch_bounds__(block_of(G)) rmsnorm_kernel(NormArgs a) {
-  constexpr int kRows = block_of(G) / G, kHeld = DT == MOE_DT_BF16 ? MOE_DT_BF16 : MOE_DT_F32;
+  constexpr int kRows = block_of(G) / G;
   __shared__ double sums[block_of(G) / kWave];
   __shared__ uint32_t tops[block_of(G) / kWave];
   const int lane = threadIdx.x % G;
@@ -88,8 +84,9 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_kernel(NormArgs a) {
   if constexpr (G < kWave) row += threadIdx.x / G;
   else if constexpr (G == kWave) row += __builtin_amdgcn_readfirstlane(threadIdx.x / G);
   if (row >= a.rows) return;
-  Unit<DT> x[U], r[U];
-  Unit<weight_dtype<DT>()> w[U];
+  Unit<XT> x[U];
+  Unit<RT> r[U];
+  Unit<kAnyDtype> w[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const Span<TAIL> p(u * G + lane, a.cols);
@@ -103,7 +100,7 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_kernel(NormArgs a) {
     float h[kUnit];
     add_residual(a, x[u], r[u], h);
     sum += squares(h, Span<TAIL>(u * G + lane, a.cols).skip);
-    hold(x[u], h);
+    hold(r[u], h);
   }
   const float m = inverse_rms(group_sum<G>(sum, sums), a.cols, a.eps);
   uint32_t top = 0;
@@ -111,8 +108,8 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_kernel(NormArgs a) {
   for (int u = 0; u < U; ++u) {
     const Span<TAIL> p(u * G + lane, a.cols);
     float h[kUnit], v[kUnit];
-    forget_values(x[u]);       // else the fp32 values stay in registers all along
-    unit_floats(x[u], kHeld, h);
+    forget_values(r[u]);       // else the fp32 values stay in registers all along
+    unit_floats(r[u], RT, h);
     if (a.h.p && p.n > 0) store_unit<TAIL>(a.h.p, a.h.dtype, row * a.h.ld + p.c, p.n, h);
     unit_floats(w[u], a.w_dtype, v);
 #pragma unroll
@@ -127,7 +124,7 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_kernel(NormArgs a) {
     for (int u = 0; u < U; ++u) {
       const Span<TAIL> p(u * G + lane, a.cols);
       float h[kUnit], v[kUnit];
-      unit_floats(x[u], kHeld, h);
+      unit_floats(r[u], RT, h);
       unit_floats(w[u], a.w_dtype, v);
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) v[i] = h[i] * m * v[i];
@@ -215,7 +212,12 @@ __device__ __forceinline__ double product(const float (&dy)[kUnit], const float 
 
 // Workgroups take rows in turn and hold dw's sums over theirs.  As in the norm,
 // nothing of a row is stored before all of it is read.
-template <int DT, int G, int U, bool TAIL>
+// Weights beside bf16 rows are bf16 too, but for any types.
+template <int DT>
+constexpr int weight_dtype() { return DT == MOE_DT_BF16 ? MOE_DT_BF16 : kAnyDtype; }
+
+// DT is the type of h, dh and dx, YT that of dy.
+template <int DT, int YT, int G, int U, bool TAIL>
 __global__ void __launch_bounds__(block_of(G)) rmsnorm_grad_kernel(NormGradArgs a) {
   constexpr int kBlock = block_of(G), kRows = kBlock / G;
   __shared__ double lds[2][2][kBlock / kWave];
@@ -232,7 +234,8 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_grad_kernel(NormGradArgs 
   }
   int turn = 0;
   for (; row < a.rows; row += (int64_t)gridDim.x * kRows, turn ^= 1) {
-    Unit<DT> hr[U], yr[U], dr[U];
+    Unit<DT> hr[U], dr[U];
+    Unit<YT> yr[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const Span<TAIL> p(u * G + lane, a.cols);
@@ -414,40 +417,45 @@ __global__ void __launch_bounds__(256) fill_zero_kernel(float* p, int n) {
   if (i < n) p[i] = 0.0f;
 }
 
-constexpr int kGradBlocks = 1024;
+// The most workgroups of the gradient, so parts of dw's sums: two per CU.  More would
+// hide more latency, but their parts cost more (16384 x 6144 bf16, norm and gradient:
+// 512 of them 299 us, 1024 314).  Rows past 8192 columns leave room for one per CU.
+constexpr int kGradBlocks = 512;
 
-// Calls f(dtype, lanes, units, tail) as integral constants for rows of up to MOST
-// columns, g() for longer ones.
+// Calls f(lanes, units, tail) as integral constants for rows of up to MOST columns,
+// g() for longer ones.
 template <int MOST, class F, class H>
-void by_shape(bool all_bf16, bool all_f32, int cols, F&& f, H&& g) {
+void by_shape(int cols, F&& f, H&& g) {
   using std::integral_constant;
   const int units = (cols + kUnit - 1) / kUnit;
-  auto shape = [&](auto D) {
-    auto at = [&](auto G, auto U) { f(D, G, U, std::false_type{}); };
-    if (cols < kUnit) f(D, integral_constant<int, 4>{}, integral_constant<int, 1>{}, std::true_type{});
-    else if (units <= 4) at(integral_constant<int, 4>{}, integral_constant<int, 1>{});
-    else if (units <= 8) at(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-    else if (units <= 16) at(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-    else if (units <= 32) at(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-    else if (units <= 64) at(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    else if (units <= 128) at(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-    else if (units <= 192) at(integral_constant<int, 64>{}, integral_constant<int, 3>{});
-    else if (units <= 256) at(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-    else if (units <= 512) at(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-    else if (units <= 768) at(integral_constant<int, 256>{}, integral_constant<int, 3>{});
-    else if (units <= 1024) at(integral_constant<int, 256>{}, integral_constant<int, 4>{});
-    else if constexpr (MOST <= 16384) at(integral_constant<int, 512>{}, integral_constant<int, 4>{});
-    else if (units <= 2048) at(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
-    else at(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
-  };
+  auto at = [&](auto G, auto U) { f(G, U, std::false_type{}); };
   if (cols > MOST) g();
-  else if (all_bf16) shape(integral_constant<int, MOE_DT_BF16>{});
-  else if (all_f32) shape(integral_constant<int, MOE_DT_F32>{});
-  else shape(integral_constant<int, kAnyDtype>{});
+  else if (cols < kUnit) f(integral_constant<int, 4>{}, integral_constant<int, 1>{}, std::true_type{});
+  else if (units <= 4) at(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  else if (units <= 8) at(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  else if (units <= 16) at(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  else if (units <= 32) at(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  else if (units <= 64) at(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (units <= 128) at(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else if (units <= 192) at(integral_constant<int, 64>{}, integral_constant<int, 3>{});
+  else if (units <= 256) at(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  else if (units <= 512) at(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  else if (units <= 768) at(integral_constant<int, 256>{}, integral_constant<int, 3>{});
+  else if (units <= 1024) at(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  else if constexpr (MOST <= 16384) at(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+  else if (units <= 2048) at(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+  else at(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
 
-bool all_of(int dtype, std::initializer_list<const RowMat*> all) {
-  return std::all_of(all.begin(), all.end(), [&](const RowMat* m) { return !m->p || m->dtype == dtype; });
+// Calls f of two dtypes as integral constants.
+template <class F>
+void by_dtypes(int a, int b, F&& f) {
+  using F32 = std::integral_constant<int, MOE_DT_F32>;
+  using Bf16 = std::integral_constant<int, MOE_DT_BF16>;
+  if (a == MOE_DT_F32 && b == MOE_DT_F32) f(F32{}, F32{});
+  else if (a == MOE_DT_F32) f(F32{}, Bf16{});
+  else if (b == MOE_DT_F32) f(Bf16{}, F32{});
+  else f(Bf16{}, Bf16{});
 }
 
 }  // namespace
@@ -457,11 +465,13 @@ hipError_t launch_rmsnorm(const NormArgs& args, hipStream_t s) {
   const RowMat& out = a.y.p ? a.y : a.h;
   a.in_order = out.p && ragged_lines(out.p, out.ld * element(out.dtype));
   by_shape<32768>(
-      a.w_dtype == MOE_DT_BF16 && all_of(MOE_DT_BF16, {&a.x, &a.res}), all_of(MOE_DT_F32, {&a.x, &a.res}), a.cols,
-      [&](auto D, auto G, auto U, auto T) {
+      a.cols,
+      [&](auto G, auto U, auto T) {
         constexpr int g = decltype(G)::value, rows = block_of(g) / g;
-        hipLaunchKernelGGL((rmsnorm_kernel<decltype(D)::value, g, decltype(U)::value, decltype(T)::value>),
-                           dim3((a.rows + rows - 1) / rows), dim3(block_of(g)), 0, s, a);
+        by_dtypes(a.x.dtype, a.res.p ? a.res.dtype : a.x.dtype, [&](auto X, auto R) {
+          hipLaunchKernelGGL((rmsnorm_kernel<decltype(X)::value, decltype(R)::value, g, decltype(U)::value, decltype(T)::value>),
+                             dim3((a.rows + rows - 1) / rows), dim3(block_of(g)), 0, s, a);
+        });
       },
       [&] { hipLaunchKernelGGL(rmsnorm_wide_kernel, dim3(a.rows), dim3(kWide), 0, s, a); });
   return hipGetLastError();
@@ -478,21 +488,29 @@ hipError_t launch_rmsnorm_grad(const NormGradArgs& args, hipStream_t s) {
   }
   // workgroups of `per` rows at a time, each as many times as the others
   int blocks = 0;
-  auto grid = [&](int per) {
+  auto grid = [&](int per, int most) {
     const int steps = (a.rows + per - 1) / per;
-    const int turns = (steps + kGradBlocks - 1) / kGradBlocks;
+    int turns = (steps + most - 1) / most;
+    // few: one workgroup, which needs no launch to join the parts (norm and gradient of 8
+    // x 300 rows through Python 13.8 us against 15.5; 8 x 1000 17.9, 8 x 6144 22.1)
+    if (a.dw && steps <= (a.cols <= 64 * kUnit ? 8 : 4)) turns = steps;
     return dim3(blocks = (steps + turns - 1) / turns);
   };
   by_shape<16384>(
-      a.w_dtype == MOE_DT_BF16 && all_of(MOE_DT_BF16, {&a.h, &a.dy, &a.dh}), all_of(MOE_DT_F32, {&a.h, &a.dy, &a.dh}), a.cols,
-      [&](auto D, auto G, auto U, auto T) {
-        constexpr int g = decltype(G)::value;
-        hipLaunchKernelGGL((rmsnorm_grad_kernel<decltype(D)::value, g, decltype(U)::value, decltype(T)::value>), grid(block_of(g) / g),
-                           dim3(block_of(g)), 0, s, a);
+      a.cols,
+      [&](auto G, auto U, auto T) {
+        auto launch = [&](auto D, auto Y) {
+          constexpr int g = decltype(G)::value;
+          hipLaunchKernelGGL((rmsnorm_grad_kernel<decltype(D)::value, decltype(Y)::value, g, decltype(U)::value, decltype(T)::value>),
+                             grid(block_of(g) / g, g > 256 ? kGradBlocks / 2 : kGradBlocks), dim3(block_of(g)), 0, s, a);
+        };
+        const bool same = a.dx.dtype == a.h.dtype && (a.h.dtype == MOE_DT_F32 || a.w_dtype == MOE_DT_BF16);
+        if (same) by_dtypes(a.h.dtype, a.dy.dtype, launch);
+        else launch(std::integral_constant<int, kAnyDtype>{}, std::integral_constant<int, kAnyDtype>{});
       },
       [&] {
-        if (a.cols <= 8 * kGradWide * kUnit) hipLaunchKernelGGL((rmsnorm_grad_wide_kernel<8>), grid(1), dim3(kGradWide), 0, s, a);
-        else hipLaunchKernelGGL((rmsnorm_grad_wide_kernel<16>), grid(1), dim3(kGradWide), 0, s, a);
+        if (a.cols <= 8 * kGradWide * kUnit) hipLaunchKernelGGL((rmsnorm_grad_wide_kernel<8>), grid(1, kGradBlocks / 2), dim3(kGradWide), 0, s, a);
+        else hipLaunchKernelGGL((rmsnorm_grad_wide_kernel<16>), grid(1, kGradBlocks / 2), dim3(kGradWide), 0, s, a);
       });
   if (a.dw && blocks > 1)
     hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((a.cols + kDwCols - 1) / kDwCols), dim3(1024), 0, s, a.part, blocks, a.cols, a.dw);
