@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kBlock) collect_grad_kernel(CollectGradArgs a,
   const int lanes = G ? G : blockDim.x;
   const int lane = G ? threadIdx.x % (G ? G : 1) : threadIdx.x;
   const int spans = (a.K + span - 1) / span;
-  unsigned at = block_number(a.in_order);
+  unsigned at = blockIdx.x;
   if constexpr (G == kWave) at = at * (kBlock / G) + __builtin_amdgcn_readfirstlane(threadIdx.x / G);
   else if constexpr (G != 0) at = at * (kBlock / G) + threadIdx.x / G;
   const int t = (int)(at / (unsigned)spans), begin = (int)(at - (unsigned)t * spans) * span;
@@ -251,7 +251,7 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
 
 hipError_t launch_collect(const CollectArgs& a, hipStream_t s) {
   const bool tail = a.cols < kUnit || (a.y.p == a.add.p && a.cols % kUnit != 0);
-  return by_rows(row_map((a.cols + kUnit - 1) / kUnit, ragged_lines(a.y.p, a.y.ld * element(a.y.dtype))), a.T, tail,
+  return by_rows(row_map((a.cols + kUnit - 1) / kUnit, false), a.T, tail,
                  [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
     constexpr bool l = decltype(L)::value, t = decltype(T)::value;
     if (a.rows.dtype == MOE_DT_F32) hipLaunchKernelGGL((collect_kernel<MOE_DT_F32, l, t>), grid, block, 0, s, a, m);
@@ -259,9 +259,7 @@ hipError_t launch_collect(const CollectArgs& a, hipStream_t s) {
   });
 }
 
-hipError_t launch_collect_grad(const CollectGradArgs& args, hipStream_t s) {
-  CollectGradArgs a = args;
-  a.in_order = a.drows.p && ragged_lines(a.drows.p, a.drows.ld * element(a.drows.dtype));
+hipError_t launch_collect_grad(const CollectGradArgs& a, hipStream_t s) {
   using std::integral_constant;
   const int chunks = (a.cols + kUnit - 1) / kUnit;
   auto launch = [&](auto D, auto G, auto T) {

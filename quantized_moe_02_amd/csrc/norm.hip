@@ -13,9 +13,7 @@ namespace {
 
 // Lanes of a workgroup whose rows take G lanes each, and its rows.
 constexpr int block_of(int g) { return g > 256 ? g : 256; }
-// Lanes for rows that are read again; the gradient holds dweight's sums in up to 128
-// registers of each.
-constexpr int kWide = 1024, kGradWide = 512;
+constexpr int kWide = 1024;      // lanes for rows that are read again
 
 // MXFP4 of a unit's own values; all lanes of a quad take part, also those past the
 // row's end.
@@ -80,7 +78,7 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_kernel(NormArgs a) {
   __shared__ double sums[block_of(G) / kWave];
   __shared__ uint32_t tops[block_of(G) / kWave];
   const int lane = threadIdx.x % G;
-  int64_t row = block_number(a.in_order) * kRows;
+  int64_t row = a.first + (int64_t)blockIdx.x * kRows;
   if constexpr (G < kWave) row += threadIdx.x / G;
   else if constexpr (G == kWave) row += __builtin_amdgcn_readfirstlane(threadIdx.x / G);
   if (row >= a.rows) return;
@@ -139,7 +137,7 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_kernel(NormArgs a) {
 __global__ void __launch_bounds__(kWide) rmsnorm_wide_kernel(NormArgs a) {
   __shared__ double sums[kWide / kWave];
   __shared__ uint32_t tops[kWide / kWave];
-  const int64_t row = block_number(a.in_order);
+  const int64_t row = a.first + (int64_t)blockIdx.x;
   const int units = (a.cols + kMxBlock - 1) / kMxBlock * 4;     // whole quads of lanes
   auto read = [&](int c, float (&h)[kUnit]) {
     Unit<kAnyDtype> x, r;
@@ -222,7 +220,7 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_grad_kernel(NormGradArgs 
   constexpr int kBlock = block_of(G), kRows = kBlock / G;
   __shared__ double lds[2][2][kBlock / kWave];
   const int lane = threadIdx.x % G;
-  int64_t row = block_number(a.in_order) * kRows;
+  int64_t row = (int64_t)blockIdx.x * kRows;
   if constexpr (G < kWave) row += threadIdx.x / G;
   else if constexpr (G == kWave) row += __builtin_amdgcn_readfirstlane(threadIdx.x / G);
   Unit<weight_dtype<DT>()> wr[U];
@@ -309,66 +307,57 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_grad_kernel(NormGradArgs 
   }
 }
 
-// Longer rows: read twice, dweight's sums in registers.
-template <int U>
-__global__ void __launch_bounds__(kGradWide) rmsnorm_grad_wide_kernel(NormGradArgs a) {
-  __shared__ double lds[2][2][kGradWide / kWave];
-  float acc[U][kUnit] = {};
+// Longer rows: read twice, dweight's sums in the workgroup's own part.
+__global__ void __launch_bounds__(kWide) rmsnorm_grad_wide_kernel(NormGradArgs a) {
+  __shared__ double lds[2][2][kWide / kWave];
+  float* part = gridDim.x == 1 ? a.dw : a.part + (int64_t)blockIdx.x * a.cols;
+  const int64_t first = blockIdx.x;
   int turn = 0;
-  for (int64_t row = block_number(a.in_order); row < a.rows; row += gridDim.x, turn ^= 1) {
-    auto read = [&](int c, float (&h)[kUnit], float (&dy)[kUnit], float (&g)[kUnit]) {
+  for (int64_t row = first; row < a.rows; row += gridDim.x, turn ^= 1) {
+    auto read = [&](int c, float (&h)[kUnit], float (&dy)[kUnit], float (&w)[kUnit]) {
       Unit<kAnyDtype> v;
       const int n = a.cols - c;
-      load_unit<true>(v, a.h.p, a.h.dtype, (int64_t)row * a.h.ld + c, n);
+      load_unit<true>(v, a.h.p, a.h.dtype, row * a.h.ld + c, n);
       unit_floats(v, a.h.dtype, h);
-      load_unit<true>(v, a.dy.p, a.dy.dtype, (int64_t)row * a.dy.ld + c, n);
+      load_unit<true>(v, a.dy.p, a.dy.dtype, row * a.dy.ld + c, n);
       unit_floats(v, a.dy.dtype, dy);
       load_unit<true>(v, a.w, a.w_dtype, c, n);
-      unit_floats(v, a.w_dtype, g);
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) g[i] *= dy[i];
+      unit_floats(v, a.w_dtype, w);
     };
     RowSums s{0, 0};
-    float h[kUnit], dy[kUnit], g[kUnit];
-    for (int c = threadIdx.x * kUnit; c < a.cols; c += kGradWide * kUnit) {
-      read(c, h, dy, g);
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) {
-        s.squares += (double)h[i] * h[i];
-        s.product += (double)g[i] * h[i];
-      }
+    float h[kUnit], dy[kUnit], w[kUnit];
+    for (int c = threadIdx.x * kUnit; c < a.cols; c += kWide * kUnit) {
+      read(c, h, dy, w);
+      s.squares += squares(h, 0);
+      s.product += product(dy, w, h, 0);
     }
-    s.squares = group_sum<kGradWide>(s.squares, lds[turn][0]);
-    s.product = group_sum<kGradWide>(s.product, lds[turn][1]);
+    s.squares = group_sum<kWide>(s.squares, lds[turn][0]);
+    s.product = group_sum<kWide>(s.product, lds[turn][1]);
     float m, k;
     row_factors(s, a.cols, a.eps, m, k);
+    for (int c = threadIdx.x * kUnit; c < a.cols; c += kWide * kUnit) {
+      const int n = a.cols - c;
+      read(c, h, dy, w);
+      float v[kUnit];
+      if (a.dw) {
+        Unit<MOE_DT_F32> u;
+        if (row != first) load_unit<true>(u, part, MOE_DT_F32, c, n);
+        unit_floats(u, MOE_DT_F32, v);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = (u * kGradWide + threadIdx.x) * kUnit, n = a.cols - c;
-      if (n <= 0) continue;
-      read(c, h, dy, g);
-      float dx[kUnit];
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) {
-        dx[i] = m * (g[i] - h[i] * k);
-        acc[u][i] += dy[i] * (h[i] * m);
+        for (int i = 0; i < kUnit; ++i) v[i] = (row != first ? v[i] : 0.0f) + dy[i] * (h[i] * m);
+        store_unit<true>(part, MOE_DT_F32, c, n, v);
       }
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) v[i] = m * (dy[i] * w[i] - h[i] * k);
       if (a.dh.p) {
-        Unit<kAnyDtype> v;
-        load_unit<true>(v, a.dh.p, a.dh.dtype, (int64_t)row * a.dh.ld + c, n);
-        unit_floats(v, a.dh.dtype, h);
+        Unit<kAnyDtype> u;
+        load_unit<true>(u, a.dh.p, a.dh.dtype, row * a.dh.ld + c, n);
+        unit_floats(u, a.dh.dtype, h);
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) dx[i] += h[i];
+        for (int i = 0; i < kUnit; ++i) v[i] += h[i];
       }
-      store_unit<true>(a.dx.p, a.dx.dtype, (int64_t)row * a.dx.ld + c, n, dx);
+      store_unit<true>(a.dx.p, a.dx.dtype, row * a.dx.ld + c, n, v);
     }
-  }
-  if (!a.dw) return;
-  float* part = gridDim.x == 1 ? a.dw : a.part + (int64_t)blockIdx.x * a.cols;
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int c = (u * kGradWide + threadIdx.x) * kUnit;
-    if (c < a.cols) store_unit<true>(part, MOE_DT_F32, c, a.cols - c, acc[u]);
   }
 }
 
@@ -462,26 +451,31 @@ void by_dtypes(int a, int b, F&& f) {
 
 hipError_t launch_rmsnorm(const NormArgs& args, hipStream_t s) {
   NormArgs a = args;
-  const RowMat& out = a.y.p ? a.y : a.h;
-  a.in_order = out.p && ragged_lines(out.p, out.ld * element(out.dtype));
+  hipError_t e = hipSuccess;
   by_shape<32768>(
       a.cols,
       [&](auto G, auto U, auto T) {
-        constexpr int g = decltype(G)::value, rows = block_of(g) / g;
-        by_dtypes(a.x.dtype, a.res.p ? a.res.dtype : a.x.dtype, [&](auto X, auto R) {
-          hipLaunchKernelGGL((rmsnorm_kernel<decltype(X)::value, decltype(R)::value, g, decltype(U)::value, decltype(T)::value>),
-                             dim3((a.rows + rows - 1) / rows), dim3(block_of(g)), 0, s, a);
+        constexpr int g = decltype(G)::value;
+        e = by_runs(a.rows, block_of(g), block_of(g) / g, [&](int first, dim3 grid) {
+          a.first = first;
+          by_dtypes(a.x.dtype, a.res.p ? a.res.dtype : a.x.dtype, [&](auto X, auto R) {
+            hipLaunchKernelGGL((rmsnorm_kernel<decltype(X)::value, decltype(R)::value, g, decltype(U)::value, decltype(T)::value>),
+                               grid, dim3(block_of(g)), 0, s, a);
+          });
         });
       },
-      [&] { hipLaunchKernelGGL(rmsnorm_wide_kernel, dim3(a.rows), dim3(kWide), 0, s, a); });
-  return hipGetLastError();
+      [&] {
+        e = by_runs(a.rows, kWide, 1, [&](int first, dim3 grid) {
+          a.first = first;
+          hipLaunchKernelGGL(rmsnorm_wide_kernel, grid, dim3(kWide), 0, s, a);
+        });
+      });
+  return e;
 }
 
 int norm_grad_most_blocks(int rows) { return std::min(std::max(rows, 1), kGradBlocks); }
 
-hipError_t launch_rmsnorm_grad(const NormGradArgs& args, hipStream_t s) {
-  NormGradArgs a = args;
-  a.in_order = ragged_lines(a.dx.p, a.dx.ld * element(a.dx.dtype));
+hipError_t launch_rmsnorm_grad(const NormGradArgs& a, hipStream_t s) {
   if (a.rows == 0) {
     hipLaunchKernelGGL(fill_zero_kernel, dim3((a.cols + 255) / 256), dim3(256), 0, s, a.dw, a.cols);
     return hipGetLastError();
@@ -509,8 +503,7 @@ hipError_t launch_rmsnorm_grad(const NormGradArgs& args, hipStream_t s) {
         else launch(std::integral_constant<int, kAnyDtype>{}, std::integral_constant<int, kAnyDtype>{});
       },
       [&] {
-        if (a.cols <= 8 * kGradWide * kUnit) hipLaunchKernelGGL((rmsnorm_grad_wide_kernel<8>), grid(1, kGradBlocks / 2), dim3(kGradWide), 0, s, a);
-        else hipLaunchKernelGGL((rmsnorm_grad_wide_kernel<16>), grid(1, kGradBlocks / 2), dim3(kGradWide), 0, s, a);
+        hipLaunchKernelGGL(rmsnorm_grad_wide_kernel, grid(1, kGradBlocks / 2), dim3(kWide), 0, s, a);
       });
   if (a.dw && blocks > 1)
     hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((a.cols + kDwCols - 1) / kDwCols), dim3(1024), 0, s, a.part, blocks, a.cols, a.dw);

@@ -28,7 +28,7 @@ struct NormArgs {
   int q_dtype;
   int rows, cols;
   float eps;
-  bool in_order;           // set by the launcher: how workgroups are numbered
+  int first;               // set by the launcher: row of a launch's first workgroup
 };
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s);
 
@@ -40,7 +40,6 @@ struct NormGradArgs {
   float* part;             // [workgroups][cols]: the workgroups' sums for dw
   int rows, cols;
   float eps;
-  bool in_order;           // as above
 };
 // The most workgroups, a row of `part` each, that the gradient of no more rows
 // takes, whatever its columns.
@@ -71,7 +70,6 @@ struct CollectGradArgs {
   const float* w;          // nullable
   float* dw;               // nullable
   int T, K, slots, cols;
-  bool in_order;           // as above
 };
 hipError_t launch_collect_grad(const CollectGradArgs& a, hipStream_t s);
 
@@ -81,9 +79,18 @@ struct SwigluArgs {
   void* out_scale;
   const int32_t* end;      // nullable: the row behind the last that counts
   int rows, cols;
-  bool in_order;           // as above
+  int first;               // as above
 };
 hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s);
 hipError_t launch_swiglu_grad(const SwigluArgs& a, hipStream_t s);
+
+// How the rows of a matrix lie over workgroups where each lane takes one chunk of
+// a row: rows of over 32 chunks take `parts` workgroups of `threads` lanes, shorter
+// ones 2^bits lanes (bits = -1 for the former).
+struct RowMap {
+  int parts, threads, bits;
+  int first;                // row of the launch's first workgroup
+  bool in_order;            // block_number
+};
 
 }  // namespace qmoe

@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) swiglu_e4m3_kernel(SwigluAr
   constexpr int kBlock = G > 256 ? G : 256;
   __shared__ uint32_t tops[kBlock / kWave];
   const int lane = threadIdx.x % G;
-  int64_t row = block_number(a.in_order) * (kBlock / G);
+  int64_t row = a.first + (int64_t)blockIdx.x * (kBlock / G);
   if constexpr (G < kWave) row += threadIdx.x / G;
   else if constexpr (G == kWave) row += __builtin_amdgcn_readfirstlane(threadIdx.x / G);
   if (row >= rows_that_count(a)) return;
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) swiglu_e4m3_kernel(SwigluAr
 template <int DT>
 __global__ void __launch_bounds__(1024) swiglu_e4m3_wide_kernel(SwigluArgs a) {
   __shared__ uint32_t tops[16];
-  const int64_t row = block_number(a.in_order);
+  const int64_t row = a.first + (int64_t)blockIdx.x;
   if (row >= rows_that_count(a)) return;
   Unit<DT> g, u;
   float v[kUnit];
@@ -143,36 +143,39 @@ __global__ void __launch_bounds__(kMapBlock) swiglu_grad_kernel(SwigluArgs a, Ro
 }
 
 template <int DT>
-hipError_t launch_e4m3(const SwigluArgs& a, hipStream_t s) {
-  const int units = (a.cols + kUnit - 1) / kUnit;
-  auto at = [&](auto G, auto U) {
-    constexpr int g = decltype(G)::value, block = g > 256 ? g : 256, rows = block / g;
-    hipLaunchKernelGGL((swiglu_e4m3_kernel<DT, g, decltype(U)::value, false>), dim3((a.rows + rows - 1) / rows), dim3(block), 0, s, a);
-  };
+hipError_t launch_e4m3(SwigluArgs a, hipStream_t s) {
   using std::integral_constant;
-  if (a.cols < kUnit)
-    hipLaunchKernelGGL((swiglu_e4m3_kernel<DT, 8, 1, true>), dim3((a.rows + 31) / 32), dim3(256), 0, s, a);
-  else if (units <= 8) at(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-  else if (units <= 16) at(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-  else if (units <= 32) at(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  else if (units <= 64) at(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  else if (units <= 128) at(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-  else if (units <= 256) at(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-  else if (units <= 512) at(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  else if (units <= 1024) at(integral_constant<int, 256>{}, integral_constant<int, 4>{});
-  else if (units <= 2048) at(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
-  else hipLaunchKernelGGL((swiglu_e4m3_wide_kernel<DT>), dim3(a.rows), dim3(1024), 0, s, a);
-  return hipGetLastError();
+  const int units = (a.cols + kUnit - 1) / kUnit;
+  auto with = [&](auto G, auto U, auto T) {
+    constexpr int g = decltype(G)::value, block = g > 256 ? g : 256;
+    return by_runs(a.rows, block, block / g, [&](int first, dim3 grid) {
+      a.first = first;
+      hipLaunchKernelGGL((swiglu_e4m3_kernel<DT, g, decltype(U)::value, decltype(T)::value>), grid, dim3(block), 0, s, a);
+    });
+  };
+  auto at = [&](auto G, auto U) { return with(G, U, std::false_type{}); };
+  if (a.cols < kUnit) return with(integral_constant<int, 8>{}, integral_constant<int, 1>{}, std::true_type{});
+  if (units <= 8) return at(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  if (units <= 16) return at(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  if (units <= 32) return at(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  if (units <= 64) return at(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (units <= 128) return at(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  if (units <= 256) return at(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  if (units <= 512) return at(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  if (units <= 1024) return at(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  if (units <= 2048) return at(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+  return by_runs(a.rows, 1024, 1, [&](int first, dim3 grid) {
+    a.first = first;
+    hipLaunchKernelGGL((swiglu_e4m3_wide_kernel<DT>), grid, dim3(1024), 0, s, a);
+  });
 }
 
 }  // namespace
 
-hipError_t launch_swiglu(const SwigluArgs& args, hipStream_t s) {
-  SwigluArgs a = args;
-  a.in_order = ragged_lines(a.out.p, a.out.dtype == MOE_DT_E4M3 ? a.cols : a.out.ld * element(a.out.dtype));
+hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s) {
   if (a.out.dtype == MOE_DT_E4M3) return a.gu.dtype == MOE_DT_F32 ? launch_e4m3<MOE_DT_F32>(a, s) : launch_e4m3<MOE_DT_BF16>(a, s);
   const int nb = (a.cols + kMxBlock - 1) / kMxBlock;
-  return by_rows(row_map(nb * (kMxBlock / kUnit), a.in_order && a.out.dtype != MOE_DT_MXFP4), a.rows, a.cols < kUnit,
+  return by_rows(row_map(nb * (kMxBlock / kUnit), a.out.dtype != MOE_DT_MXFP4 && ragged_lines(a.out.p, a.out.ld * element(a.out.dtype))), a.rows, a.cols < kUnit,
                  [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
     constexpr bool l = decltype(L)::value, t = decltype(T)::value;
     if (a.gu.dtype == MOE_DT_F32) hipLaunchKernelGGL((swiglu_kernel<MOE_DT_F32, l, t>), grid, block, 0, s, a, m);
