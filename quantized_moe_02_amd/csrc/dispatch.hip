@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kBlock) collect_grad_kernel(CollectGradArgs a,
 
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
   if (a.x.dtype != a.rows.dtype) {
-    return by_rows(row_map((a.cols + kUnit - 1) / kUnit, ragged_lines(a.rows.p, a.rows.ld * element(a.rows.dtype))), a.T,
+    return by_rows<false>(row_map((a.cols + kUnit - 1) / kUnit, ragged_lines(a.rows.p, a.rows.ld * element(a.rows.dtype))), a.T,
                    a.cols < kUnit, [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
       constexpr bool l = decltype(L)::value, t = decltype(T)::value;
       if (a.x.dtype == MOE_DT_F32) hipLaunchKernelGGL((dispatch_cast_kernel<MOE_DT_F32, l, t>), grid, block, 0, s, a, m);
@@ -243,7 +243,7 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
   c.T = a.T;
   c.K = a.K;
   c.slots = a.slots;
-  return by_rows(row_map(c.chunks + (c.scale_bytes + 15) / 16, ragged_lines(c.rows, c.row_pitch)), a.T, false,
+  return by_rows<false>(row_map(c.chunks + (c.scale_bytes + 15) / 16, ragged_lines(c.rows, c.row_pitch)), a.T, false,
                  [&](auto L, auto, dim3 grid, dim3 block, const RowMap& m) {
     hipLaunchKernelGGL((dispatch_copy_kernel<decltype(L)::value>), grid, block, 0, s, c, m);
   });
@@ -251,7 +251,7 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
 
 hipError_t launch_collect(const CollectArgs& a, hipStream_t s) {
   const bool tail = a.cols < kUnit || (a.y.p == a.add.p && a.cols % kUnit != 0);
-  return by_rows(row_map((a.cols + kUnit - 1) / kUnit, false), a.T, tail,
+  return by_rows<true>(row_map((a.cols + kUnit - 1) / kUnit, false), a.T, tail,
                  [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
     constexpr bool l = decltype(L)::value, t = decltype(T)::value;
     if (a.rows.dtype == MOE_DT_F32) hipLaunchKernelGGL((collect_kernel<MOE_DT_F32, l, t>), grid, block, 0, s, a, m);

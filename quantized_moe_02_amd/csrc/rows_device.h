@@ -373,19 +373,23 @@ hipError_t by_runs(int rows, int block, int per, F&& f) {
 }
 
 // Calls f(LONG, TAIL, grid, block, map), the first two as integral constants, for runs
-// of rows.
-template <class F>
+// of rows.  LONG_TAIL: long rows may need tails too, where a result may lie over an
+// input; others do for less than eight columns alone.
+template <bool LONG_TAIL, class F>
 hipError_t by_rows(RowMap m, int rows, bool tail, F&& f) {
   const int64_t most = m.bits < 0 ? kMostItems / ((int64_t)m.parts * kMapBlock) : kMostItems >> 5;
   for (int64_t r = 0; r < rows; r += most) {
     const unsigned n = (unsigned)(rows - r < most ? rows - r : most);
     m.first = (int)r;
-    auto launch = [&](auto T) {
-      if (m.bits < 0) f(std::true_type{}, T, dim3(n * m.parts), dim3(m.threads), m);
-      else f(std::false_type{}, T, dim3((unsigned)((((int64_t)n << m.bits) + kMapBlock - 1) / kMapBlock)), dim3(kMapBlock), m);
-    };
-    if (tail) launch(std::true_type{});
-    else launch(std::false_type{});
+    if (m.bits >= 0) {
+      const dim3 dense((unsigned)((((int64_t)n << m.bits) + kMapBlock - 1) / kMapBlock));
+      if (tail) f(std::false_type{}, std::true_type{}, dense, dim3(kMapBlock), m);
+      else f(std::false_type{}, std::false_type{}, dense, dim3(kMapBlock), m);
+    } else if (LONG_TAIL && tail) {
+      f(std::true_type{}, std::integral_constant<bool, LONG_TAIL>{}, dim3(n * m.parts), dim3(m.threads), m);
+    } else {
+      f(std::true_type{}, std::false_type{}, dim3(n * m.parts), dim3(m.threads), m);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -175,7 +175,7 @@ hipError_t launch_e4m3(SwigluArgs a, hipStream_t s) {
 hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s) {
   if (a.out.dtype == MOE_DT_E4M3) return a.gu.dtype == MOE_DT_F32 ? launch_e4m3<MOE_DT_F32>(a, s) : launch_e4m3<MOE_DT_BF16>(a, s);
   const int nb = (a.cols + kMxBlock - 1) / kMxBlock;
-  return by_rows(row_map(nb * (kMxBlock / kUnit), a.out.dtype != MOE_DT_MXFP4 && ragged_lines(a.out.p, a.out.ld * element(a.out.dtype))), a.rows, a.cols < kUnit,
+  return by_rows<false>(row_map(nb * (kMxBlock / kUnit), a.out.dtype != MOE_DT_MXFP4 && ragged_lines(a.out.p, a.out.ld * element(a.out.dtype))), a.rows, a.cols < kUnit,
                  [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
     constexpr bool l = decltype(L)::value, t = decltype(T)::value;
     if (a.gu.dtype == MOE_DT_F32) hipLaunchKernelGGL((swiglu_kernel<MOE_DT_F32, l, t>), grid, block, 0, s, a, m);
@@ -185,7 +185,7 @@ hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s) {
 
 hipError_t launch_swiglu_grad(const SwigluArgs& a, hipStream_t s) {
   const bool tail = a.cols < kUnit || (a.dgu.p == a.gu.p && a.cols % kUnit != 0);
-  return by_rows(row_map((a.cols + kUnit - 1) / kUnit, ragged_lines(a.dgu.p, a.dgu.ld * element(a.dgu.dtype))), a.rows, tail,
+  return by_rows<true>(row_map((a.cols + kUnit - 1) / kUnit, ragged_lines(a.dgu.p, a.dgu.ld * element(a.dgu.dtype))), a.rows, tail,
                  [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
     constexpr bool l = decltype(L)::value, t = decltype(T)::value;
     if (a.gu.dtype == MOE_DT_F32) hipLaunchKernelGGL((swiglu_grad_kernel<MOE_DT_F32, l, t>), grid, block, 0, s, a, m);

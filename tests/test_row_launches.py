@@ -1,0 +1,211 @@
+"""Launches of the row operators without a GPU: their objects over
+tests/native/record_rows.cpp in place of the HIP runtime.  Every launch is one
+that the runtime takes, the launches of a call cover its rows, and every kernel
+of the objects is reached."""
+import collections
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+import quantized_moe_02_amd as q
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CLANG = "/opt/rocm/llvm/bin/clang++"
+OBJECTS = [os.path.join(ROOT, "_build", o + ".o") for o in ("rows_api", "norm", "dispatch", "swiglu")]
+F = 1 << 40                                          # aligned, never dereferenced
+F32, BF16, MX, E4 = q.MOE_DT_F32, q.MOE_DT_BF16, q.MOE_DT_MXFP4, q.MOE_DT_E4M3
+MAX_T, MAX_R = q.MOE_MAX_TOKENS, 16 * q.MOE_MAX_TOKENS
+Launch = collections.namedtuple("Launch", "kernel args blocks threads first parts bits")
+
+
+class Recorder:
+    def __init__(self, folder):
+        so = os.path.join(str(folder), "librecord_rows.so")
+        subprocess.run([CLANG, "-x", "c++", "-std=c++17", "-O1", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__",
+                        "-I", os.path.join(ROOT, "include"), "-I", os.path.join(ROOT, "quantized_moe_02_amd", "csrc"),
+                        "-I", "/opt/rocm/include", os.path.join(ROOT, "tests", "native", "record_rows.cpp"),
+                        "-x", "none", *OBJECTS, "-Wl,-Bsymbolic", "-o", so], check=True)
+        self.lib = L = ctypes.CDLL(so)
+        for name in ("rmsnorm", "rmsnorm_grad", "rmsnorm_workspace_size", "dispatch", "collect", "collect_grad", "swiglu",
+                     "swiglu_grad"):
+            getattr(L, "moe_" + name).argtypes = getattr(q.lib(), "moe_" + name).argtypes
+        L.recorded_name.restype = L.registered_name.restype = ctypes.c_char_p
+        L.recorded_blocks.restype = L.recorded_threads.restype = ctypes.c_uint64
+        self.reached = set()
+
+    @staticmethod
+    def parse(mangled):
+        m = re.search(r"_GLOBAL__N_1\d+([a-z]\w*?)_kernel(?:I((?:L[bi]n?\d+E)+)E)?", mangled)
+        return m[1], tuple(int(v.replace("n", "-")) for v in re.findall(r"L[bi](n?\d+)E", m[2] or ""))
+
+    def take(self):
+        L, out = self.lib, []
+        for i in range(L.recorded()):
+            name = L.recorded_name(i).decode()
+            self.reached.add(name)
+            out.append(Launch(*self.parse(name), L.recorded_blocks(i), L.recorded_threads(i), L.recorded_first(i),
+                              L.recorded_parts(i), L.recorded_bits(i)))
+        L.forget()
+        return out
+
+
+@pytest.fixture(scope="module")
+def record(tmp_path_factory):
+    if not shutil.which(CLANG) or not all(map(os.path.exists, OBJECTS)):
+        pytest.skip("needs the regular build (_build/*.o) and the ROCm clang")
+    return Recorder(tmp_path_factory.mktemp("record_rows"))
+
+
+def _covers(launches, rows, units):
+    """Launches with a map: each row once, all its units."""
+    at = 0
+    for l in launches:
+        assert l.first == at and l.blocks * l.threads < 1 << 32
+        if l.bits < 0:
+            assert l.parts * l.threads >= units and l.threads % 64 == 0 and l.blocks % l.parts == 0
+            at += l.blocks // l.parts
+        else:
+            assert l.threads == 256 and 1 << l.bits >= units
+            assert len(launches) == 1 and l.blocks * 256 >= rows << l.bits
+            at += rows
+    assert at == rows
+
+
+SIZES = [(1, 1), (1, 7), (3, 8), (6, 99), (6, 104), (5, 33), (9, 255), (77, 256), (100, 257), (64, 6144), (1000, 2057), (MAX_T, 1), (MAX_T, 250),
+         (MAX_T, 6144), (MAX_T, 65535), (MAX_T - 1, 65536)]
+
+
+def _rows(fn, rec, T, cols, K=1, tt=BF16, rt=BF16, slots=MAX_R, alias=False, align=0, **over):
+    ld = cols
+    c = q.MoeRowsConfig(T, cols, K, slots, tt, rt, rt, ld, ld, ld)
+    coded = tt in (E4, MX)
+    p = F + align
+    args = {"dispatch": (p, F if coded else None, F, p, F if coded else None), "collect": (p, F, F, p if alias else p + (1 << 39), p),
+            "collect_grad": (p, p + (0 if alias else 1 << 39), F, F, p, F)}[fn]
+    args = tuple(over.get(i, a) for i, a in enumerate(args))
+    assert getattr(rec.lib, "moe_" + fn)(ctypes.byref(c), *args, None) == q.MOE_OK
+    return rec.take()
+
+
+@pytest.mark.parametrize("T,cols", SIZES)
+@pytest.mark.parametrize("tt,rt", [(BF16, BF16), (F32, F32), (F32, BF16), (BF16, F32), (E4, E4), (MX, MX)])
+def test_dispatch_launches(record, T, cols, tt, rt):
+    if tt == rt:
+        size = {F32: 4 * cols, BF16: 2 * cols, E4: cols, MX: (cols + 31) // 32 * 16}[tt]
+        scale = {E4: 4, MX: (cols + 31) // 32}.get(tt, 0)
+        units = -(-size // 16) + -(-scale // 16)
+    else:
+        units = -(-cols // 8)
+    _covers(_rows("dispatch", record, T, cols, tt=tt, rt=rt), T, units)
+
+
+@pytest.mark.parametrize("T,cols", SIZES)
+@pytest.mark.parametrize("rt", [BF16, F32])
+@pytest.mark.parametrize("alias", [False, True])
+def test_collect_launches(record, T, cols, rt, alias):
+    ls = _rows("collect", record, T, cols, K=16, rt=rt, alias=alias)
+    _covers(ls, T, -(-cols // 8))
+    # over the addend no value may be read by one lane and written by another
+    assert all(l.args[2] == int(cols < 8 or (alias and cols % 8 != 0)) for l in ls)
+    for K in (1, 16):
+        for T2 in (1, 100, T):
+            ls = _rows("collect_grad", record, T2, cols, K=K, rt=rt, alias=alias)
+            assert len(ls) == 1 and ls[0].blocks * ls[0].threads < 1 << 32
+            l = ls[0]
+            assert l.args[2] == int(cols < 8 or (alias and cols % 8 != 0))
+            groups = T2 * -(-K // l.parts)
+            per = l.threads // l.args[1] if l.args[1] else 1
+            assert l.blocks * per >= groups and (l.args[1] or l.threads * 4 >= min(-(-cols // 8), 256))
+
+
+def _swiglu(rec, rows, cols, gt=BF16, ot=BF16, grad=False, alias=False):
+    c = q.MoeSwigluConfig(rows, cols, 1, gt, ot, 2 * cols, cols)
+    if grad:
+        assert rec.lib.moe_swiglu_grad(ctypes.byref(c), F, F, None, F if alias else 2 * F, None) == q.MOE_OK
+    else:
+        assert rec.lib.moe_swiglu(ctypes.byref(c), F, None, F, F if ot in (E4, MX) else None, None) == q.MOE_OK
+    return rec.take()
+
+
+E4_SIZES = [(4, c) for c in (1, 8, 64, 128, 256, 512, 1024, 2048, 4096, 8192, 16384, 16385)] + [(MAX_R, 65536), (MAX_R, 16384)]
+
+
+@pytest.mark.parametrize("rows,cols", SIZES + [(MAX_R, 1), (MAX_R, 200), (MAX_R, 65536)])
+@pytest.mark.parametrize("gt", [BF16, F32])
+def test_swiglu_launches(record, rows, cols, gt):
+    for ot in (BF16, MX):
+        _covers(_swiglu(record, rows, cols, gt, ot), rows, -(-cols // 32) * 4)
+    for alias in (False, True):
+        ls = _swiglu(record, rows, cols, gt, grad=True, alias=alias)
+        _covers(ls, rows, -(-cols // 8))
+        assert all(l.args[2] == int(cols < 8 or (alias and cols % 8 != 0)) for l in ls)
+
+
+@pytest.mark.parametrize("rows,cols", SIZES + E4_SIZES)
+@pytest.mark.parametrize("gt", [BF16, F32])
+def test_swiglu_e4m3_launches(record, rows, cols, gt):
+    at = 0
+    for l in _swiglu(record, rows, cols, gt, E4):
+        per = l.threads // l.args[1] if len(l.args) > 1 else 1
+        assert l.first == at and l.blocks * l.threads < 1 << 32
+        assert len(l.args) == 1 or l.args[1] * l.args[2] * 8 >= cols
+        at += l.blocks * per
+    assert 0 <= at - rows < per
+
+
+NORM = [(4, c) for c in (1, 8, 33, 65, 129, 257, 513, 1025, 1537, 2049, 4097, 6145, 8193, 16385, 32769)] + [
+    (MAX_R, c) for c in (1, 512, 6144, 16384, 32768, 65536)]
+
+
+@pytest.mark.parametrize("rows,cols", NORM)
+@pytest.mark.parametrize("xt", [F32, BF16])
+@pytest.mark.parametrize("rt", [F32, BF16])
+def test_norm_launches(record, rows, cols, xt, rt):
+    c = q.MoeRmsnormConfig(rows, cols, xt, rt, F32, BF16, 0, 1e-6, cols, cols, cols, cols)
+    assert record.lib.moe_rmsnorm(ctypes.byref(c), F, F, F, F, F, None, None, None) == q.MOE_OK
+    at = 0
+    for l in record.take():
+        per = l.threads // l.args[2] if l.args else 1
+        assert l.first == at and l.blocks * l.threads < 1 << 32 and (not l.args or l.args[2] * l.args[3] * 8 >= cols)
+        at += l.blocks * per
+    assert 0 <= at - rows < per
+
+
+@pytest.mark.parametrize("rows,cols", NORM + [(r, c) for r in (1, 2, 31, 32, 33, 511, 512, 513, 5000) for c in (1, 40, 512, 513, 6144, 9000, 20000)])
+def test_norm_grad_launches(record, rows, cols):
+    for ht, yt, xt, wt in ((F32, F32, F32, BF16), (F32, BF16, F32, F32), (BF16, F32, BF16, BF16), (BF16, BF16, BF16, BF16),
+                           (BF16, BF16, BF16, F32), (F32, BF16, BF16, BF16)):
+        c = q.MoeRmsnormGradConfig(rows, cols, ht, wt, yt, xt, 1e-6, cols, cols, cols, cols)
+        n = ctypes.c_size_t(0)
+        assert record.lib.moe_rmsnorm_workspace_size(rows, cols, ctypes.byref(n)) == q.MOE_OK
+        assert record.lib.moe_rmsnorm_grad(ctypes.byref(c), F, F, F, F, F, F, F, n.value, None) == q.MOE_OK
+        ls = record.take()
+        main = ls[0]
+        assert main.kernel.startswith("rmsnorm_grad") and all(l.blocks * l.threads < 1 << 32 for l in ls)
+        assert main.blocks * cols * 4 <= n.value               # the workgroups' parts fit the workspace
+        assert [l.kernel for l in ls[1:]] == (["rmsnorm_dw"] if main.blocks > 1 else [])
+        assert not ls[1:] or ls[1].blocks * 32 >= cols
+        # the last turn of the workgroups is not an idle one for all of them
+        per = main.threads // main.args[2] if main.args else 1
+        steps = -(-rows // per)
+        assert main.blocks <= steps and not main.args or main.args[2] * main.args[3] * 8 >= cols
+        assert record.lib.moe_rmsnorm_grad(ctypes.byref(c), F, F, F, None, F, None, None, 0, None) == q.MOE_OK
+        assert len(record.take()) == 1                          # no dweight: nothing to join
+    if rows == 4:
+        c = q.MoeRmsnormGradConfig(0, cols, F32, F32, F32, F32, 1e-6, cols, cols, cols, cols)
+        assert record.lib.moe_rmsnorm_grad(ctypes.byref(c), F, F, F, F, F, F, F, 1 << 30, None) == q.MOE_OK
+        ls = record.take()
+        assert [l.kernel for l in ls] == ["fill_zero"] and ls[0].blocks * ls[0].threads >= cols
+
+
+def test_every_kernel_is_reached(record):
+    """After the calls above (this test runs last in its file)."""
+    every = {record.lib.registered_name(i).decode() for i in range(record.lib.registered())}
+    missing = {Recorder.parse(n) for n in every - record.reached}
+    if len(record.reached) < 20:
+        pytest.skip("needs the file's other tests")
+    assert not missing, sorted(missing)
