@@ -568,7 +568,13 @@ def _packer(config):
     code = {ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_int64: "q"}
     s = struct.Struct("@" + "".join(code[t] for _, t in config._fields_))
     assert s.size == ctypes.sizeof(config)
-    return s.pack
+
+    def pack(*values):
+        try:
+            return s.pack(*values)
+        except (struct.error, OverflowError):      # sizes past 32 bits
+            raise QmoeError(MOE_ERR_UNSUPPORTED, config.__name__) from None
+    return pack
 
 
 _norm_config, _norm_grad_config = _packer(MoeRmsnormConfig), _packer(MoeRmsnormGradConfig)

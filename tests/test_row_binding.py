@@ -101,3 +101,15 @@ def test_combinations(no_library):  # noqa: F811
                  lambda: q.moe_collect(z(6, 65)[:, 1:], inv, z(2, 66)[:, :64])):
         with pytest.raises(Reached):                 # rows at a pitch of their own are taken
             call()
+
+
+def test_sizes_past_the_limits(monkeypatch):
+    """A matrix of more than 2^31 rows, an eps past fp32."""
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0)
+    monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    far = lambda *s: On.of(torch.empty(s, dtype=BF, device="meta"))
+    w = On.of(torch.zeros(1))
+    for call in (lambda: q.moe_rmsnorm(far(3 << 31, 1), w, 1e-6, y=far(3 << 31, 1)), lambda: q.moe_swiglu(far(3 << 31, 2), far(3 << 31, 1)),
+                 lambda: q.moe_rmsnorm(On.of(torch.zeros(2, 1)), w, 1e39, y=On.of(torch.zeros(2, 1)))):
+        with pytest.raises(q.QmoeError):
+            call()
