@@ -108,11 +108,11 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_kernel(NormArgs a) {
     float h[kUnit], v[kUnit];
     forget_values(r[u]);       // else the fp32 values stay in registers all along
     unit_floats(r[u], RT, h);
-    if (a.h.p && p.n > 0) store_unit<TAIL>(a.h.p, a.h.dtype, row * a.h.ld + p.c, p.n, h);
+    if (a.h.p && p.n > 0) store_unit<TAIL>(a.h.p, a.h.dtype, row * a.h.ld + p.c, p.n, h, a.past_cache);
     unit_floats(w[u], a.w_dtype, v);
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) v[i] = h[i] * m * v[i];
-    if (a.y.p && p.n > 0) store_unit<TAIL>(a.y.p, a.y.dtype, row * a.y.ld + p.c, p.n, v);
+    if (a.y.p && p.n > 0) store_unit<TAIL>(a.y.p, a.y.dtype, row * a.y.ld + p.c, p.n, v, a.past_cache);
     if (a.q && a.q_dtype == MOE_DT_MXFP4) put_mxfp4(a, row, u * G + lane, p.skip, v);
     if (a.q && a.q_dtype == MOE_DT_E4M3) top = max(top, top_bits(v));
   }
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_grad_kernel(NormGradArgs 
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) dx[i] += d[i];
       }
-      if (p.n > 0) store_unit<TAIL>(a.dx.p, a.dx.dtype, row * a.dx.ld + p.c, p.n, dx);
+      if (p.n > 0) store_unit<TAIL>(a.dx.p, a.dx.dtype, row * a.dx.ld + p.c, p.n, dx, a.past_cache);
     }
   }
   if (!a.dw) return;
@@ -451,6 +451,7 @@ void by_dtypes(int a, int b, F&& f) {
 
 hipError_t launch_rmsnorm(const NormArgs& args, hipStream_t s) {
   NormArgs a = args;
+  a.past_cache = past_cache((int64_t)a.rows * a.cols * ((a.h.p ? element(a.h.dtype) : 0) + (a.y.p ? element(a.y.dtype) : 0)));
   hipError_t e = hipSuccess;
   by_shape<32768>(
       a.cols,
@@ -475,7 +476,9 @@ hipError_t launch_rmsnorm(const NormArgs& args, hipStream_t s) {
 
 int norm_grad_most_blocks(int rows) { return std::min(std::max(rows, 1), kGradBlocks); }
 
-hipError_t launch_rmsnorm_grad(const NormGradArgs& a, hipStream_t s) {
+hipError_t launch_rmsnorm_grad(const NormGradArgs& args, hipStream_t s) {
+  NormGradArgs a = args;
+  a.past_cache = past_cache((int64_t)a.rows * a.cols * element(a.dx.dtype));
   if (a.rows == 0) {
     hipLaunchKernelGGL(fill_zero_kernel, dim3((a.cols + 255) / 256), dim3(256), 0, s, a.dw, a.cols);
     return hipGetLastError();

@@ -144,23 +144,42 @@ __device__ __forceinline__ void round_to(int dtype, float (&v)[kUnit]) {
   }
 }
 
+// 16 bytes to memory, past the caches where the results are more than they hold.
+__device__ __forceinline__ void store16(uint8_t* p, const uint32_t* w, bool past_cache) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+  const u32x4 v = {w[0], w[1], w[2], w[3]};
+  if (past_cache) {
+    // the empty statements keep the two stores from becoming one ordinary one
+    asm volatile("");
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+    asm volatile("");
+  } else {
+    *reinterpret_cast<u32x4*>(p) = v;
+  }
+}
+
 // Eight values to [at, at + 8) of a matrix; TAIL: the first n > 0 of them.
 template <bool TAIL>
-__device__ __forceinline__ void store_unit(void* base, int dtype, int64_t at, int n, const float (&v)[kUnit]) {
+__device__ __forceinline__ void store_unit(void* base, int dtype, int64_t at, int n, const float (&v)[kUnit],
+                                           bool past_cache = false) {
   if (dtype == MOE_DT_BF16) {
     uint8_t* p = static_cast<uint8_t*>(base) + at * 2;
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    if (!TAIL || n >= kUnit) __builtin_memcpy(p, w, 16);
+    if (!TAIL || n >= kUnit) store16(p, w, past_cache);
     else store_tail(p, w, n);
   } else {
     uint8_t* p = static_cast<uint8_t*>(base) + at * 4;
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
-    if (!TAIL || n >= kUnit) __builtin_memcpy(p, w, 32);
-    else store_tail(p, w, n);
+    if (!TAIL || n >= kUnit) {
+      store16(p, w, past_cache);
+      store16(p + 16, w + 4, past_cache);
+    } else {
+      store_tail(p, w, n);
+    }
   }
 }
 
@@ -324,6 +343,15 @@ __device__ __forceinline__ unsigned block_number(bool in_order) {
   const unsigned n = gridDim.x, xcd = blockIdx.x & 7, each = n >> 3, more = n & 7;
   return xcd * each + min(xcd, more) + (blockIdx.x >> 3);
 }
+// Whether the norm's results go past the caches: more of them than the 256 MB behind
+// L2 hold only push out what is yet to be read.  Norm of 16384 x 6144 bf16 with the
+// kernel that quantises its result 183 us past the caches and 190 through them (alone
+// 133 and 140); of 8192 rows, which the next kernel finds there, 89 and 85.  The
+// gradient of collect is faster past them by itself (4096 tokens, 403 MB: 173 us, 182),
+// but the products that read its rows lose more (811 us in all, 806), and so it is with
+// SwiGLU (32768 x 2048 and what quantises it: 99 us, 89).
+inline bool past_cache(int64_t bytes) { return bytes > (int64_t)256 << 20; }
+
 // Whether the rows of a matrix that is written end inside lines.
 inline bool ragged_lines(const void* p, int64_t pitch_bytes) {
   return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch_bytes) & 127) != 0;

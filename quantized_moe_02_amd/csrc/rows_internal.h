@@ -28,7 +28,10 @@ struct NormArgs {
   int q_dtype;
   int rows, cols;
   float eps;
-  int first;               // set by the launcher: row of a launch's first workgroup
+  // set by the launcher: row of a launch's first workgroup; whether results go past
+  // the caches
+  int first;
+  bool past_cache;
 };
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s);
 
@@ -40,6 +43,7 @@ struct NormGradArgs {
   float* part;             // [workgroups][cols]: the workgroups' sums for dw
   int rows, cols;
   float eps;
+  bool past_cache;         // as above
 };
 // The most workgroups, a row of `part` each, that the gradient of no more rows
 // takes, whatever its columns.
