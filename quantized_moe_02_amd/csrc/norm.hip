@@ -1,9 +1,30 @@
 // Root-mean-square norm with the residual's addition, and its gradient.
 //
-// A row lies in the registers of the G lanes that share it, U units of eight
-// values a lane, so that it is read once for its sum of squares and its result
-// alike: a wave takes a row of up to 512 columns, a workgroup of 256 one of up to
-// 8192.  Longer rows are read again from L2 for each pass over them.
+//   h = x + residual,  y = h m w  with  m = 1 / sqrt(mean(h^2) + eps)
+//   g = dy w,  dx = dh + m (g - h m^2 mean(g h)),  dw = sum over rows of dy h m
+//
+// Both move bytes and are bound by HBM.  A row lies in the registers of the G lanes
+// that share it, U units of eight values a lane, so that it is read once for its sums
+// and its results alike; it stays there as it came (bf16 as bf16) and is widened again
+// after the sums, which halves the registers.  Rows of up to 512 columns take the 4 to
+// 64 lanes that they fill, of up to 1536 a wave, of up to 8192 a workgroup of 256, then
+// of 512 or 1024; past 32768 (gradient: 16384) they are read again from L2.
+//
+// Sums over a row are float64: squares of fp32 values leave fp32's range, and fp64
+// additions do not show beside the bytes.  m, the products and y are fp32, each result
+// rounded once.
+//
+// dw: a workgroup of the gradient takes rows in turn and holds the sums of its columns
+// in registers (rows of several to a workgroup meet in LDS); a second launch adds the
+// workgroups' parts in float64, in order.  No atomics, the same bits every time.
+//
+// Measured, averages: 16384 x 6144 bf16 with residual 135 us (805 MB, 6.0 TB/s), with
+// E4M3 rows beside 156 (906 MB, 5.8 TB/s); followed by its gradient 146 + 140, and 5 to
+// join 512 parts (1.61 GB in all, 5.5 TB/s).  1 x 6144 4 us, 64 x 6144 fp32 onto bf16 to
+// MXFP4 5.5: the latency of one row.  1027 x 2057 fp32 7 us, its gradient 11.5 + 4: the
+// launches, and three rows one after the other.  24000 x 1503 bf16 58 us (5.0 TB/s).
+// 1627 x 8815 with fp32 dy 73 us for both against 42 at a copy's rate: one workgroup of
+// 512 per CU, its registers full, waits for each row.
 #include <algorithm>
 
 #include "rows_device.h"

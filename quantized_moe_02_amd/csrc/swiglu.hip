@@ -1,4 +1,17 @@
 // SwiGLU over rows [gate | up] in expert order, and its gradient.
+//
+//   out = g s up with s = 1 / (1 + e^-g);  dgate = dh up s (1 + g (1 - s)),  dup = dh g s
+//
+// Both move bytes and are bound by HBM: a lane takes eight values of gate, up (and dh)
+// at once, rows behind the last expert's are left out by their number alone.  E4M3 needs
+// a row's largest value first, so there the row stays in the registers of 8 to 1024
+// lanes.  e^-|g| never overflows, and 1 - s comes without cancellation; it is the
+// hardware's power of two with its argument rounded at its own size, so s is off by up
+// to (1.5 |g| + 12) 2^-24 of itself, and is 0 where e^-|g| lies below 2^-126.
+//
+// Measured, averages: 32768 x 2048 bf16 72 us, its gradient 114 (403 and 671 MB, 5.6 and
+// 5.9 TB/s); to E4M3 20000 x 2048 37 us (5.4 TB/s); 777 x 1001 fp32 4.0 and 5.0 us; 8 x
+// 2048 to E4M3 2.7 us.
 #include <algorithm>
 
 #include "rows_device.h"
