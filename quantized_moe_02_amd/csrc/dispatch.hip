@@ -7,17 +7,18 @@
 // All of it moves bytes and is bound by HBM.  A workgroup goes by tokens, so that a
 // token's row is read (written) once and its top_k rows are written (read) where
 // inv_perm says; going by slots would read it top_k times.  Long rows: one token a
-// workgroup, whose slots are then scalars; a lane has eight rows in flight (collect) or
-// four and dy (gradient: eight take 192 registers, 4096 tokens of 8 x 6144 300 us for
-// both against 283).  Few tokens of the gradient: a workgroup for each pick.  Sums are
-// fp32, in the order of the picks; a dot product's lanes meet in a fixed order.
+// workgroup, whose slots are then scalars; a lane has four rows in flight (eight in sums
+// of fp32 take 76 registers, 6315 tokens of 11 x 517 40 us against 36; in the gradient
+// of bf16 192, 4096 tokens of 8 x 6144 300 us for both calls against 283).  Few tokens of
+// the gradient: a workgroup for each pick.  Sums are fp32, in the order of the picks; a
+// dot product's lanes meet in a fixed order.
 //
 // Measured, averages, 8 rows a token, 6144 columns bf16: dispatch of 16384 tokens 333 us
-// (1.81 GB, 5.4 TB/s); collect of 4096 119 (503 MB, 4.2 TB/s), its gradient 162 (856 MB,
-// 5.3 TB/s); one token's collect 3.8 us, dispatch of 64 in E4M3 4.6.  8000 tokens of 8 x
-// 1502: sums 50 us (as of 1504: units end where the row ends), with their gradient 141 (135).
-// Rows that end inside lines cost dispatch most, 8 x 2056 73 us against 58 for 2048: the
-// line between two rows is written by two workgroups.
+// (1.81 GB, 5.4 TB/s); collect of 4096 99 (503 MB, 5.1 TB/s), its gradient 178 (856 MB,
+// 4.8 TB/s); one token's collect 4.0 us, dispatch of 64 in E4M3 4.6.  8000 tokens of 8 x
+// 1502: sums 45 us, with their gradient 142 (1504: 135).  Rows that end inside lines cost
+// dispatch most, 8 x 2056 73 us against 58 for 2048: the line between two rows is written
+// by two workgroups.
 #include <algorithm>
 
 #include "rows_device.h"
@@ -114,7 +115,7 @@ __device__ __forceinline__ void slots_of(const int32_t* inv, int64_t pick, int n
 
 template <int DT, bool LONG, bool TAIL>
 __global__ void __launch_bounds__(kBlock) collect_kernel(CollectArgs a, RowMap m) {
-  constexpr int N = 8;          // rows in flight
+  constexpr int N = 4;          // rows in flight
   int t, unit;
   locate<LONG>(m, t, unit);
   const Span<TAIL> p(unit, a.cols);
@@ -127,13 +128,13 @@ __global__ void __launch_bounds__(kBlock) collect_kernel(CollectArgs a, RowMap m
     Unit<DT> u[N];
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      if (slot[j] >= 0) load_unit<TAIL>(u[j], a.rows.p, DT, (int64_t)slot[j] * a.rows.ld + p.c, p.n);
+      if (slot[j] >= 0) load_unit<TAIL>(u[j], a.rows.p, kPlain<DT>, (int64_t)slot[j] * a.rows.ld + p.c, p.n);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       if (slot[j] < 0) continue;
       const float w = a.w ? a.w[pick + j] : 1.0f;
       float v[kUnit];
-      unit_floats(u[j], DT, v);
+      unit_floats(u[j], kPlain<DT>, v);
 #pragma unroll
       for (int l = 0; l < kUnit; ++l) y[l] = fmaf(w, v[l], y[l]);
     }
@@ -268,9 +269,19 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
 
 hipError_t launch_collect(const CollectArgs& a, hipStream_t s) {
   const bool tail = a.cols < kUnit || (a.y.p == a.add.p && a.cols % kUnit != 0);
+  // large bf16 rows past the caches, also those that end inside lines (read_once; 4096
+  // tokens of 8 x 6144: 92 us against 101, 8000 of 8 x 1502: 45 against 50).  The gradient
+  // reads them as the rest: 276 us for both calls either way.
+  const bool once = !tail && a.rows.dtype == MOE_DT_BF16 && (int64_t)a.T * a.K * a.cols * 2 >= kOnceBytes;
   return by_rows<true>(row_map((a.cols + kUnit - 1) / kUnit, false), a.T, tail,
-                 [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
+                       [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
     constexpr bool l = decltype(L)::value, t = decltype(T)::value;
+    if constexpr (!t) {
+      if (once) {
+        hipLaunchKernelGGL((collect_kernel<kBf16Once, l, t>), grid, block, 0, s, a, m);
+        return;
+      }
+    }
     if (a.rows.dtype == MOE_DT_F32) hipLaunchKernelGGL((collect_kernel<MOE_DT_F32, l, t>), grid, block, 0, s, a, m);
     else hipLaunchKernelGGL((collect_kernel<MOE_DT_BF16, l, t>), grid, block, 0, s, a, m);
   });

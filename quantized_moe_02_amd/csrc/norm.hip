@@ -18,9 +18,9 @@
 // in registers (rows of several to a workgroup meet in LDS); a second launch adds the
 // workgroups' parts in float64, in order.  No atomics, the same bits every time.
 //
-// Measured, averages: 16384 x 6144 bf16 with residual 135 us (805 MB, 6.0 TB/s), with
-// E4M3 rows beside 156 (906 MB, 5.8 TB/s); followed by its gradient 146 + 140, and 5 to
-// join 512 parts (1.61 GB in all, 5.5 TB/s).  1 x 6144 4 us, 64 x 6144 fp32 onto bf16 to
+// Measured, averages: 16384 x 6144 bf16 with residual 131 us (805 MB, 6.1 TB/s), with
+// E4M3 rows beside 155 (906 MB, 5.8 TB/s); followed by its gradient 131 + 144, and 5 to
+// join 512 parts (1.61 GB in all, 5.7 TB/s).  1 x 6144 4 us, 64 x 6144 fp32 onto bf16 to
 // MXFP4 5.5: the latency of one row.  1027 x 2057 fp32 7 us, its gradient 11.5 + 4: the
 // launches, and three rows one after the other.  24000 x 1503 bf16 58 us (5.0 TB/s).
 // 1627 x 8815 with fp32 dy 73 us for both against 42 at a copy's rate: one workgroup of
@@ -75,14 +75,14 @@ __device__ __forceinline__ void add_residual(const NormArgs& a, const Unit<XT>& 
     unit_floats(r, a.res.dtype, v);
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) h[i] += v[i];
-    round_to(RT == kAnyDtype ? a.res.dtype : RT, h);
+    round_to(RT == kAnyDtype ? a.res.dtype : kPlain<RT>, h);
   }
 }
 
 // h of a unit between the sum and its use: bf16 where it is that, else fp32.
 template <int DT>
 __device__ __forceinline__ void hold(Unit<DT>& u, const float (&h)[kUnit]) {
-  if constexpr (DT == MOE_DT_BF16) {
+  if constexpr (kIsBf16<DT>) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) u.w[i] = pack_bf16(h[2 * i], h[2 * i + 1]);
   } else {
@@ -233,7 +233,7 @@ __device__ __forceinline__ double product(const float (&dy)[kUnit], const float 
 // nothing of a row is stored before all of it is read.
 // Weights beside bf16 rows are bf16 too, but for any types.
 template <int DT>
-constexpr int weight_dtype() { return DT == MOE_DT_BF16 ? MOE_DT_BF16 : kAnyDtype; }
+constexpr int weight_dtype() { return kIsBf16<DT> ? MOE_DT_BF16 : kAnyDtype; }
 
 // DT is the type of h, dh and dx, YT that of dy.
 template <int DT, int YT, int G, int U, bool TAIL>
@@ -480,10 +480,15 @@ hipError_t launch_rmsnorm(const NormArgs& args, hipStream_t s) {
         constexpr int g = decltype(G)::value;
         e = by_runs(a.rows, block_of(g), block_of(g) / g, [&](int first, dim3 grid) {
           a.first = first;
-          by_dtypes(a.x.dtype, a.res.p ? a.res.dtype : a.x.dtype, [&](auto X, auto R) {
+          auto launch = [&](auto X, auto R) {
             hipLaunchKernelGGL((rmsnorm_kernel<decltype(X)::value, decltype(R)::value, g, decltype(U)::value, decltype(T)::value>),
                                grid, dim3(block_of(g)), 0, s, a);
-          });
+          };
+          if constexpr (!decltype(T)::value) {
+            using Once = std::integral_constant<int, kBf16Once>;
+            if (read_once(a.x, a.rows, a.cols) && read_once(a.res, a.rows, a.cols)) return launch(Once{}, Once{});
+          }
+          by_dtypes(a.x.dtype, a.res.p ? a.res.dtype : a.x.dtype, launch);
         });
       },
       [&] {
@@ -523,6 +528,11 @@ hipError_t launch_rmsnorm_grad(const NormGradArgs& args, hipStream_t s) {
                              grid(block_of(g) / g, g > 256 ? kGradBlocks / 2 : kGradBlocks), dim3(block_of(g)), 0, s, a);
         };
         const bool same = a.dx.dtype == a.h.dtype && (a.h.dtype == MOE_DT_F32 || a.w_dtype == MOE_DT_BF16);
+        if constexpr (!decltype(T)::value) {
+          using Once = std::integral_constant<int, kBf16Once>;
+          if (same && read_once(a.h, a.rows, a.cols) && read_once(a.dy, a.rows, a.cols) && read_once(a.dh, a.rows, a.cols))
+            return launch(Once{}, Once{});
+        }
         if (same) by_dtypes(a.h.dtype, a.dy.dtype, launch);
         else launch(std::integral_constant<int, kAnyDtype>{}, std::integral_constant<int, kAnyDtype>{});
       },

@@ -8,8 +8,14 @@
 namespace qmoe {
 
 constexpr int kUnit = 8;
-// dtype of a matrix known at compile time, or only at run time
+// dtype of a matrix known at compile time, or only at run time, or bf16 of a matrix that
+// is read once and whose lines go first when room is needed (read_once)
 constexpr int kAnyDtype = -1;
+constexpr int kBf16Once = 0x100 | MOE_DT_BF16;
+template <int DT>
+constexpr bool kIsBf16 = DT == MOE_DT_BF16 || DT == kBf16Once;
+template <int DT>
+constexpr int kPlain = kIsBf16<DT> ? (int)MOE_DT_BF16 : DT;
 
 // Where a lane's unit lies in its row.  A row's last values come with those before
 // them, as whole units that end where the row ends: `skip` of the eight are another
@@ -33,13 +39,13 @@ struct Span {
 
 template <int DT>
 struct Unit {
-  uint32_t w[DT == MOE_DT_BF16 ? 4 : 8];
+  uint32_t w[kIsBf16<DT> ? 4 : 8];
 };
 
 template <int DT>
 __device__ __forceinline__ bool is_bf16(int dtype) {
   if constexpr (DT == kAnyDtype) return dtype == MOE_DT_BF16;
-  return DT == MOE_DT_BF16;
+  return kIsBf16<DT>;
 }
 
 // The first n < 8 values of a row's last unit come and go as a run of four, one of
@@ -89,10 +95,15 @@ __device__ __forceinline__ void store_tail(uint8_t* p, const uint32_t (&w)[WORDS
 // (n <= 0: none is read).
 template <bool TAIL, int DT>
 __device__ __forceinline__ void load_unit(Unit<DT>& u, const void* base, int dtype, int64_t at, int n) {
-  constexpr int kWords = DT == MOE_DT_BF16 ? 4 : 8;
+  constexpr int kWords = kIsBf16<DT> ? 4 : 8;
 #pragma unroll
   for (int i = 0; i < kWords; ++i) u.w[i] = 0;
-  if (is_bf16<DT>(dtype)) {
+  if constexpr (DT == kBf16Once && !TAIL) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+    const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + at));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u.w[i] = v[i];
+  } else if (is_bf16<DT>(dtype)) {
     const uint8_t* p = static_cast<const uint8_t*>(base) + at * 2;
     uint32_t w[4] = {};
     if (!TAIL || n >= kUnit) __builtin_memcpy(w, p, 16);
@@ -114,7 +125,7 @@ __device__ __forceinline__ void unit_floats(const Unit<DT>& u, int dtype, float 
       v[2 * i] = bf16_lo(u.w[i]);
       v[2 * i + 1] = bf16_hi(u.w[i]);
     }
-  } else if constexpr (DT != MOE_DT_BF16) {
+  } else if constexpr (!kIsBf16<DT>) {
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) v[i] = __uint_as_float(u.w[i]);
   }
@@ -125,7 +136,7 @@ __device__ __forceinline__ void unit_floats(const Unit<DT>& u, int dtype, float 
 template <int DT>
 __device__ __forceinline__ void forget_values(Unit<DT>& u) {
 #pragma unroll
-  for (int i = 0; i < (DT == MOE_DT_BF16 ? 4 : 8); ++i) opaque(u.w[i]);
+  for (int i = 0; i < (kIsBf16<DT> ? 4 : 8); ++i) opaque(u.w[i]);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -352,9 +363,23 @@ __device__ __forceinline__ unsigned block_number(bool in_order) {
 // SwiGLU (32768 x 2048 and what quantises it: 99 us, 89).
 inline bool past_cache(int64_t bytes) { return bytes > (int64_t)256 << 20; }
 
-// Whether the rows of a matrix that is written end inside lines.
+// Whether the rows of a matrix end inside lines.
 inline bool ragged_lines(const void* p, int64_t pitch_bytes) {
   return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch_bytes) & 127) != 0;
+}
+
+// Whether the bf16 rows of a matrix are read with kBf16Once.  Inputs that the caches
+// cannot hold then leave them to what is written, for the next reader: SwiGLU of 32768 x
+// 2048 66 us against 69, right after gu was written 162 against 172 for both; norm of
+// 16384 x 6144 with its gradient, x written before, 344 against 372, of 8192 (96 MB each)
+// 174 against 200.  Under that the caches still hold what was written last, and it comes
+// slower so: norm of 4096 right after x 50 us against 47, SwiGLU of 8000 x 1024 11.6
+// against 10.4.  Rows that end inside lines are read in part by two workgroups (norm of
+// 24000 x 1503 60 us against 58), fp32 rows in two requests a line (SwiGLU and gradient
+// of 10000 x 2056 183 against 153).
+constexpr int64_t kOnceBytes = (int64_t)96 << 20;
+inline bool read_once(const RowMat& m, int64_t rows, int64_t cols) {
+  return !m.p || (m.dtype == MOE_DT_BF16 && rows * cols * 2 >= kOnceBytes && !ragged_lines(m.p, m.ld * 2));
 }
 
 constexpr int kMapBlock = 256;

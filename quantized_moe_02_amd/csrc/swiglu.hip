@@ -9,9 +9,9 @@
 // hardware's power of two with its argument rounded at its own size, so s is off by up
 // to (1.5 |g| + 12) 2^-24 of itself, and is 0 where e^-|g| lies below 2^-126.
 //
-// Measured, averages: 32768 x 2048 bf16 72 us, its gradient 114 (403 and 671 MB, 5.6 and
-// 5.9 TB/s); to E4M3 20000 x 2048 37 us (5.4 TB/s); 777 x 1001 fp32 4.0 and 5.0 us; 8 x
-// 2048 to E4M3 2.7 us.
+// Measured, averages: 32768 x 2048 bf16 64 us, its gradient 118 (403 and 671 MB, 6.3 and
+// 5.7 TB/s); to E4M3 20000 x 2048 34 us (6.0 TB/s); 777 x 1001 fp32 3.9 and 5.1 us; 8 x
+// 2048 to E4M3 3.0 us.
 #include <algorithm>
 
 #include "rows_device.h"
@@ -34,15 +34,15 @@ __device__ __forceinline__ int rows_that_count(const SwigluArgs& a) {
 
 template <bool TAIL, int DT>
 __device__ __forceinline__ void load_gate_up(const SwigluArgs& a, int64_t row, const Span<TAIL>& p, Unit<DT>& g, Unit<DT>& u) {
-  load_unit<TAIL>(g, a.gu.p, DT, row * a.gu.ld + p.c, p.n);
-  load_unit<TAIL>(u, a.gu.p, DT, row * a.gu.ld + a.cols + p.c, p.n);
+  load_unit<TAIL>(g, a.gu.p, kPlain<DT>, row * a.gu.ld + p.c, p.n);
+  load_unit<TAIL>(u, a.gu.p, kPlain<DT>, row * a.gu.ld + a.cols + p.c, p.n);
 }
 
 template <int DT>
 __device__ __forceinline__ void swiglu_unit(const Unit<DT>& gr, const Unit<DT>& ur, float (&v)[kUnit]) {
   float g[kUnit], up[kUnit];
-  unit_floats(gr, DT, g);
-  unit_floats(ur, DT, up);
+  unit_floats(gr, kPlain<DT>, g);
+  unit_floats(ur, kPlain<DT>, up);
 #pragma unroll
   for (int i = 0; i < kUnit; ++i) {
     float s, t;
@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(kMapBlock) swiglu_grad_kernel(SwigluArgs a, Ro
   load_gate_up(a, row, p, gr, ur);
   load_unit<TAIL>(dr, a.out.p, a.out.dtype, row * a.out.ld + p.c, p.n);
   float g[kUnit], up[kUnit], dh[kUnit];
-  unit_floats(gr, DT, g);
-  unit_floats(ur, DT, up);
+  unit_floats(gr, kPlain<DT>, g);
+  unit_floats(ur, kPlain<DT>, up);
   unit_floats(dr, a.out.dtype, dh);
 #pragma unroll
   for (int i = 0; i < kUnit; ++i) {
@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(kMapBlock) swiglu_grad_kernel(SwigluArgs a, Ro
     up[i] = d * g[i];
     g[i] = dg;
   }
-  store_unit<TAIL>(a.dgu.p, DT, row * a.dgu.ld + p.c, p.n, g);
-  store_unit<TAIL>(a.dgu.p, DT, row * a.dgu.ld + a.cols + p.c, p.n, up);
+  store_unit<TAIL>(a.dgu.p, kPlain<DT>, row * a.dgu.ld + p.c, p.n, g);
+  store_unit<TAIL>(a.dgu.p, kPlain<DT>, row * a.dgu.ld + a.cols + p.c, p.n, up);
 }
 
 template <int DT>
@@ -167,7 +167,9 @@ hipError_t launch_e4m3(SwigluArgs a, hipStream_t s) {
     });
   };
   auto at = [&](auto G, auto U) { return with(G, U, std::false_type{}); };
-  if (a.cols < kUnit) return with(integral_constant<int, 8>{}, integral_constant<int, 1>{}, std::true_type{});
+  if constexpr (DT != kBf16Once) {
+    if (a.cols < kUnit) return with(integral_constant<int, 8>{}, integral_constant<int, 1>{}, std::true_type{});
+  }
   if (units <= 8) return at(integral_constant<int, 8>{}, integral_constant<int, 1>{});
   if (units <= 16) return at(integral_constant<int, 16>{}, integral_constant<int, 1>{});
   if (units <= 32) return at(integral_constant<int, 32>{}, integral_constant<int, 1>{});
@@ -179,18 +181,26 @@ hipError_t launch_e4m3(SwigluArgs a, hipStream_t s) {
   if (units <= 2048) return at(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
   return by_runs(a.rows, 1024, 1, [&](int first, dim3 grid) {
     a.first = first;
-    hipLaunchKernelGGL((swiglu_e4m3_wide_kernel<DT>), grid, dim3(1024), 0, s, a);
+    hipLaunchKernelGGL((swiglu_e4m3_wide_kernel<kPlain<DT>>), grid, dim3(1024), 0, s, a);
   });
 }
 
 }  // namespace
 
 hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s) {
-  if (a.out.dtype == MOE_DT_E4M3) return a.gu.dtype == MOE_DT_F32 ? launch_e4m3<MOE_DT_F32>(a, s) : launch_e4m3<MOE_DT_BF16>(a, s);
+  const bool once = a.cols >= kUnit && read_once(a.gu, a.rows, (int64_t)2 * a.cols);
+  if (a.out.dtype == MOE_DT_E4M3)
+    return a.gu.dtype == MOE_DT_F32 ? launch_e4m3<MOE_DT_F32>(a, s) : once ? launch_e4m3<kBf16Once>(a, s) : launch_e4m3<MOE_DT_BF16>(a, s);
   const int nb = (a.cols + kMxBlock - 1) / kMxBlock;
   return by_rows<false>(row_map(nb * (kMxBlock / kUnit), a.out.dtype != MOE_DT_MXFP4 && ragged_lines(a.out.p, a.out.ld * element(a.out.dtype))), a.rows, a.cols < kUnit,
                  [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
     constexpr bool l = decltype(L)::value, t = decltype(T)::value;
+    if constexpr (!t) {
+      if (once) {
+        hipLaunchKernelGGL((swiglu_kernel<kBf16Once, l, t>), grid, block, 0, s, a, m);
+        return;
+      }
+    }
     if (a.gu.dtype == MOE_DT_F32) hipLaunchKernelGGL((swiglu_kernel<MOE_DT_F32, l, t>), grid, block, 0, s, a, m);
     else hipLaunchKernelGGL((swiglu_kernel<MOE_DT_BF16, l, t>), grid, block, 0, s, a, m);
   });
@@ -198,9 +208,16 @@ hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s) {
 
 hipError_t launch_swiglu_grad(const SwigluArgs& a, hipStream_t s) {
   const bool tail = a.cols < kUnit || (a.dgu.p == a.gu.p && a.cols % kUnit != 0);
+  const bool once = !tail && a.dgu.p != a.gu.p && read_once(a.gu, a.rows, (int64_t)2 * a.cols);
   return by_rows<true>(row_map((a.cols + kUnit - 1) / kUnit, ragged_lines(a.dgu.p, a.dgu.ld * element(a.dgu.dtype))), a.rows, tail,
                  [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {
     constexpr bool l = decltype(L)::value, t = decltype(T)::value;
+    if constexpr (!t) {
+      if (once) {
+        hipLaunchKernelGGL((swiglu_grad_kernel<kBf16Once, l, t>), grid, block, 0, s, a, m);
+        return;
+      }
+    }
     if (a.gu.dtype == MOE_DT_F32) hipLaunchKernelGGL((swiglu_grad_kernel<MOE_DT_F32, l, t>), grid, block, 0, s, a, m);
     else hipLaunchKernelGGL((swiglu_grad_kernel<MOE_DT_BF16, l, t>), grid, block, 0, s, a, m);
   });

@@ -56,6 +56,61 @@ def test_norm_of_each_shape_and_type(cols, xt, rt):
     close(dx, want[0], 8 * U * want[2], xt)
 
 
+@pytest.mark.parametrize("cols", [64, 192, 320, 960, 1984, 4032, 8128, 16320, 32704, 40000])
+def test_large_inputs_give_the_bits_of_small_ones(cols):
+    """Large bf16 inputs are read past the caches; no value of a row depends on it."""
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    rows = (100 << 20) // (2 * cols) // 32 * 32
+    step = rows // 4
+    x, r = (torch.randn(rows, cols, generator=gen, device="cuda").to(BF) for _ in range(2))
+    w = (1 + 0.3 * torch.randn(cols, generator=gen, device="cuda")).to(BF)
+
+    def quarters(call, *mats):
+        """The outputs of one call, and of four calls over quarters of the rows."""
+        one, four = ([torch.zeros_like(m) for m in mats] for _ in range(2))
+        call(slice(0, rows), *one)
+        for i in range(0, rows, step):
+            call(slice(i, i + step), *(m[i:i + step] for m in four))
+        for a, b in zip(one, four):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+    quarters(lambda at, y, h: q.moe_rmsnorm(x[at], w, EPS, y=y, residual=r[at], h=h), x, x)
+    quarters(lambda at, c, s: q.moe_rmsnorm(x[at], w, EPS, q=c, q_scale=s),
+           torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(rows, device="cuda"))
+    quarters(lambda at, dx: q.moe_rmsnorm_grad(r[at], x[at], w, EPS, dx, dh=r[at]), x)
+    dw, part = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    dx, total, size = torch.empty_like(x), torch.zeros(cols, device="cuda", dtype=torch.float64), torch.zeros(cols, device="cuda", dtype=torch.float64)
+    q.moe_rmsnorm_grad(r, x, w, EPS, dx, dweight=dw)
+    for i in range(0, rows, step):
+        q.moe_rmsnorm_grad(r[i:i + step], x[i:i + step], w, EPS, dx[i:i + step], dweight=part)
+        total += part
+        n = x[i:i + step].double() / (x[i:i + step].double().square().mean(1, keepdim=True) + EPS).sqrt()
+        size += (r[i:i + step].double() * n).abs().sum(0)
+    # at most (rows of a part + 8) roundings either way
+    assert ((dw.double() - total).abs() <= 2 * (-(-rows // 256) + 8) * U * size + 1e-30).all()
+    if cols % 128 == 0:
+        half = cols // 2
+        quarters(lambda at, o: q.moe_swiglu(x[at], o), r[:, :half].contiguous())
+        quarters(lambda at, c, s: q.moe_swiglu(x[at], c, s),
+               torch.empty(rows, half, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(rows, device="cuda"))
+        quarters(lambda at, d: q.moe_swiglu_grad(x[at], r[at, :half], d), x)
+    else:
+        quarters(lambda at, o: q.moe_swiglu(torch.cat([x[at], r[at]], 1), o), x)
+    K = 4
+    T = rows // K
+    inv = torch.randperm(rows, generator=gen, device="cuda").reshape(T, K).to(torch.int32)
+    weights = torch.rand(T, K, generator=gen, device="cuda")
+    one, four, dws, dws4 = torch.empty(T, cols, dtype=BF, device="cuda"), torch.empty(T, cols, dtype=BF, device="cuda"), torch.empty_like(weights), torch.empty_like(weights)
+    d, d4 = torch.empty_like(x), torch.empty_like(x)
+    q.moe_collect(x, inv, one, weights)
+    q.moe_collect_grad(r[:T], inv, d, weights, rows=x, dweights=dws)
+    for i in range(0, T, T // 4):
+        at = slice(i, i + T // 4)
+        q.moe_collect(x, inv[at], four[at], weights[at])
+        q.moe_collect_grad(r[at], inv[at], d4, weights[at], rows=x, dweights=dws4[at])
+    assert torch.equal(one, four) and torch.equal(d, d4) and torch.equal(dws, dws4)
+
+
 # ---- many tokens: a workgroup takes a token's picks, not one of them -----------------------
 @pytest.mark.parametrize("T,K,cols", [(16400, 3, 30), (8200, 5, 100), (2100, 9, 300), (2050, 16, 513), (600, 6, 2050), (520, 16, 1600),
                                       (16400, 2, 5), (2100, 4, 200)])

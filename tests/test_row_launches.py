@@ -202,6 +202,59 @@ def test_norm_grad_launches(record, rows, cols):
         assert [l.kernel for l in ls] == ["fill_zero"] and ls[0].blocks * ls[0].threads >= cols
 
 
+ONCE = 0x100 | BF16                                  # bf16 rows that are read past the caches
+LARGE = 96 << 20
+
+
+@pytest.mark.parametrize("cols", [8, 32, 64, 65, 128, 256, 257, 500, 512, 1024, 1536, 2048, 4096, 6144, 8192, 8200, 16384, 32768, 65536])
+def test_large_rows_are_read_past_the_caches(record, cols):
+    """bf16 inputs of 96 MiB and more, in rows of whole 128-byte lines and not written
+    by the same call: those kernels and no others, at both sides of the limit."""
+    ld = -(-cols // 64) * 64
+    for odd in (0, 1):                               # rows that end inside lines
+        pitch = ld + odd
+        for under in (0, 1):
+            rows = min(-(-LARGE // (2 * cols)) - under, MAX_R)
+            once = not odd and 2 * rows * cols >= LARGE
+            wide = cols > 32768
+            c = q.MoeRmsnormConfig(rows, cols, BF16, BF16, BF16, BF16, 0, 1e-6, pitch, pitch, pitch, pitch)
+            for res in (F, None):
+                assert record.lib.moe_rmsnorm(ctypes.byref(c), F, res, F, F if res else None, F, None, None, None) == q.MOE_OK
+                for l in record.take():
+                    assert wide or cols < 8 or (l.args[0] == ONCE) == once == (l.args[1] == ONCE)
+            c = q.MoeRmsnormGradConfig(rows, cols, BF16, BF16, BF16, BF16, 1e-6, pitch, pitch, pitch, pitch)
+            for dh in (F, None):
+                assert record.lib.moe_rmsnorm_grad(ctypes.byref(c), F, F, F, dh, F, None, None, 0, None) == q.MOE_OK
+                (l,) = record.take()
+                assert cols > 16384 or (l.args[0] == ONCE) == once
+            for K in (1, 16):
+                T = min(-(-LARGE // (2 * cols * K)) - under, MAX_T)
+                large = 2 * T * K * cols >= LARGE
+                for alias in (False, True):
+                    c = q.MoeRowsConfig(T, cols, K, T * K, BF16, BF16, BF16, pitch, pitch, pitch)
+                    y = F + (1 << 39)
+                    assert record.lib.moe_collect(ctypes.byref(c), F, F, F, y if alias else None, y, None) == q.MOE_OK
+                    for l in record.take():          # at any pitch
+                        assert (l.args[0] == ONCE) == (large and (not alias or cols % 8 == 0))
+                    assert record.lib.moe_collect_grad(ctypes.byref(c), F, F, F, F, F if alias else y, F, None) == q.MOE_OK
+                    (l,) = record.take()
+                    assert l.args[0] == BF16         # the gradient reads them as others
+            rows = -(-LARGE // (4 * cols)) - under
+            once = not under and not odd
+            pitch = -(-2 * cols // 64) * 64 + odd
+            c = q.MoeSwigluConfig(rows, cols, 1, BF16, BF16, pitch, cols)
+            for ot in (BF16, MX, E4):
+                c.out_dtype = ot
+                assert record.lib.moe_swiglu(ctypes.byref(c), F, None, F, F if ot != BF16 else None, None) == q.MOE_OK
+                for l in record.take():
+                    assert not l.args or len(l.args) == 1 or (l.args[0] == ONCE) == once
+            c.out_dtype = BF16
+            for alias in (False, True):
+                assert record.lib.moe_swiglu_grad(ctypes.byref(c), F, F, None, F if alias else 2 * F, None) == q.MOE_OK
+                for l in record.take():
+                    assert (l.args[0] == ONCE) == (once and not alias)
+
+
 def test_every_kernel_is_reached(record):
     """After the calls above (this test runs last in its file)."""
     every = {record.lib.registered_name(i).decode() for i in range(record.lib.registered())}
