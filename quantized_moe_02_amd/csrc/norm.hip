@@ -23,7 +23,7 @@
 // join 512 parts (1.61 GB in all, 5.7 TB/s).  1 x 6144 4 us, 64 x 6144 fp32 onto bf16 to
 // MXFP4 5.5: the latency of one row.  1027 x 2057 fp32 7 us, its gradient 11.5 + 4: the
 // launches, and three rows one after the other.  24000 x 1503 bf16 58 us (5.0 TB/s).
-// 1627 x 8815 with fp32 dy 73 us for both against 42 at a copy's rate: one workgroup of
+// 1627 x 8815 with fp32 dy 64 us for both against 42 at a copy's rate: one workgroup of
 // 512 per CU, its registers full, waits for each row.
 #include <algorithm>
 
@@ -433,7 +433,10 @@ __global__ void __launch_bounds__(256) fill_zero_kernel(float* p, int n) {
 constexpr int kGradBlocks = 512;
 
 // Calls f(lanes, units, tail) as integral constants for rows of up to MOST columns,
-// g() for longer ones.
+// g() for longer ones.  Lanes that a row fills to two thirds and more, fewer of them with
+// more units before more with fewer (bf16 norm of 4000 x 9000 64 us with 512 of three
+// against 81 with 1024 of two, 2000 x 14000 49 with 512 of four against 54, 2000 x 20000
+// 77 with 1024 of three against 87 with four).
 template <int MOST, class F, class H>
 void by_shape(int cols, F&& f, H&& g) {
   using std::integral_constant;
@@ -452,9 +455,12 @@ void by_shape(int cols, F&& f, H&& g) {
   else if (units <= 512) at(integral_constant<int, 256>{}, integral_constant<int, 2>{});
   else if (units <= 768) at(integral_constant<int, 256>{}, integral_constant<int, 3>{});
   else if (units <= 1024) at(integral_constant<int, 256>{}, integral_constant<int, 4>{});
-  else if constexpr (MOST <= 16384) at(integral_constant<int, 512>{}, integral_constant<int, 4>{});
-  else if (units <= 2048) at(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
-  else at(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+  else if (units <= 1536) at(integral_constant<int, 512>{}, integral_constant<int, 3>{});
+  else if (units <= 2048) at(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+  else if constexpr (MOST > 16384) {
+    if (units <= 3 * 1024) at(integral_constant<int, 1024>{}, integral_constant<int, 3>{});
+    else at(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+  }
 }
 
 // Calls f of two dtypes as integral constants.
@@ -523,8 +529,13 @@ hipError_t launch_rmsnorm_grad(const NormGradArgs& args, hipStream_t s) {
       a.cols,
       [&](auto G, auto U, auto T) {
         auto launch = [&](auto D, auto Y) {
-          constexpr int g = decltype(G)::value;
-          hipLaunchKernelGGL((rmsnorm_grad_kernel<decltype(D)::value, decltype(Y)::value, g, decltype(U)::value, decltype(T)::value>),
+          // bf16 rows of up to 2048 columns by a wave each, without barriers (norm and
+          // gradient of 20000 x 2000 129 us against 144); fp32 rows take too many registers
+          // for that (8000 x 1600 88 us against 82), and the norm alone has more of them in
+          // flight by workgroups (20000 x 2000 60 us against 64)
+          constexpr bool wave = kIsBf16<decltype(D)::value> && decltype(G)::value == 256 && decltype(U)::value == 1;
+          constexpr int g = wave ? kWave : decltype(G)::value, u = wave ? 4 : decltype(U)::value;
+          hipLaunchKernelGGL((rmsnorm_grad_kernel<decltype(D)::value, decltype(Y)::value, g, u, decltype(T)::value>),
                              grid(block_of(g) / g, g > 256 ? kGradBlocks / 2 : kGradBlocks), dim3(block_of(g)), 0, s, a);
         };
         const bool same = a.dx.dtype == a.h.dtype && (a.h.dtype == MOE_DT_F32 || a.w_dtype == MOE_DT_BF16);

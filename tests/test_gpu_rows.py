@@ -372,7 +372,7 @@ def test_collect_grad(T, K, cols, E, rt, yt, weighted, drop, pad):
 
 
 # ---- SwiGLU ----------------------------------------------------------------------------
-SW = [(1, 1), (3, 7), (8, 2048), (5, 256), (33, 1001), (2, 65536), (6, 8200), (100, 40), (257, 33), (9, 4096), (7, 4104)]
+SW = [(1, 1), (3, 7), (8, 2048), (5, 256), (33, 1001), (2, 65536), (6, 8200), (100, 40), (257, 33), (9, 4096), (7, 4104), (6, 1300), (3, 5001), (2, 9001), (2, 14001)]
 
 
 @pytest.mark.parametrize("rows,cols", SW)

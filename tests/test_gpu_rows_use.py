@@ -29,7 +29,7 @@ def _gen(seed):
 
 
 # ---- every norm kernel with every pair of types ---------------------------------------
-NARROW = [5, 24, 60, 100, 250, 500, 1000, 1500, 2040, 3100, 6100, 8100, 8201, 16385, 32800]
+NARROW = [5, 24, 60, 100, 250, 500, 1000, 1500, 2040, 3100, 6100, 8100, 8201, 12300, 16385, 24600, 32800]
 
 
 @pytest.mark.parametrize("cols", NARROW)

@@ -131,7 +131,7 @@ def _swiglu(rec, rows, cols, gt=BF16, ot=BF16, grad=False, alias=False):
     return rec.take()
 
 
-E4_SIZES = [(4, c) for c in (1, 8, 64, 128, 256, 512, 1024, 2048, 4096, 8192, 16384, 16385)] + [(MAX_R, 65536), (MAX_R, 16384)]
+E4_SIZES = [(4, c) for c in (1, 8, 64, 128, 256, 512, 1024, 1536, 2048, 4096, 6144, 8192, 12288, 16384, 16385)] + [(MAX_R, 65536), (MAX_R, 16384)]
 
 
 @pytest.mark.parametrize("rows,cols", SIZES + [(MAX_R, 1), (MAX_R, 200), (MAX_R, 65536)])
@@ -157,7 +157,7 @@ def test_swiglu_e4m3_launches(record, rows, cols, gt):
     assert 0 <= at - rows < per
 
 
-NORM = [(4, c) for c in (1, 8, 33, 65, 129, 257, 513, 1025, 1537, 2049, 4097, 6145, 8193, 16385, 32769)] + [
+NORM = [(4, c) for c in (1, 8, 33, 65, 129, 257, 513, 1025, 1537, 2049, 4097, 6145, 8193, 12289, 16385, 24577, 32769)] + [
     (MAX_R, c) for c in (1, 512, 6144, 16384, 32768, 65536)]
 
 
@@ -206,7 +206,7 @@ ONCE = 0x100 | BF16                                  # bf16 rows that are read p
 LARGE = 96 << 20
 
 
-@pytest.mark.parametrize("cols", [8, 32, 64, 65, 128, 256, 257, 500, 512, 1024, 1536, 2048, 4096, 6144, 8192, 8200, 16384, 32768, 65536])
+@pytest.mark.parametrize("cols", [8, 32, 64, 65, 128, 256, 257, 500, 512, 1024, 1536, 2048, 4096, 6144, 8192, 8200, 16384, 24576, 32768, 65536])
 def test_large_rows_are_read_past_the_caches(record, cols):
     """bf16 inputs of 96 MiB and more, in rows of whole 128-byte lines and not written
     by the same call: those kernels and no others, at both sides of the limit."""
