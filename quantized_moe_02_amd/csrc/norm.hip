@@ -23,7 +23,7 @@
 // join 512 parts (1.61 GB in all, 5.7 TB/s).  1 x 6144 4 us, 64 x 6144 fp32 onto bf16 to
 // MXFP4 5.5: the latency of one row.  1027 x 2057 fp32 7 us, its gradient 11.5 + 4: the
 // launches, and three rows one after the other.  24000 x 1503 bf16 58 us (5.0 TB/s).
-// 1627 x 8815 with fp32 dy 64 us for both against 42 at a copy's rate: one workgroup of
+// 1627 x 8815 with fp32 dy 65 us for both against 42 at a copy's rate: one workgroup of
 // 512 per CU, its registers full, waits for each row.
 #include <algorithm>
 
