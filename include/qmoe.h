@@ -709,7 +709,9 @@ moe_status moe_collect_grad(const moe_rows_config* cfg, const void* dy, const vo
  *   out[r][j] = silu(gu[r][j]) * gu[r][cols + j],  silu(g) = g / (1 + e^-g).
  * Rows from expert_offsets[n_experts] on belong to no expert: they are not read,
  * and what belongs to them is left as it is.  An infinite gate gives what the
- * formula gives: itself for +inf, NaN for -inf (and NaN in the gate's gradient). */
+ * formula gives: itself for +inf, NaN for -inf (and NaN in the gate's gradient).
+ * s = 1 / (1 + e^-g) is within 6 * 2^-24 of itself, 1 - s within 7 * 2^-24, at any
+ * gate; an s below 2^-126 (gates under -87.3) counts as 0. */
 typedef struct {
   int32_t rows, cols;   /* rows <= 16 * MOE_MAX_TOKENS, else MOE_ERR_UNSUPPORTED */
   int32_t n_experts;    /* places of expert_offsets' last entry; >= 1 */

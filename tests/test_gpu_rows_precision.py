@@ -1,0 +1,62 @@
+"""How exactly the row operators hold what they compute in fp32, against float64:
+bounds that count the roundings of each form, whatever the size of the inputs."""
+import numpy as np
+import pytest
+import torch
+
+import quantized_moe_02_amd as q
+from oracle import rows as ref
+from row_cases import BF, F, U, close, f64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    q.lib()
+
+
+# ---- SwiGLU ------------------------------------------------------------------------
+# s = 1 / (1 + x), x = e^-g: the hardware's power of two 2, the product by 1 - c 1 (c holds
+# what its argument's rounding lost); 1 + x 1; the hardware's reciprocal 2.  1 - s = x s: x's
+# share, the others and the product.
+S_BOUND, REST_BOUND = 6 * U, 7 * U
+
+
+def _gates(lo, hi, t, rows=64, cols=520):
+    gen = torch.Generator().manual_seed(int(10 * lo))
+    g = (torch.rand(rows, cols, generator=gen) * (hi - lo) + lo).to(t)
+    g[::2] *= -1
+    up, dh = torch.randn(rows, cols, generator=gen).to(t), torch.randn(rows, cols, generator=gen)
+    return torch.cat([g, up], 1).cuda(), dh.cuda()
+
+
+@pytest.mark.parametrize("lo,hi", [(0, 1), (1, 4), (4, 10), (10, 20), (20, 50), (50, 87), (87, 95)])
+@pytest.mark.parametrize("t", [F, BF])
+def test_swiglu_at_every_gate(lo, hi, t):
+    """As exact for gates far from 0 as for those near it."""
+    gu, dh = _gates(lo, hi, t)
+    out, dgu = torch.empty_like(dh), torch.empty_like(gu)
+    q.moe_swiglu(gu, out)
+    g, up = np.split(f64(gu), 2, axis=1)
+    lost = 2.0 ** -126                            # an s below that counts as 0
+    want = ref.swiglu(f64(gu))
+    close(out, want, (S_BOUND + 2 * U) * np.abs(want) + lost * np.abs(g * up), F)
+    q.moe_swiglu_grad(gu, dh, dgu)
+    want, mag = ref.swiglu_grad(f64(gu), f64(dh))
+    d = np.abs(f64(dh))
+    # dgate: s, rest in the slope, the slope's sum and three products; dup: s and two products
+    rel = np.concatenate([np.full(g.shape, S_BOUND + REST_BOUND + 4 * U), np.full(g.shape, S_BOUND + 2 * U)], 1)
+    close(dgu, want, rel * mag + lost * np.concatenate([d * np.abs(up) * (1 + np.abs(g)), d * np.abs(g)], 1), t)
+
+
+def test_codes_are_those_of_the_exact_values():
+    """E4M3 and MXFP4 rows of bf16 gates are made of the same fp32 values."""
+    gu, _ = _gates(0, 20, BF, cols=512)
+    y, mx, codes = torch.empty(64, 512, device="cuda"), q.mxfp4_empty(64, 512), q.mxfp4_empty(64, 512)
+    q.moe_swiglu(gu, y)
+    q.moe_swiglu(gu, mx[0], out_scale=mx[1])
+    q.moe_mxfp4_quantize(y, *codes)
+    assert torch.equal(mx[0], codes[0]) and torch.equal(mx[1], codes[1])
