@@ -634,8 +634,9 @@ moe_status moe_rmsnorm(const moe_rmsnorm_config* cfg, const void* x, const void*
  *   g = dy * w,  dx = dh + m * (g - h * m^2 * mean(g * h)),  dweight = sum over
  * rows of dy * h * m.  dx is the gradient of x and of the residual alike; dh is
  * the gradient that reaches h on the residual's own way.  The sums over a row are
- * float64; dweight's are fp32 over the rows that one workgroup takes and float64
- * over the workgroups.  Fields as in moe_rmsnorm_config. */
+ * float64; dweight's are fp32 over eight rows at most and float64 over these, with
+ * one rounding to fp32 for each of up to 512 parts of the rows.  Fields as in
+ * moe_rmsnorm_config. */
 typedef struct {
   int32_t rows, cols;
   int32_t h_dtype, weight_dtype, dy_dtype;

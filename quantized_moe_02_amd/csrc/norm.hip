@@ -14,9 +14,10 @@
 // additions do not show beside the bytes.  m, the products and y are fp32, each result
 // rounded once.
 //
-// dw: a workgroup of the gradient takes rows in turn and holds the sums of its columns
-// in registers (rows of several to a workgroup meet in LDS); a second launch adds the
-// workgroups' parts in float64, in order.  No atomics, the same bits every time.
+// dw: a workgroup of the gradient takes rows in turn and sums its columns in registers, in
+// fp32 over eight rows; runs of eight are added in float64, in LDS (rows past 16384 columns:
+// in the workgroup's own part in memory).  A second launch adds the workgroups' sums in
+// float64, in order.  No atomics, the same bits every time.
 //
 // Measured, averages: 16384 x 6144 bf16 with residual 131 us (805 MB, 6.1 TB/s), with
 // E4M3 rows beside 155 (906 MB, 5.8 TB/s); followed by its gradient 131 + 144, and 5 to
@@ -229,17 +230,24 @@ __device__ __forceinline__ double product(const float (&dy)[kUnit], const float 
   return sum;
 }
 
-// Workgroups take rows in turn and hold dw's sums over theirs.  As in the norm,
-// nothing of a row is stored before all of it is read.
 // Weights beside bf16 rows are bf16 too, but for any types.
 template <int DT>
 constexpr int weight_dtype() { return kIsBf16<DT> ? MOE_DT_BF16 : kAnyDtype; }
 
-// DT is the type of h, dh and dx, YT that of dy.
+// Rows whose share of dw is summed in fp32 before it is added to the float64 sums: about as
+// exact as float64 alone (16384 x 6144 bf16 dw off by 7.1e-8 of its norm, 4.9e-8 by the final
+// rounding, 1.1e-7 with all 32 rows of a workgroup in fp32) at an eighth of its LDS traffic
+// (with fp32 sums alone: 20000 x 2000 129.5 us against 127.7, 16384 x 6144 282 both).
+constexpr int kDwRun = 8;
+
+// Workgroups take rows in turn and hold dw's sums over theirs, each lane its own in LDS.
+// As in the norm, nothing of a row is stored before all of it is read.  DT is the type of h,
+// dh and dx, YT that of dy.
 template <int DT, int YT, int G, int U, bool TAIL>
 __global__ void __launch_bounds__(block_of(G)) rmsnorm_grad_kernel(NormGradArgs a) {
   constexpr int kBlock = block_of(G), kRows = kBlock / G;
   __shared__ double lds[2][2][kBlock / kWave];
+  __shared__ double sums[U][kUnit][kBlock + (kRows > 1 ? 8 : 0)];     // a row's columns in banks of their own
   const int lane = threadIdx.x % G;
   int64_t row = (int64_t)blockIdx.x * kRows;
   if constexpr (G < kWave) row += threadIdx.x / G;
@@ -251,7 +259,9 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_grad_kernel(NormGradArgs 
     const Span<TAIL> p(u * G + lane, a.cols);
     load_unit<TAIL>(wr[u], a.w, a.w_dtype, p.c, p.n);
   }
-  int turn = 0;
+  auto total = [&](int u, int i, bool first) { return (first ? 0.0 : sums[u][i][threadIdx.x]) + acc[u][i]; };
+  int turn = 0, run = 0;
+  bool first = true;           // no run of rows is in the sums yet
   for (; row < a.rows; row += (int64_t)gridDim.x * kRows, turn ^= 1) {
     Unit<DT> hr[U], dr[U];
     Unit<YT> yr[U];
@@ -262,6 +272,20 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_grad_kernel(NormGradArgs 
       load_unit<TAIL>(yr[u], a.dy.p, a.dy.dtype, row * a.dy.ld + p.c, p.n);
       if (a.dh.p) load_unit<TAIL>(dr[u], a.dh.p, a.dh.dtype, row * a.dh.ld + p.c, p.n);
     }
+    // while the row is on its way
+    if (a.dw && run == kDwRun) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+          sums[u][i][threadIdx.x] = total(u, i, first);
+          acc[u][i] = 0.0f;
+        }
+      }
+      first = false;
+      run = 0;
+    }
+    ++run;
     RowSums s{0, 0};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -302,82 +326,125 @@ __global__ void __launch_bounds__(block_of(G)) rmsnorm_grad_kernel(NormGradArgs 
     }
   }
   if (!a.dw) return;
-  float* part = gridDim.x == 1 ? a.dw : a.part + (int64_t)blockIdx.x * a.cols;
+  float* part = gridDim.x == 1 ? a.dw : static_cast<float*>(a.part) + (int64_t)blockIdx.x * a.cols;
   if constexpr (kRows > 1) {       // the sums of the workgroup's rows, in order
-    __shared__ float all[kRows][G * U * kUnit];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const Span<TAIL> p(u * G + lane, a.cols);
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i)
-        if (p.n > 0) all[threadIdx.x / G][p.c + i] = acc[u][i];
+      for (int i = 0; i < kUnit; ++i) sums[u][i][threadIdx.x] = total(u, i, first);
     }
     __syncthreads();
     for (int c = threadIdx.x; c < a.cols; c += kBlock) {
-      float v = all[0][c];
+      const int unit = c / kUnit, i = c - Span<TAIL>(unit, a.cols).c;
+      double v = 0;
 #pragma unroll 8
-      for (int i = 1; i < kRows; ++i) v += all[i][c];
-      part[c] = v;
+      for (int r = 0; r < kRows; ++r) v += sums[unit / G][i][r * G + unit % G];
+      part[c] = (float)v;
     }
   } else {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const Span<TAIL> p(u * G + lane, a.cols);
-      if (p.n > 0) store_unit<TAIL>(part, MOE_DT_F32, p.c, p.n, acc[u]);
+      float v[kUnit];
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) v[i] = (float)total(u, i, first);
+      if (p.n > 0) store_unit<TAIL>(part, MOE_DT_F32, p.c, p.n, v);
     }
   }
 }
 
-// Longer rows: read twice, dweight's sums in the workgroup's own part.
+// Longer rows: read twice, kWideTurns of them for each reading and writing of dweight's
+// sums, which lie in the workgroup's own part: as float64, but where it takes no more rows
+// than that (T float), whose sums are written once.
+constexpr int kWideTurns = 4;
+template <class T>
 __global__ void __launch_bounds__(kWide) rmsnorm_grad_wide_kernel(NormGradArgs a) {
+  constexpr int kTurns = kWideTurns;
   __shared__ double lds[2][2][kWide / kWave];
-  float* part = gridDim.x == 1 ? a.dw : a.part + (int64_t)blockIdx.x * a.cols;
-  const int64_t first = blockIdx.x;
-  int turn = 0;
-  for (int64_t row = first; row < a.rows; row += gridDim.x, turn ^= 1) {
-    auto read = [&](int c, float (&h)[kUnit], float (&dy)[kUnit], float (&w)[kUnit]) {
-      Unit<kAnyDtype> v;
-      const int n = a.cols - c;
-      load_unit<true>(v, a.h.p, a.h.dtype, row * a.h.ld + c, n);
-      unit_floats(v, a.h.dtype, h);
-      load_unit<true>(v, a.dy.p, a.dy.dtype, row * a.dy.ld + c, n);
-      unit_floats(v, a.dy.dtype, dy);
-      load_unit<true>(v, a.w, a.w_dtype, c, n);
-      unit_floats(v, a.w_dtype, w);
-    };
-    RowSums s{0, 0};
-    float h[kUnit], dy[kUnit], w[kUnit];
-    for (int c = threadIdx.x * kUnit; c < a.cols; c += kWide * kUnit) {
-      read(c, h, dy, w);
-      s.squares += squares(h, 0);
-      s.product += product(dy, w, h, 0);
+  __shared__ float factors[kTurns][2];          // m and k of the rows in turn
+  T* part = gridDim.x == 1 ? reinterpret_cast<T*>(a.dw) : static_cast<T*>(a.part) + (int64_t)blockIdx.x * a.cols;   // one: T float
+  auto read = [&](int64_t row, int c, float (&h)[kUnit], float (&dy)[kUnit]) {
+    Unit<kAnyDtype> v;
+    const int n = a.cols - c;
+    load_unit<true>(v, a.h.p, a.h.dtype, row * a.h.ld + c, n);
+    unit_floats(v, a.h.dtype, h);
+    load_unit<true>(v, a.dy.p, a.dy.dtype, row * a.dy.ld + c, n);
+    unit_floats(v, a.dy.dtype, dy);
+  };
+  auto weight = [&](int c, float (&w)[kUnit]) {
+    Unit<kAnyDtype> v;
+    load_unit<true>(v, a.w, a.w_dtype, c, a.cols - c);
+    unit_floats(v, a.w_dtype, w);
+  };
+  // hides that rows ascend, else an address of each matrix for each loop over them is kept
+  auto row_of = [](int row) {
+    uint32_t r = row;
+    opaque(r);
+    return (int64_t)r;
+  };
+  const int step = gridDim.x;
+  float h[kUnit], dy[kUnit], w[kUnit];
+  for (int first = blockIdx.x; first < a.rows; first += kTurns * step) {
+    const int turns = min(kTurns, (a.rows - first + step - 1) / step);
+#pragma unroll 1
+    for (int t = 0; t < turns; ++t) {
+      const int64_t row = row_of(first + t * step);
+      RowSums s{0, 0};
+      for (int c = threadIdx.x * kUnit; c < a.cols; c += kWide * kUnit) {
+        read(row, c, h, dy);
+        weight(c, w);
+        s.squares += squares(h, 0);
+        s.product += product(dy, w, h, 0);
+      }
+      s.squares = group_sum<kWide>(s.squares, lds[t % 2][0]);
+      s.product = group_sum<kWide>(s.product, lds[t % 2][1]);
+      if (threadIdx.x == 0) row_factors(s, a.cols, a.eps, factors[t][0], factors[t][1]);
     }
-    s.squares = group_sum<kWide>(s.squares, lds[turn][0]);
-    s.product = group_sum<kWide>(s.product, lds[turn][1]);
-    float m, k;
-    row_factors(s, a.cols, a.eps, m, k);
+    __syncthreads();
     for (int c = threadIdx.x * kUnit; c < a.cols; c += kWide * kUnit) {
       const int n = a.cols - c;
-      read(c, h, dy, w);
-      float v[kUnit];
-      if (a.dw) {
-        Unit<MOE_DT_F32> u;
-        if (row != first) load_unit<true>(u, part, MOE_DT_F32, c, n);
-        unit_floats(u, MOE_DT_F32, v);
+      weight(c, w);
+      double sum[kUnit] = {};
+      if (sizeof(T) == 8 && a.dw && first != blockIdx.x) {
+        if (n >= kUnit) {
+          __builtin_memcpy(sum, part + c, sizeof(sum));
+        } else {
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) v[i] = (row != first ? v[i] : 0.0f) + dy[i] * (h[i] * m);
-        store_unit<true>(part, MOE_DT_F32, c, n, v);
+          for (int i = 0; i < kUnit - 1; ++i)
+            if (i < n) sum[i] = part[c + i];
+        }
       }
+#pragma unroll 1
+      for (int t = 0; t < turns; ++t) {
+        const int64_t row = row_of(first + t * step);
+        const float m = factors[t][0], k = factors[t][1];
+        read(row, c, h, dy);
+        float v[kUnit];
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) v[i] = m * (dy[i] * w[i] - h[i] * k);
-      if (a.dh.p) {
-        Unit<kAnyDtype> u;
-        load_unit<true>(u, a.dh.p, a.dh.dtype, row * a.dh.ld + c, n);
-        unit_floats(u, a.dh.dtype, h);
+        for (int i = 0; i < kUnit; ++i) {
+          v[i] = m * (dy[i] * w[i] - h[i] * k);
+          sum[i] += dy[i] * (h[i] * m);
+        }
+        if (a.dh.p) {
+          Unit<kAnyDtype> u;
+          load_unit<true>(u, a.dh.p, a.dh.dtype, row * a.dh.ld + c, n);
+          unit_floats(u, a.dh.dtype, h);
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) v[i] += h[i];
+          for (int i = 0; i < kUnit; ++i) v[i] += h[i];
+        }
+        store_unit<true>(a.dx.p, a.dx.dtype, row * a.dx.ld + c, n, v);
       }
-      store_unit<true>(a.dx.p, a.dx.dtype, row * a.dx.ld + c, n, v);
+      if (!a.dw) continue;
+      T v[kUnit];
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) v[i] = (T)sum[i];
+      if (n >= kUnit) {
+        __builtin_memcpy(part + c, v, sizeof(v));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kUnit - 1; ++i)
+          if (i < n) part[c + i] = v[i];
+      }
     }
   }
 }
@@ -385,7 +452,8 @@ __global__ void __launch_bounds__(kWide) rmsnorm_grad_wide_kernel(NormGradArgs a
 // dw[c] = sum of the workgroups' parts: 32 columns a workgroup, eight lanes to a part,
 // the shares of the parts joined in order.
 constexpr int kDwCols = 32;
-__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* part, int parts, int cols, float* dw) {
+template <class T>
+__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const T* part, int parts, int cols, float* dw) {
   constexpr int kShares = 1024 / 8, kGroups = 1024 / kDwCols;
   __shared__ double lds[kShares][kDwCols];
   const int lane = threadIdx.x % 8, share = threadIdx.x / 8;
@@ -393,10 +461,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* part, int
   double v[4] = {};
 #pragma unroll 8
   for (int p = share; p < parts; p += kShares) {
-    float x[4] = {};
-    const float* at = part + (int64_t)p * cols + c;
+    T x[4] = {};
+    const T* at = part + (int64_t)p * cols + c;
     if (c + 4 <= cols) {
-      __builtin_memcpy(x, at, 16);
+      __builtin_memcpy(x, at, sizeof(x));
     } else {
 #pragma unroll
       for (int i = 0; i < 3; ++i)
@@ -506,7 +574,10 @@ hipError_t launch_rmsnorm(const NormArgs& args, hipStream_t s) {
   return e;
 }
 
-int norm_grad_most_blocks(int rows) { return std::min(std::max(rows, 1), kGradBlocks); }
+size_t norm_grad_part_bytes(int rows, int cols) {
+  const size_t most = cols > kNormGradCols ? kGradBlocks / 2 * sizeof(double) : kGradBlocks * sizeof(float);
+  return std::min(std::max(rows, 1) * (cols > kNormGradCols ? sizeof(double) : sizeof(float)), most) * cols;
+}
 
 hipError_t launch_rmsnorm_grad(const NormGradArgs& args, hipStream_t s) {
   NormGradArgs a = args;
@@ -517,6 +588,7 @@ hipError_t launch_rmsnorm_grad(const NormGradArgs& args, hipStream_t s) {
   }
   // workgroups of `per` rows at a time, each as many times as the others
   int blocks = 0;
+  bool deep = false;           // parts in float64
   auto grid = [&](int per, int most) {
     const int steps = (a.rows + per - 1) / per;
     int turns = (steps + most - 1) / most;
@@ -525,7 +597,7 @@ hipError_t launch_rmsnorm_grad(const NormGradArgs& args, hipStream_t s) {
     if (a.dw && steps <= (a.cols <= 64 * kUnit ? 8 : 4)) turns = steps;
     return dim3(blocks = (steps + turns - 1) / turns);
   };
-  by_shape<16384>(
+  by_shape<kNormGradCols>(
       a.cols,
       [&](auto G, auto U, auto T) {
         auto launch = [&](auto D, auto Y) {
@@ -548,10 +620,18 @@ hipError_t launch_rmsnorm_grad(const NormGradArgs& args, hipStream_t s) {
         else launch(std::integral_constant<int, kAnyDtype>{}, std::integral_constant<int, kAnyDtype>{});
       },
       [&] {
-        hipLaunchKernelGGL(rmsnorm_grad_wide_kernel, grid(1, kGradBlocks / 2), dim3(kWide), 0, s, a);
+        const dim3 wide = grid(1, kGradBlocks / 2);
+        deep = a.rows > kWideTurns * blocks;
+        if (deep) hipLaunchKernelGGL(rmsnorm_grad_wide_kernel<double>, wide, dim3(kWide), 0, s, a);
+        else hipLaunchKernelGGL(rmsnorm_grad_wide_kernel<float>, wide, dim3(kWide), 0, s, a);
       });
-  if (a.dw && blocks > 1)
-    hipLaunchKernelGGL(rmsnorm_dw_kernel, dim3((a.cols + kDwCols - 1) / kDwCols), dim3(1024), 0, s, a.part, blocks, a.cols, a.dw);
+  if (!a.dw || blocks == 1) return hipGetLastError();
+  auto join = [&](auto* part) {
+    hipLaunchKernelGGL((rmsnorm_dw_kernel<std::remove_pointer_t<decltype(part)>>), dim3((a.cols + kDwCols - 1) / kDwCols), dim3(1024), 0,
+                       s, part, blocks, a.cols, a.dw);
+  };
+  if (deep) join(static_cast<double*>(a.part));
+  else join(static_cast<float*>(a.part));
   return hipGetLastError();
 }
 

@@ -51,7 +51,7 @@ int scale_bytes(int dtype, int cols) {
 
 // Ascends in both sizes, and is not 0 for no rows.
 size_t norm_workspace(int rows, int cols) {
-  return ((size_t)norm_grad_most_blocks(rows) * cols * sizeof(float) + kAlign - 1) / kAlign * kAlign;
+  return (norm_grad_part_bytes(rows, cols) + kAlign - 1) / kAlign * kAlign;
 }
 
 moe_status check_rows(const moe_rows_config* c) {
@@ -147,7 +147,7 @@ moe_status moe_rmsnorm_grad(const moe_rmsnorm_grad_config* cfg, const void* dy, 
   a.w = weight;
   a.w_dtype = c.weight_dtype;
   a.dw = dweight;
-  a.part = static_cast<float*>(ws);
+  a.part = ws;
   a.rows = c.rows;
   a.cols = c.cols;
   a.eps = c.eps;

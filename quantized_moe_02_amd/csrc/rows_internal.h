@@ -40,14 +40,15 @@ struct NormGradArgs {
   const void* w;
   int w_dtype;
   float* dw;               // nullable
-  float* part;             // [workgroups][cols]: the workgroups' sums for dw
+  void* part;              // [workgroups][cols]: the workgroups' sums for dw (norm_grad_part_bytes)
   int rows, cols;
   float eps;
   bool past_cache;         // as above
 };
-// The most workgroups, a row of `part` each, that the gradient of no more rows
-// takes, whatever its columns.
-int norm_grad_most_blocks(int rows);
+// Columns up to which the gradient holds a row in registers; past it parts may be float64.
+constexpr int kNormGradCols = 16384;
+// Bytes of `part` that are enough for the gradient of no more rows and columns.
+size_t norm_grad_part_bytes(int rows, int cols);
 hipError_t launch_rmsnorm_grad(const NormGradArgs& a, hipStream_t s);
 
 struct DispatchArgs {

@@ -60,3 +60,35 @@ def test_codes_are_those_of_the_exact_values():
     q.moe_swiglu(gu, mx[0], out_scale=mx[1])
     q.moe_mxfp4_quantize(y, *codes)
     assert torch.equal(mx[0], codes[0]) and torch.equal(mx[1], codes[1])
+
+
+# ---- the norm's weight gradient ------------------------------------------------------
+# A term dy h m: m, h m and the product. Eight terms added in fp32: 7 roundings. A workgroup's
+# sum 1; everything else is float64, the result's own rounding is close()'s.
+DW_BOUND = (3 + 7 + 1) * U
+
+
+@pytest.mark.parametrize("rows,cols", [(64 * 32768 + 5, 24), (64 * 2048 + 1, 500), (64 * 2048, 1100), (64 * 2048 + 3, 2000), (64 * 512 + 1, 2056),
+                                       (64 * 512, 5003), (64 * 256 + 2, 9000), (64 * 256, 16380), (64 * 256 + 1, 16392)])
+@pytest.mark.parametrize("t,wt", [(BF, BF), (BF, F), (F, F)])
+def test_norm_weight_gradient_of_long_batches(rows, cols, t, wt):
+    """A few large terms in front of many that vanish beside them one by one: 64
+    and more rows a workgroup, the large ones first in each."""
+    if t is F and rows * cols > 150 << 20:
+        rows //= 2
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols)
+    rand = lambda *s: torch.rand(*s, generator=gen, device="cuda")
+    h = (0.5 + rand(rows, cols)).to(t)
+    dy = (0.5 + rand(rows, cols)).mul_(2.0 ** -25)
+    dy[:-(-rows // 64)] *= 2.0 ** 25
+    dy = dy.to(t)
+    w = (0.5 + rand(cols)).to(wt)
+    dx, dw = torch.empty_like(h), torch.empty(cols, device="cuda")
+    q.moe_rmsnorm_grad(dy, h, w, 1e-5, dx, dweight=dw, ws=q.rmsnorm_workspace(rows, cols))
+    want = torch.zeros(cols, dtype=torch.float64, device="cuda")
+    eps = float(np.float32(1e-5))
+    for i in range(0, rows, 4096):
+        hh = h[i:i + 4096].double()
+        want += (dy[i:i + 4096].double() * hh * (hh.square().mean(1, keepdim=True) + eps).rsqrt()).sum(0)
+    want = f64(want)
+    close(dw, want, DW_BOUND * want, F, "dweight")          # every term is positive
