@@ -568,12 +568,18 @@ def _packer(config):
     code = {ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_int64: "q"}
     s = struct.Struct("@" + "".join(code[t] for _, t in config._fields_))
     assert s.size == ctypes.sizeof(config)
+    floats = [i for i, (_, t) in enumerate(config._fields_) if t is ctypes.c_float]
 
     def pack(*values):
         try:
             return s.pack(*values)
-        except (struct.error, OverflowError):      # sizes past 32 bits
-            raise QmoeError(MOE_ERR_UNSUPPORTED, config.__name__) from None
+        except (struct.error, OverflowError):
+            pass
+        try:                                       # no number, or one past fp32
+            struct.pack("f" * len(floats), *(values[i] for i in floats))
+        except (struct.error, OverflowError):
+            raise QmoeError(MOE_ERR_INVALID_ARG, config.__name__) from None
+        raise QmoeError(MOE_ERR_UNSUPPORTED, config.__name__)      # sizes past 32 bits
     return pack
 
 
