@@ -658,8 +658,12 @@ def moe_rmsnorm(x, weight, eps, y=None, residual=None, h=None, q=None, q_scale=N
 
 
 def moe_rmsnorm_workspace_size(rows: int, cols: int) -> int:
+    where = "moe_rmsnorm_workspace_size"
+    if max(rows, cols) >= 1 << 31:           # ctypes would cut them to 32 bits
+        raise QmoeError(MOE_ERR_UNSUPPORTED, where)
+    _require(min(rows, cols) >= 0, where)
     n = ctypes.c_size_t(0)
-    _check(lib().moe_rmsnorm_workspace_size(rows, cols, ctypes.byref(n)), "moe_rmsnorm_workspace_size")
+    _check(lib().moe_rmsnorm_workspace_size(rows, cols, ctypes.byref(n)), where)
     return n.value
 
 

@@ -38,3 +38,10 @@ def test_sizes_past_32_bits():
                  lambda: q.moe_swiglu(far(rows, 2), far(rows, 1)),
                  lambda: q.moe_collect(far(rows, 1), On.of(torch.zeros(1, 1, dtype=torch.int32)), far(1, 1))):
         assert _status(call) == q.MOE_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("rows,cols,status", [((1 << 32) + 4, 64, "UNSUPPORTED"), (4, (1 << 32) + 64, "UNSUPPORTED"), (1 << 31, 64, "UNSUPPORTED"),
+                                              (4 - (1 << 32), 64, "INVALID_ARG"), (4, 64 - (1 << 32), "INVALID_ARG")])
+def test_a_workspace_of_sizes_past_32_bits(rows, cols, status):
+    for size in (q.moe_rmsnorm_workspace_size, q.rmsnorm_workspace):
+        assert _status(lambda: size(rows, cols)) == getattr(q, "MOE_ERR_" + status)
