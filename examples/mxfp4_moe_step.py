@@ -65,7 +65,7 @@ class Mxfp4MoE:
             q.moe_mxfp4_matmul(x, *self.gate_up, gu, expert_offsets=offs, row_index=tok)
         h = torch.empty(T * k, I, dtype=torch.bfloat16, device=dev)
         q.moe_swiglu(gu, h, expert_offsets=offs)
-        out = torch.empty(T * k, H, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(T * k, H, device=dev)
         q.moe_mxfp4_matmul(h, *self.down, out, expert_offsets=offs)
         y = torch.empty(T, H, device=dev)
         inv = inv.view(T, k)
@@ -88,8 +88,9 @@ class Mxfp4MoE:
         x, ids, tw, offs, tok, inv, gu, out, logits, counts, n_tok, seq = self.saved
         g, T, dev = self.geom, x.shape[0], x.device
         H, I, k = g["hidden"], g["moe_inter"], g["top_k"]
-        d_out, d_tw = torch.empty_like(out), torch.empty_like(tw)
-        q.moe_collect_grad(dy, inv, drows=d_out, weights=tw, rows=out, dweights=d_tw)
+        d_out, d_tw = torch.empty(T * k, H, dtype=torch.bfloat16, device=dev), torch.empty_like(tw)
+        q.moe_collect_grad(dy, inv, drows=d_out, weights=tw)
+        q.moe_collect_grad(dy, inv, rows=out, dweights=d_tw)
         dh = torch.empty(T * k, I, device=dev)
         q.moe_mxfp4_matmul_dx(d_out, *self.down, dh, expert_offsets=offs)
         d_gu = torch.empty_like(gu)

@@ -1,0 +1,41 @@
+"""The MXFP4 step's use of the row operators: what it holds between them, and the
+gradients that it takes."""
+import os
+import sys
+
+import pytest
+import torch
+
+import quantized_moe_02_amd as q
+import synth
+from oracle import rows as ref
+from row_cases import BF, F, U, close, f64
+
+pytestmark = pytest.mark.gpu
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    q.lib()
+
+
+def _layer(T):
+    import mxfp4_moe_step as ex
+    layer = ex.make_layer(synth.WORKLOADS["tiny"]["geom"], seed=T, score_coef=0.5)
+    return layer, torch.randn(T, layer.geom["hidden"], generator=torch.Generator().manual_seed(T)).to(BF).cuda()
+
+
+@pytest.mark.parametrize("T", [1, 9, 70])
+def test_the_experts_rows_reach_their_sum_in_fp32(T):
+    layer, x = _layer(T)
+    y, _, _ = layer.forward(x)
+    _, _, tw, offs, _, inv, gu = layer.saved[:7]
+    k, I = tw.shape[1], layer.geom["moe_inter"]
+    h, rows = torch.empty(T * k, I, dtype=BF, device="cuda"), torch.empty(T * k, x.shape[1], device="cuda")
+    q.moe_swiglu(gu, h, expert_offsets=offs)
+    q.moe_mxfp4_matmul(h, *layer.down, rows, expert_offsets=offs)
+    want, mag = ref.collect(f64(rows), inv.cpu().numpy(), f64(tw))
+    close(y, want, (k + 2) * U * mag, F)                   # the products and sums of k rows
