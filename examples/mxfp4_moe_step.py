@@ -88,9 +88,8 @@ class Mxfp4MoE:
         x, ids, tw, offs, tok, inv, gu, out, logits, counts, n_tok, seq = self.saved
         g, T, dev = self.geom, x.shape[0], x.device
         H, I, k = g["hidden"], g["moe_inter"], g["top_k"]
-        d_out, d_tw = torch.empty(T * k, H, dtype=torch.bfloat16, device=dev), torch.empty_like(tw)
+        d_out = torch.empty(T * k, H, dtype=torch.bfloat16, device=dev)
         q.moe_collect_grad(dy, inv, drows=d_out, weights=tw)
-        q.moe_collect_grad(dy, inv, rows=out, dweights=d_tw)
         dh = torch.empty(T * k, I, device=dev)
         q.moe_mxfp4_matmul_dx(d_out, *self.down, dh, expert_offsets=offs)
         d_gu = torch.empty_like(gu)
@@ -103,7 +102,8 @@ class Mxfp4MoE:
         q.moe_balance_loss_grad(logits, ids, counts, n_tok, dlogits, coef=self.coef, seq_offsets=seq)
         if through_router:
             # weights rsf s_i / sum s over a token's picks, s = sigmoid(logits)
-            at = ids.long()
+            d_tw, at = torch.empty_like(tw), ids.long()
+            q.moe_collect_grad(dy, inv, rows=out, dweights=d_tw)
             s = torch.sigmoid(logits.gather(1, at))
             ds = (g["routed_scaling_factor"] * d_tw - (d_tw * tw).sum(1, keepdim=True)) / s.sum(1, keepdim=True)
             dlogits.scatter_add_(1, at, ds * s * (1 - s))

@@ -39,3 +39,14 @@ def test_the_experts_rows_reach_their_sum_in_fp32(T):
     q.moe_mxfp4_matmul(h, *layer.down, rows, expert_offsets=offs)
     want, mag = ref.collect(f64(rows), inv.cpu().numpy(), f64(tw))
     close(y, want, (k + 2) * U * mag, F)                   # the products and sums of k rows
+
+
+@pytest.mark.parametrize("through_router", [False, True])
+def test_the_weights_gradient_is_taken_where_it_is_asked_for(through_router, monkeypatch):
+    """It reads every expert's row again."""
+    layer, x = _layer(9)
+    y, _, _ = layer.forward(x)
+    asked, call = [], q.moe_collect_grad
+    monkeypatch.setattr(q, "moe_collect_grad", lambda *a, **k: (asked.append(k.get("dweights") is not None), call(*a, **k))[1])
+    layer.backward(torch.ones_like(y), through_router=through_router)
+    assert any(asked) == through_router
