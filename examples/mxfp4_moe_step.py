@@ -81,13 +81,14 @@ class Mxfp4MoE:
         return y, loss, counts
 
     def backward(self, dy, through_router=False):
-        """dy fp32 [T][H] -> (gradient of x through the experts, fp32 [T][H];
+        """dy fp32 [T][H], in any layout -> (gradient of x through the experts, fp32 [T][H];
         gradient of the router weights from the balance loss, [E][H]).  With
         through_router both hold all of it: the routing weights' share and, in x, the
         way through the router."""
         x, ids, tw, offs, tok, inv, gu, out, logits, counts, n_tok, seq = self.saved
         g, T, dev = self.geom, x.shape[0], x.device
         H, I, k = g["hidden"], g["moe_inter"], g["top_k"]
+        dy = dy.float().contiguous()                             # one broadcast over rows or columns, too
         d_out = torch.empty(T * k, H, dtype=torch.bfloat16, device=dev)
         q.moe_collect_grad(dy, inv, drows=d_out, weights=tw)
         dh = torch.empty(T * k, I, device=dev)

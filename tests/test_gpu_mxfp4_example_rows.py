@@ -50,3 +50,18 @@ def test_the_weights_gradient_is_taken_where_it_is_asked_for(through_router, mon
     monkeypatch.setattr(q, "moe_collect_grad", lambda *a, **k: (asked.append(k.get("dweights") is not None), call(*a, **k))[1])
     layer.backward(torch.ones_like(y), through_router=through_router)
     assert any(asked) == through_router
+
+
+@pytest.mark.parametrize("layout", ["broadcast over tokens", "broadcast over columns", "transposed", "float64"])
+def test_a_gradient_in_any_layout(layout):
+    T = 9
+    layer, x = _layer(T)
+    y, _, _ = layer.forward(x)
+    gen = torch.Generator().manual_seed(1)
+    n = lambda *s: torch.randn(*s, generator=gen).cuda()
+    H = y.shape[1]
+    dy = {"broadcast over tokens": lambda: n(1, H).expand(T, H), "broadcast over columns": lambda: n(T, 1).expand(T, H),
+          "transposed": lambda: n(H, T).t(), "float64": lambda: n(T, H).double()}[layout]()
+    plain = torch.empty(T, H, device="cuda").copy_(dy)
+    for got, want in zip(layer.backward(dy), layer.backward(plain)):
+        assert torch.equal(got, want)
