@@ -92,3 +92,26 @@ def test_norm_weight_gradient_of_long_batches(rows, cols, t, wt):
         want += (dy[i:i + 4096].double() * hh * (hh.square().mean(1, keepdim=True) + eps).rsqrt()).sum(0)
     want = f64(want)
     close(dw, want, DW_BOUND * want, F, "dweight")          # every term is positive
+
+
+@pytest.mark.parametrize("rows,cols", [(1025, 40), (5000, 17), (4099, 512), (6150, 700), (6500, 1300), (2500, 1537), (6161, 2000), (4200, 2048),
+                                       (2049, 2056), (1100, 5003), (1100, 8000), (800, 8200), (700, 14000), (1300, 16400)])
+@pytest.mark.parametrize("types", [(BF, BF, BF), (BF, BF, F), (F, F, F), (BF, F, BF)])
+def test_norm_gradient_of_many_rows(rows, cols, types):
+    """Several workgroups of several rows each, joined: every shape, bf16 rows beside
+    bf16 weights, dy in fp32, all in fp32, and types without a kernel of their own."""
+    ht, wt, yt = types
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    h, dy, dh, w = n(rows, cols).to(ht), (0.1 * n(rows, cols)).to(yt), (0.1 * n(rows, cols)).to(ht), (1 + 0.3 * n(cols)).to(wt)
+    dx, dw = torch.empty_like(h), torch.empty(cols, device="cuda")
+    q.moe_rmsnorm_grad(dy, h, w, 1e-5, dx, dh=dh, dweight=dw, ws=q.rmsnorm_workspace(rows, cols))
+    H, D, W = h.double(), dy.double(), w.double()
+    m = (H.square().mean(1, keepdim=True) + float(np.float32(1e-5))).rsqrt()
+    g, k = D * W, m * m
+    want = dh.double() + m * (g - H * (k * (g * H).mean(1, keepdim=True)))
+    mag = dh.double().abs() + m * (g.abs() + H.abs() * (k * (g * H).abs().mean(1, keepdim=True)))
+    # g, its product with h, m, k, h k, the difference, its product with m, dh's addition
+    close(dx, f64(want), 8 * U * f64(mag), ht, "dx")
+    t = D * H * m
+    close(dw, f64(t.sum(0)), DW_BOUND * f64(t.abs().sum(0)), F, "dweight")
