@@ -596,8 +596,9 @@ moe_status moe_balance_loss_grad(const moe_balance_config* cfg, const void* logi
  * largest 448) and one fp32 scale a row, value = code * scale:
  *   codes  uint8 [rows][cols] without gaps, 8-byte aligned; scale float32 [rows]
  * A row is brought to it with scale = max(amax / 448, 2^-126), amax its largest
- * magnitude, each code the nearest E4M3 value of x / scale (ties to even).  A
- * row that holds an infinity or a NaN gets scale NaN and codes 0.
+ * magnitude, each code the nearest E4M3 value of x / scale (ties to even), x and
+ * scale as fp32 has them.  A row that holds an infinity or a NaN gets scale NaN and
+ * codes 0.
  *
  * Root-mean-square norm with the residual's addition.  Per row of cols values:
  *   h = x + residual            (rounded to h's type; without a residual h = x)
@@ -621,7 +622,7 @@ typedef struct {
  *   residual  [rows][cols], or NULL
  *   weight    [cols]
  *   h         [rows][cols] out, NULL if not wanted or without a residual; may be
- *             `residual` itself (at the same stride), or x where the types agree
+ *             `residual` or x itself (same type and stride)
  *   y         [rows][cols] out, or NULL
  *   q, q_scale  out, or both NULL: y before its rounding, in q_dtype (E4M3 rows,
  *             or MXFP4 as moe_mxfp4_quantize makes them, codes 16-byte aligned)

@@ -14,8 +14,8 @@
 // dot product's lanes meet in a fixed order.
 //
 // Measured, averages, 8 rows a token, 6144 columns bf16: dispatch of 16384 tokens 333 us
-// (1.81 GB, 5.4 TB/s); collect of 4096 99 (503 MB, 5.1 TB/s), its gradient 178 (856 MB,
-// 4.8 TB/s); one token's collect 4.0 us, dispatch of 64 in E4M3 4.6.  8000 tokens of 8 x
+// (1.81 GB, 5.4 TB/s); collect of 4096 103 (503 MB, 4.9 TB/s), its gradient 184 (856 MB,
+// 4.7 TB/s); one token's collect 4.0 us, dispatch of 64 in E4M3 4.6.  8000 tokens of 8 x
 // 1502: sums 45 us, with their gradient 142 (1504: 135).  Rows that end inside lines cost
 // dispatch most, 8 x 2056 73 us against 58 for 2048: the line between two rows is written
 // by two workgroups.
@@ -269,9 +269,13 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
 
 hipError_t launch_collect(const CollectArgs& a, hipStream_t s) {
   const bool tail = a.cols < kUnit || (a.y.p == a.add.p && a.cols % kUnit != 0);
-  // large bf16 rows past the caches, also those that end inside lines (read_once; 4096
-  // tokens of 8 x 6144: 92 us against 101, 8000 of 8 x 1502: 45 against 50).  The gradient
-  // reads them as the rest: 276 us for both calls either way.
+  // large bf16 rows past the caches, also those that end inside lines (read_once; the same
+  // rows again and again, 4096 tokens of 8 x 6144: 81 us against 92, 8000 of 8 x 1502: 45
+  // against 50).  Right after the product that writes them, both in all: 2048 x 8 x 6144 120
+  // against 124, 8000 x 8 x 2048 153 against 165, 1100 x 8 x 6144 the same, 4096 x 8 x 6144
+  // 711 - 718 against 707; after a copy 223 against 239.  Rows of 200 MB that nothing wrote
+  // or read in between are slower so (41 against 34).  The gradient reads them as the rest:
+  // 276 us for both calls either way.
   const bool once = !tail && a.rows.dtype == MOE_DT_BF16 && (int64_t)a.T * a.K * a.cols * 2 >= kOnceBytes;
   return by_rows<true>(row_map((a.cols + kUnit - 1) / kUnit, false), a.T, tail,
                        [&](auto L, auto T, dim3 grid, dim3 block, const RowMap& m) {

@@ -19,13 +19,14 @@
 // in the workgroup's own part in memory).  A second launch adds the workgroups' sums in
 // float64, in order.  No atomics, the same bits every time.
 //
-// Measured, averages: 16384 x 6144 bf16 with residual 131 us (805 MB, 6.1 TB/s), with
-// E4M3 rows beside 155 (906 MB, 5.8 TB/s); followed by its gradient 131 + 144, and 5 to
-// join 512 parts (1.61 GB in all, 5.7 TB/s).  1 x 6144 4 us, 64 x 6144 fp32 onto bf16 to
+// Measured, averages: 16384 x 6144 bf16 with residual 133 us (805 MB, 6.1 TB/s), with
+// E4M3 rows beside 155 (906 MB, 5.8 TB/s); followed by its gradient 133 + 147, and 5 to
+// join 512 parts (1.61 GB in all, 5.7 TB/s).  1 x 6144 3.8 us, 64 x 6144 fp32 onto bf16 to
 // MXFP4 5.5: the latency of one row.  1027 x 2057 fp32 7 us, its gradient 11.5 + 4: the
 // launches, and three rows one after the other.  24000 x 1503 bf16 58 us (5.0 TB/s).
 // 1627 x 8815 with fp32 dy 65 us for both against 42 at a copy's rate: one workgroup of
-// 512 per CU, its registers full, waits for each row.
+// 512 a CU (a second would have to do with 128 registers and 80 KB of LDS) waits for each
+// row.
 #include <algorithm>
 
 #include "rows_device.h"
@@ -92,8 +93,9 @@ __device__ __forceinline__ void hold(Unit<DT>& u, const float (&h)[kUnit]) {
   }
 }
 
-// RT is h's type, with or without a residual.  Nothing is stored before the whole row is read: h may be the residual itself, and
-// the last lanes of a row read values of the ones before them.
+// RT is h's type, with or without a residual.  Nothing is stored before the whole row is
+// read: h may be the residual itself, and the last lanes of a row read values of the ones
+// before them.
 template <int XT, int RT, int G, int U, bool TAIL>
 __global__ void __launch_bounds__(block_of(G)) rmsnorm_kernel(NormArgs a) {
   constexpr int kRows = block_of(G) / G;
@@ -504,7 +506,8 @@ constexpr int kGradBlocks = 512;
 // g() for longer ones.  Lanes that a row fills to two thirds and more, fewer of them with
 // more units before more with fewer (bf16 norm of 4000 x 9000 64 us with 512 of three
 // against 81 with 1024 of two, 2000 x 14000 49 with 512 of four against 54, 2000 x 20000
-// 77 with 1024 of three against 87 with four).
+// 77 with 1024 of three against 87 with four).  1024 lanes have 128 registers each, of which
+// four units of fp32 rows are three short (12 bytes of scratch a lane).
 template <int MOST, class F, class H>
 void by_shape(int cols, F&& f, H&& g) {
   using std::integral_constant;

@@ -8,9 +8,9 @@
 // lanes.  s is off by up to 6 2^-24 of itself at any g, 1 - s by 7 (sigmoids), and s is 0
 // where it lies below 2^-126.
 //
-// Measured, averages: 32768 x 2048 bf16 64 us, its gradient 118 (403 and 671 MB, 6.3 and
-// 5.7 TB/s); to E4M3 20000 x 2048 34 us (6.0 TB/s); 777 x 1001 fp32 3.9 and 5.1 us; 8 x
-// 2048 to E4M3 3.0 us.
+// Measured, averages: 32768 x 2048 bf16 66 us, its gradient 122 (403 and 671 MB, 6.1 and
+// 5.5 TB/s); to E4M3 20000 x 2048 34.5 us (5.9 TB/s); 777 x 1001 fp32 4.0 and 5.0 us; 8 x
+// 2048 to E4M3 2.8 us.
 #include <algorithm>
 
 #include "rows_device.h"
